@@ -20,6 +20,9 @@
  * the FFN in stages (moelb_grouped_ffn_stages) and expert weights packed once
  * for the FFN's weight streams (moelb_pack_weights).
  *
+ * For training: the FFN's forward that keeps its projections and its gradients
+ * (moelb_grouped_ffn_train, moelb_grouped_ffn_backward).
+ *
  * Conventions for every entry point:
  *  - Plain C ABI.  Every pointer argument is DEVICE memory owned by the caller
  *    (e.g. a PyTorch tensor's data pointer), unless stated otherwise; the
@@ -441,6 +444,55 @@ int moelb_grouped_ffn_stages(int stages, const void* x, int rows_x, int rows,
  * MOELB_EINVAL before any launch.
  */
 int moelb_pack_weights(const void* w, int E, int rows, int K, int dtype, void* packed, void* stream);
+
+/*
+ * Training form of the grouped FFN: moelb_grouped_ffn's result, and its
+ * gradients.  Groups, rows, gather, rank and the clamping of device offsets
+ * are moelb_grouped_ffn's; one group (num_groups = E = 1, group_off = {0, T})
+ * is a dense gated block.  For row q of expert e with x_q its source row:
+ *   [g, u] = W13[e] x_q, a = SiLU(g) u, y[q] = W2[e] a              (train)
+ *   s = 1 / (1 + exp(-g)), da = W2[e]^T dy[q],
+ *   dz = [dg, du] = [da u s (1 + g (1 - s)), da g s]
+ *   dx[q] = W13[e]^T dz, dw13[e] = sum_q dz x_q^T, dw2[e] = sum_q dy[q] a^T
+ *                                                                (backward)
+ * with fp32 accumulation; y, dx and the weight gradients are rounded to dtype
+ * once, and so are a and dz as operands of the products that read them; z
+ * stays fp32.  dx[q] is the gradient of row q: with `gather`, a token's
+ * gradient is the sum over its rows (moelb_combine with unit weights).
+ * Results do not depend on the order of execution: the same call gives the
+ * same bits.
+ *  x          [rows_x,d]   dtype
+ *  w13        [E,2*inter,d], w2 [E,d,inter]  dtype, row-major
+ *  z          [rows,2*inter] fp32: the projections [g, u], kept from the
+ *             forward for the backward, in the call's expert-major row order
+ *             (group_off, gather, rank, E and rows of both calls the same)
+ *  y          [rows,d]  dtype out (train); dy [rows,d] dtype (backward): rows
+ *             outside every computed group are neither written nor read
+ *  dx         [rows,d]  dtype out or NULL: rows outside every computed group
+ *             are not written
+ *  dw13, dw2  as w13, w2, out or NULL: overwritten; zero for an expert without
+ *             rows
+ *  ws         train: moelb_grouped_ffn_workspace_bytes(...) bytes; backward:
+ *             moelb_grouped_ffn_backward_workspace_bytes(...) bytes; no state
+ *             is kept in it between the calls.
+ * Requires what moelb_grouped_ffn requires, and rows*d, rows_x*d,
+ * rows*2*inter and 2*inter*d elements each below 2^32 - 65536 bytes.
+ * All row data, weights, z and ws 16-byte aligned.  Outputs must not overlap
+ * the inputs or each other.
+ */
+int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, const int32_t* group_off,
+                            int num_groups, int E, int G, int rank,
+                            const int32_t* gather, int gather_k,
+                            int d, int inter, int dtype, const void* w13, const void* w2,
+                            void* ws, size_t ws_bytes, float* z, void* y, void* stream);
+size_t moelb_grouped_ffn_backward_workspace_bytes(int rows, int num_groups, int E, int d,
+                                                  int inter, int dtype);
+int moelb_grouped_ffn_backward(const void* dy, const void* x, int rows_x, int rows,
+                               const int32_t* group_off, int num_groups, int E, int G, int rank,
+                               const int32_t* gather, int gather_k, int d, int inter, int dtype,
+                               const void* w13, const void* w2, const float* z,
+                               void* ws, size_t ws_bytes, void* dx, void* dw13, void* dw2,
+                               void* stream);
 
 /*
  * Top-k weighted combine (FreeBalance section 2.1: MoE(h) = sum_i W_i

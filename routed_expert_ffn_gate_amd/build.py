@@ -59,7 +59,8 @@ _M0_WRITE = re.compile(r"^\s*s_mov_b32\s+m0,\s*s\d+\s*$")
 
 def m0_violations(asm_lines) -> list:
     """Lines of device assembly that use M0 other than as the LDS DMA helpers
-    do (s_mov_b32 m0, sN; s_nop 0; global_load_lds_dwordx4)."""
+    do (s_mov_b32 m0, sN; s_nop 0; global_load_lds_dwordx4 or
+    buffer_load_dwordx4 ... lds)."""
     lines = [l.split(";")[0].strip() for l in asm_lines]
     lines = [l for l in lines if l]
     bad = []
@@ -67,7 +68,8 @@ def m0_violations(asm_lines) -> list:
         if not re.search(r"\bm0\b", l):
             continue
         ok = (_M0_WRITE.match(l) and i + 2 < len(lines) and lines[i + 1] == "s_nop 0"
-              and lines[i + 2].startswith("global_load_lds_dwordx4"))
+              and (lines[i + 2].startswith("global_load_lds_dwordx4")
+                   or re.match(r"buffer_load_dwordx4 .* lds$", lines[i + 2])))
         if not ok:
             bad.append(l)
     return bad
@@ -85,6 +87,11 @@ def _check_m0(src: str) -> None:
         raise RuntimeError(f"{src}: M0 used outside the LDS DMA helpers: {bad[:4]}")
 
 
+def _uses_lds_dma(src: str) -> bool:
+    text = open(src).read()
+    return "m0" in text or "mfma_tile.h" in text
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
@@ -99,7 +106,7 @@ def build(verbose: bool = False) -> str:
             if verbose and out.strip():
                 print(out)
     with ThreadPoolExecutor(min(8, len(srcs))) as ex:
-        list(ex.map(_check_m0, [src for src in srcs if "m0" in open(src).read()]))
+        list(ex.map(_check_m0, [src for src in srcs if _uses_lds_dma(src)]))
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp])
     _check_kernel_stubs(tmp)

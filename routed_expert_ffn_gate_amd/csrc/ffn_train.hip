@@ -1,0 +1,507 @@
+// Training form of the grouped SwiGLU FFN: a forward that keeps its two
+// projections, and the gradients.
+//
+// Definition (FreeBalance, "FreeBalance: Pre-Routing Online MoE Load Balancing
+// via Residual Workload Prediction", section 2.1: expert_i(h), here the SwiGLU
+// block of moelb_grouped_ffn), for a row x of expert e:
+//   [g, u] = W13 x, a = silu(g) u, y = W2 a
+// and with s = 1 / (1 + e^-g), dy the gradient of y:
+//   da = W2^T dy, dg = da u s (1 + g (1 - s)), du = da g s
+//   dx = W13^T [dg, du], dW13 = sum [dg, du] x^T, dW2 = sum dy a^T
+// the sums over the expert's rows.
+//
+// Six products, all on the tile of mfma_tile.h, over the row schedule of the
+// forward (rows expert-major, "virtual" rows):
+//   up     x rows (gathered) x W13, z = [g, u] kept in fp32, a out
+//   down   a x W2, y rows scattered
+//   da     dy rows (gathered) x W2 read as columns; the epilogue reads z and
+//          writes [dg, du] and a again (a is not kept between the calls: it
+//          costs one fused recomputation and saves rows x inter of memory)
+//   dx     [dg, du] x W13 read as columns, dx rows scattered
+//   dW13   [dg, du] and x (gathered), both read as columns, summed over rows
+//   dW2    dy (gathered) and a, likewise
+// z stays fp32: rounded to bf16 it would add as much error to dx as all the
+// other roundings together.  a and [dg, du] are rounded to the storage type,
+// once each, because they are the next products' operands.
+// Weight gradients: one workgroup owns a tile of one expert's gradient and
+// walks that expert's rows in order, so a gradient is one fixed sum; where
+// that leaves compute units idle the rows are cut into `splits` parts with
+// fp32 partial sums, added in order by a second kernel.
+#include "ffn_sched.h"
+#include "mfma_tile.h"
+
+namespace {
+
+enum { OP_UP = 0, OP_DOWN = 1, OP_DA = 2, OP_DX = 3, OP_DW13 = 4, OP_DW2 = 5 };
+
+template <typename T>
+struct TrainArgs {
+  const T* x;
+  int rows_x;
+  const T* w13;
+  const T* w2;
+  const T* dy;
+  float* z;    // [rows][2 inter], virtual rows
+  T* a;        // [rows][inter], virtual rows
+  T* dz;       // [rows][2 inter], virtual rows
+  T* out;      // y or dx, physical rows; dW13 or dW2
+  float* part; // weight gradients: [splits][E][M][N] partial sums
+  int splits;
+  int rows, d, inter, E, ntn, ntm;
+  FfnSched s;
+};
+
+__device__ __forceinline__ uint32_t bytes_u32(size_t n) {
+  return n < mt::OUTSIDE ? (uint32_t)n : mt::OUTSIDE;
+}
+
+__device__ __forceinline__ int clampi(int v, int n) { return min(max(v, 0), n - 1); }
+
+// The epilogues of the row-tiled products, on 8 adjacent columns at n of
+// virtual row v.
+template <typename T>
+__device__ __forceinline__ void put_up(const TrainArgs<T>& p, int v, int n, const float* g, const float* u) {
+  float* z = p.z + (size_t)v * 2 * p.inter + n;
+  mt::store8(z, g);
+  mt::store8(z + p.inter, u);
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = silu_f32(g[i]) * u[i];
+  mt::store8(p.a + (size_t)v * p.inter + n, a);
+}
+
+template <typename T>
+__device__ __forceinline__ void put_da(const TrainArgs<T>& p, int v, int n, const float* da) {
+  const float* z = p.z + (size_t)v * 2 * p.inter + n;
+  float g[8], u[8], dg[8], du[8], a[8];
+  mt::load8(z, g);
+  mt::load8(z + p.inter, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[i]));
+    const float gs = g[i] * s;
+    a[i] = gs * u[i];
+    du[i] = da[i] * gs;
+    dg[i] = da[i] * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+  }
+  T* dz = p.dz + (size_t)v * 2 * p.inter + n;
+  mt::store8(dz, dg);
+  mt::store8(dz + p.inter, du);
+  mt::store8(p.a + (size_t)v * p.inter + n, a);
+}
+
+// ---------------------------------------------------------------- row-tiled products
+
+template <int F, int OP>
+__global__ __launch_bounds__(mt::THREADS) void train_rows_kernel(TrainArgs<uint16_t> p) {
+  extern __shared__ __align__(16) char smem[];
+  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+  const int n_mtiles = *p.s.n_mtiles;
+  const int tile = xcd_tile(n_mtiles * p.ntn);
+  if (tile < 0) return;
+  int mti, nt;
+  grouped_tile(tile, n_mtiles, p.ntn, mti, nt);
+  const int e = p.s.mt_e[mti], v0 = p.s.mt_v0[mti], vend = p.s.eoff[e + 1];
+  const int d = p.d, I = p.inter;
+  constexpr bool GU = OP == OP_UP;
+  constexpr int HB = 32 * F;  // gate (or up) rows of an "up" tile
+  const int n0 = nt * (GU ? HB : 64 * F);
+  const int N = (OP == OP_UP || OP == OP_DA) ? I : d;
+  const int K = OP == OP_DOWN ? I : OP == OP_DX ? 2 * I : d;
+
+  mt::RowOp<F> oa;
+  {
+    const uint16_t* base = OP == OP_UP ? p.x : OP == OP_DOWN ? p.a : OP == OP_DA ? p.dy : p.dz;
+    const int rows = OP == OP_UP ? p.rows_x : p.rows;
+    const int32_t* map = OP == OP_UP ? p.s.asrc : OP == OP_DA ? p.s.rowmap : nullptr;
+    oa.init(base, bytes_u32((size_t)rows * K * 2), K, K, [&](int r) {
+      int v = v0 + r;
+      v = v < vend ? v : v0;
+      return map ? clampi(map[v], rows) : v;
+    });
+  }
+  f32x16_t acc[F][F];
+  const int KT = (K + mt::BK - 1) / mt::BK;
+  if constexpr (OP == OP_UP || OP == OP_DOWN) {
+    mt::RowOp<F> ob;
+    const uint16_t* w = OP == OP_UP ? p.w13 + (size_t)e * 2 * I * d : p.w2 + (size_t)e * d * I;
+    ob.init(w, bytes_u32((size_t)(GU ? 2 * I : d) * K * 2), K, K, [&](int r) {
+      const int c = n0 + (GU ? r % HB : r);
+      return (c < N ? c : 0) + (GU && r >= HB ? I : 0);
+    });
+    mt::k_loop<F, GU>(lds, oa, ob, KT, acc);
+  } else {
+    mt::ColOp<F, false> ob;
+    const uint16_t* w = OP == OP_DA ? p.w2 + (size_t)e * d * I : p.w13 + (size_t)e * 2 * I * d;
+    ob.init(w, bytes_u32((size_t)K * N * 2), N, K, n0, N);
+    mt::k_loop<F, GU>(lds, oa, ob, KT, acc);
+  }
+  if constexpr (GU) {
+    mt::drain<F, true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
+      if (v0 + r < vend && n0 + c < N) put_up(p, v0 + r, n0 + c, g, u);
+    });
+  } else if constexpr (OP == OP_DA) {
+    mt::drain<F, false>(lds, acc, [&](int r, int c, const float* v) {
+      if (v0 + r < vend && n0 + c < N) put_da(p, v0 + r, n0 + c, v);
+    });
+  } else {
+    mt::drain<F, false>(lds, acc, [&](int r, int c, const float* v) {
+      if (v0 + r < vend && n0 + c < N)
+        mt::store8(p.out + (size_t)clampi(p.s.rowmap[v0 + r], p.rows) * d + n0 + c, v);
+    });
+  }
+}
+
+template <int OP>
+__global__ __launch_bounds__(mt::THREADS) void train_rows_f32_kernel(TrainArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::S_FLOATS];
+  const int n_mtiles = *p.s.n_mtiles;
+  const int tile = xcd_tile(n_mtiles * p.ntn);
+  if (tile < 0) return;
+  const int mti = tile / p.ntn, nt = tile % p.ntn;
+  const int e = p.s.mt_e[mti], v0 = p.s.mt_v0[mti], vend = p.s.eoff[e + 1];
+  const int d = p.d, I = p.inter;
+  constexpr bool GU = OP == OP_UP;
+  const int n0 = nt * (GU ? 32 : 64);
+  const int N = (OP == OP_UP || OP == OP_DA) ? I : d;
+  const int K = OP == OP_DOWN ? I : OP == OP_DX ? 2 * I : d;
+  const float* base = OP == OP_UP ? p.x : OP == OP_DOWN ? p.a : OP == OP_DA ? p.dy : p.dz;
+  const int rows = OP == OP_UP ? p.rows_x : p.rows;
+  const int32_t* map = OP == OP_UP ? p.s.asrc : OP == OP_DA ? p.s.rowmap : nullptr;
+  const int va = v0 + (threadIdx.x >> 2);  // the row this thread fetches
+  const int ra = va < vend ? (map ? clampi(map[va], rows) : va) : -1;
+  auto pa = [&](int, int k) { return ra < 0 ? nullptr : base + (size_t)ra * K + k; };
+  f32x16_t acc;
+  if constexpr (OP == OP_UP || OP == OP_DOWN) {
+    const float* w = OP == OP_UP ? p.w13 + (size_t)e * 2 * I * d : p.w2 + (size_t)e * d * I;
+    auto pb = [&](int r, int k) {
+      const int c = n0 + (GU ? r & 31 : r);
+      return c < N ? w + ((size_t)c + (GU && r >= 32 ? I : 0)) * K + k : nullptr;
+    };
+    mt::k_loop_f32<false, false>(lds, pa, pb, K, acc);
+  } else {
+    const float* w = OP == OP_DA ? p.w2 + (size_t)e * d * I : p.w13 + (size_t)e * 2 * I * d;
+    auto pb = [&](int r, int k) { return n0 + r < N ? w + (size_t)k * N + n0 + r : nullptr; };
+    mt::k_loop_f32<false, true>(lds, pa, pb, K, acc);
+  }
+  if constexpr (GU) {
+    mt::drain_f32<true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
+      if (v0 + r < vend && n0 + c < N) put_up(p, v0 + r, n0 + c, g, u);
+    });
+  } else if constexpr (OP == OP_DA) {
+    mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) {
+      if (v0 + r < vend && n0 + c < N) put_da(p, v0 + r, n0 + c, v);
+    });
+  } else {
+    mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) {
+      if (v0 + r < vend && n0 + c < N)
+        mt::store8(p.out + (size_t)clampi(p.s.rowmap[v0 + r], p.rows) * d + n0 + c, v);
+    });
+  }
+}
+
+// ---------------------------------------------------------------- weight gradients
+
+// Tile t -> expert, split of its rows, tile of its gradient.
+struct WTile {
+  int e, mi, ni, split, k0, n, v0;
+};
+template <typename T>
+__device__ __forceinline__ bool w_tile(const TrainArgs<T>& p, WTile& w) {
+  const int per = p.ntm * p.ntn * p.splits;
+  int t = xcd_tile(p.E * per);
+  if (t < 0) return false;
+  w.e = t / per;
+  t -= w.e * per;
+  w.split = t / (p.ntm * p.ntn);
+  t -= w.split * p.ntm * p.ntn;
+  grouped_tile(t, p.ntm, p.ntn, w.mi, w.ni);
+  const int vb = p.s.eoff[w.e], n = p.s.eoff[w.e + 1] - vb;
+  const int steps = (n + mt::BK - 1) / mt::BK;
+  const int ps = (steps + p.splits - 1) / p.splits * mt::BK;  // rows of a split
+  w.k0 = min(n, w.split * ps);
+  w.n = min(n, w.k0 + ps) - w.k0;
+  w.v0 = vb + w.k0;
+  return true;
+}
+
+template <typename T>
+__device__ __forceinline__ void put_w(const TrainArgs<T>& p, const WTile& w, int M, int N, int m, int n,
+                                      const float* v) {
+  if (m >= M || n >= N) return;
+  const size_t at = ((size_t)w.e * M + m) * N + n;
+  if (p.splits > 1)
+    mt::store8(p.part + (size_t)w.split * p.E * M * N + at, v);
+  else
+    mt::store8(p.out + at, v);
+}
+
+template <int F, int OP>
+__global__ __launch_bounds__(mt::THREADS) void train_weights_kernel(TrainArgs<uint16_t> p) {
+  extern __shared__ __align__(16) char smem[];
+  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+  WTile w;
+  if (!w_tile(p, w)) return;
+  const int d = p.d, I = p.inter;
+  const int M = OP == OP_DW13 ? 2 * I : d, N = OP == OP_DW13 ? d : I;
+  const int m0 = w.mi * 64 * F, n0 = w.ni * 64 * F;
+  const int KT = max(1, (w.n + mt::BK - 1) / mt::BK);  // no rows: one step of zeros
+  f32x16_t acc[F][F];
+  if constexpr (OP == OP_DW13) {
+    mt::ColOp<F, false> oa;
+    mt::ColOp<F, true> ob;
+    oa.init(p.dz + (size_t)w.v0 * M, bytes_u32((size_t)w.n * M * 2), M, w.n, m0, M);
+    ob.init(p.x, bytes_u32((size_t)p.rows_x * N * 2), N, w.n, n0, N, p.s.asrc + w.v0, p.rows_x);
+    mt::k_loop<F, false>(lds, oa, ob, KT, acc);
+  } else {
+    mt::ColOp<F, true> oa;
+    mt::ColOp<F, false> ob;
+    oa.init(p.dy, bytes_u32((size_t)p.rows * M * 2), M, w.n, m0, M, p.s.rowmap + w.v0, p.rows);
+    ob.init(p.a + (size_t)w.v0 * N, bytes_u32((size_t)w.n * N * 2), N, w.n, n0, N);
+    mt::k_loop<F, false>(lds, oa, ob, KT, acc);
+  }
+  mt::drain<F, false>(lds, acc, [&](int r, int c, const float* v) { put_w(p, w, M, N, m0 + r, n0 + c, v); });
+}
+
+template <int OP>
+__global__ __launch_bounds__(mt::THREADS) void train_weights_f32_kernel(TrainArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::S_FLOATS];
+  WTile w;
+  if (!w_tile(p, w)) return;
+  const int d = p.d, I = p.inter;
+  const int M = OP == OP_DW13 ? 2 * I : d, N = OP == OP_DW13 ? d : I;
+  const int m0 = w.mi * 64, n0 = w.ni * 64;
+  f32x16_t acc;
+  auto pa = [&](int r, int k) -> const float* {
+    if (m0 + r >= M) return nullptr;
+    if (OP == OP_DW13) return p.dz + (size_t)(w.v0 + k) * M + m0 + r;
+    return p.dy + (size_t)clampi(p.s.rowmap[w.v0 + k], p.rows) * M + m0 + r;
+  };
+  auto pb = [&](int r, int k) -> const float* {
+    if (n0 + r >= N) return nullptr;
+    if (OP == OP_DW13) return p.x + (size_t)clampi(p.s.asrc[w.v0 + k], p.rows_x) * N + n0 + r;
+    return p.a + (size_t)(w.v0 + k) * N + n0 + r;
+  };
+  mt::k_loop_f32<true, true>(lds, pa, pb, w.n, acc);
+  mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) { put_w(p, w, M, N, m0 + r, n0 + c, v); });
+}
+
+// out[i] = sum over splits, in order, of part[s][i]; 8 values per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part, int splits, size_t n8,
+                                                         T* __restrict__ out) {
+  const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n8) return;
+  float v[8];
+  mt::load8(part + i * 8, v);
+  for (int s = 1; s < splits; ++s) {
+    float u[8];
+    mt::load8(part + ((size_t)s * n8 + i) * 8, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += u[j];
+  }
+  mt::store8(out + i * 8, v);
+}
+
+// ---------------------------------------------------------------- host
+
+// Row tile of a call (64 F, or 64 for fp32): 256 rows where the experts
+// average enough of them and the tiles still cover the compute units.
+int row_f(int rows, int E, int d, int inter) {
+  const int least = d < inter ? d : inter;
+  const size_t tiles = (size_t)(rows + 255) / 256 * ((least + 255) / 256);
+  return (size_t)rows >= (size_t)192 * E && tiles >= 192 ? 4 : 2;
+}
+
+int weight_f(int E, int M, int N) { return (size_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= 64 ? 4 : 2; }
+
+// Parts the rows of every expert are cut into for the weight gradients: enough
+// workgroups for the compute units, at least 512 rows each on average.
+int weight_splits(int rows, int E, int M, int N, int dtype) {
+  const int b = dtype == MOELB_BF16 ? 64 * weight_f(E, M, N) : mt::S_BM;
+  const int slots = b == 256 ? 256 : 512;
+  const size_t tiles = (size_t)E * ((M + b - 1) / b) * ((N + b - 1) / b);
+  const size_t want = slots / tiles, most = (size_t)rows / E / 512;
+  const size_t s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+
+struct BackLayout {
+  size_t dz, part, total;
+};
+BackLayout back_layout(int rows, int num_groups, int E, int d, int inter, int dtype) {
+  BackLayout l;
+  const size_t eb = moelb_elem_bytes(dtype);
+  l.dz = sched_layout(rows, num_groups, E, inter, dtype, nullptr, nullptr);  // schedule tables and a
+  l.part = l.dz + moelb_align256((size_t)rows * 2 * inter * eb);
+  const size_t s13 = weight_splits(rows, E, 2 * inter, d, dtype), s2 = weight_splits(rows, E, d, inter, dtype);
+  const size_t p13 = s13 > 1 ? s13 * E * 2 * inter * d * 4 : 0, p2 = s2 > 1 ? s2 * E * inter * d * 4 : 0;
+  l.total = l.part + moelb_align256(p13 > p2 ? p13 : p2);
+  return l;
+}
+
+template <typename T, int OP>
+int launch_rows(TrainArgs<T> p, int BM, hipStream_t s) {
+  if (p.rows == 0) return MOELB_OK;
+  const int bn = OP == OP_UP ? BM / 2 : BM;
+  const int N = (OP == OP_UP || OP == OP_DA) ? p.inter : p.d;
+  p.ntn = (N + bn - 1) / bn;
+  const size_t grid = ((size_t)(p.rows + BM - 1) / BM + p.E) * p.ntn + 8;
+  if (grid > 0x7fffffffull) return MOELB_EINVAL;
+  if constexpr (sizeof(T) == 4) {
+    hipLaunchKernelGGL((train_rows_f32_kernel<OP>), dim3((unsigned)grid), dim3(mt::THREADS), 0, s, p);
+  } else if (BM == 256) {
+    if (!moelb_allow_lds(train_rows_kernel<4, OP>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_rows_kernel<4, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<4>(), s, p);
+  } else {
+    if (!moelb_allow_lds(train_rows_kernel<2, OP>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_rows_kernel<2, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<2>(), s, p);
+  }
+  MOELB_CHECK_LAUNCH();
+  return MOELB_OK;
+}
+
+template <typename T, int OP>
+int launch_weights(TrainArgs<T> p, T* out, hipStream_t s) {
+  const int M = OP == OP_DW13 ? 2 * p.inter : p.d, N = OP == OP_DW13 ? p.d : p.inter;
+  const int dtype = sizeof(T) == 4 ? MOELB_F32 : MOELB_BF16;
+  const int b = sizeof(T) == 4 ? mt::S_BM : 64 * weight_f(p.E, M, N);
+  p.out = out;
+  p.splits = weight_splits(p.rows, p.E, M, N, dtype);
+  p.ntm = (M + b - 1) / b;
+  p.ntn = (N + b - 1) / b;
+  const size_t grid = (size_t)p.E * p.ntm * p.ntn * p.splits + 8;
+  if (grid > 0x7fffffffull) return MOELB_EINVAL;
+  if constexpr (sizeof(T) == 4) {
+    hipLaunchKernelGGL((train_weights_f32_kernel<OP>), dim3((unsigned)grid), dim3(mt::THREADS), 0, s, p);
+  } else if (b == 256) {
+    if (!moelb_allow_lds(train_weights_kernel<4, OP>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_weights_kernel<4, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<4>(), s,
+                       p);
+  } else {
+    if (!moelb_allow_lds(train_weights_kernel<2, OP>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_weights_kernel<2, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<2>(), s,
+                       p);
+  }
+  MOELB_CHECK_LAUNCH();
+  if (p.splits > 1) {
+    const size_t n8 = (size_t)p.E * M * N / 8;
+    hipLaunchKernelGGL((sum_splits_kernel<T>), dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, p.part, p.splits,
+                       n8, out);
+    MOELB_CHECK_LAUNCH();
+  }
+  return MOELB_OK;
+}
+
+bool misaligned(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15; }
+
+// What both calls require of their sizes; operands of 32-bit byte offsets.
+bool sizes_ok(int rows_x, int rows, int num_groups, int E, int G, int rank, const void* gather, int gather_k, int d,
+              int inter, int dtype) {
+  if (rows < 0 || rows_x < 0 || num_groups < 1 || num_groups > 32768 || E < 1 || E > MOELB_MAX_E) return false;
+  if (d <= 0 || d % 8 != 0 || inter <= 0 || inter % 8 != 0 || !moelb_dtype_ok(dtype)) return false;
+  if (rank >= 0 && (G < 1 || rank >= G || num_groups % E != 0)) return false;
+  if (gather && gather_k < 1) return false;
+  if (rows > 0 && rows_x < 1) return false;
+  const size_t eb = moelb_elem_bytes(dtype), most = (1ull << 32) - 65536;
+  return (size_t)rows_x * d * eb < most && (size_t)rows * d * eb < most && (size_t)rows * 2 * inter * eb < most &&
+         (size_t)2 * inter * d * eb < most;
+}
+
+template <typename T>
+int run_forward(TrainArgs<T> p, int BM, hipStream_t s) {
+  int st = launch_rows<T, OP_UP>(p, BM, s);
+  return st != MOELB_OK ? st : launch_rows<T, OP_DOWN>(p, BM, s);
+}
+
+template <typename T>
+int run_backward(TrainArgs<T> p, int BM, T* dx, T* dw13, T* dw2, hipStream_t s) {
+  int st = launch_rows<T, OP_DA>(p, BM, s);
+  if (st == MOELB_OK && dx) {
+    p.out = dx;
+    st = launch_rows<T, OP_DX>(p, BM, s);
+  }
+  if (st == MOELB_OK && dw13) st = launch_weights<T, OP_DW13>(p, dw13, s);
+  if (st == MOELB_OK && dw2) st = launch_weights<T, OP_DW2>(p, dw2, s);
+  return st;
+}
+
+}  // namespace
+
+extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, const int32_t* group_off, int num_groups,
+                                       int E, int G, int rank, const int32_t* gather, int gather_k, int d, int inter,
+                                       int dtype, const void* w13, const void* w2, void* ws, size_t ws_bytes,
+                                       float* z, void* y, void* stream) {
+  if (!sizes_ok(rows_x, rows, num_groups, E, G, rank, gather, gather_k, d, inter, dtype)) return MOELB_EINVAL;
+  if (!group_off || !w13 || !w2 || (rows > 0 && (!x || !y || !z))) return MOELB_EINVAL;
+  if (misaligned(x) || misaligned(w13) || misaligned(w2) || misaligned(z) || misaligned(y)) return MOELB_EINVAL;
+  const size_t need = sched_layout(rows, num_groups, E, inter, dtype, nullptr, nullptr);
+  if (!ws || misaligned(ws) || ws_bytes < need) return MOELB_EWORKSPACE;
+  if (rows == 0) return MOELB_OK;
+  FfnSched sc;
+  sched_layout(rows, num_groups, E, inter, dtype, &sc, static_cast<char*>(ws));
+  sc.wpacked = 0;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int BM = dtype == MOELB_BF16 ? 64 * row_f(rows, E, d, inter) : mt::S_BM;
+  const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, sc, s);
+  if (st != MOELB_OK) return st;
+  auto run = [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    TrainArgs<T> p = {};
+    p.x = static_cast<const T*>(x);
+    p.rows_x = rows_x;
+    p.w13 = static_cast<const T*>(w13);
+    p.w2 = static_cast<const T*>(w2);
+    p.z = z;
+    p.a = static_cast<T*>(sc.amid);
+    p.out = static_cast<T*>(y);
+    p.rows = rows, p.d = d, p.inter = inter, p.E = E, p.s = sc;
+    return run_forward<T>(p, BM, s);
+  };
+  return dtype == MOELB_BF16 ? run(static_cast<uint16_t*>(nullptr)) : run(static_cast<float*>(nullptr));
+}
+
+extern "C" size_t moelb_grouped_ffn_backward_workspace_bytes(int rows, int num_groups, int E, int d, int inter,
+                                                             int dtype) {
+  if (rows < 0 || num_groups < 1 || E < 1 || d < 1 || inter < 1 || !moelb_dtype_ok(dtype)) return 0;
+  return back_layout(rows, num_groups, E, d, inter, dtype).total;
+}
+
+extern "C" int moelb_grouped_ffn_backward(const void* dy, const void* x, int rows_x, int rows,
+                                          const int32_t* group_off, int num_groups, int E, int G, int rank,
+                                          const int32_t* gather, int gather_k, int d, int inter, int dtype,
+                                          const void* w13, const void* w2, const float* z, void* ws, size_t ws_bytes,
+                                          void* dx, void* dw13, void* dw2, void* stream) {
+  if (!sizes_ok(rows_x, rows, num_groups, E, G, rank, gather, gather_k, d, inter, dtype)) return MOELB_EINVAL;
+  if (!group_off || !w13 || !w2 || (rows > 0 && (!x || !dy || !z))) return MOELB_EINVAL;
+  if (misaligned(x) || misaligned(dy) || misaligned(w13) || misaligned(w2) || misaligned(z) || misaligned(dx) ||
+      misaligned(dw13) || misaligned(dw2))
+    return MOELB_EINVAL;
+  const BackLayout l = back_layout(rows, num_groups, E, d, inter, dtype);
+  if (!ws || misaligned(ws) || ws_bytes < l.total) return MOELB_EWORKSPACE;
+  if (!dx && !dw13 && !dw2) return MOELB_OK;
+  char* base = static_cast<char*>(ws);
+  FfnSched sc;
+  sched_layout(rows, num_groups, E, inter, dtype, &sc, base);
+  sc.wpacked = 0;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int BM = dtype == MOELB_BF16 ? 64 * row_f(rows, E, d, inter) : mt::S_BM;
+  const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, sc, s);
+  if (st != MOELB_OK) return st;
+  auto run = [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    TrainArgs<T> p = {};
+    p.x = static_cast<const T*>(x);
+    p.rows_x = rows_x;
+    p.w13 = static_cast<const T*>(w13);
+    p.w2 = static_cast<const T*>(w2);
+    p.dy = static_cast<const T*>(dy);
+    p.z = const_cast<float*>(z);
+    p.a = static_cast<T*>(sc.amid);
+    p.dz = reinterpret_cast<T*>(base + l.dz);
+    p.part = reinterpret_cast<float*>(base + l.part);
+    p.rows = rows, p.d = d, p.inter = inter, p.E = E, p.s = sc;
+    return run_backward<T>(p, BM, static_cast<T*>(dx), static_cast<T*>(dw13), static_cast<T*>(dw2), s);
+  };
+  return dtype == MOELB_BF16 ? run(static_cast<uint16_t*>(nullptr)) : run(static_cast<float*>(nullptr));
+}

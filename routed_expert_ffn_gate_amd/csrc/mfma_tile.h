@@ -1,0 +1,507 @@
+// Matrix-core tile of the training and adapter kernels: one workgroup computes
+// a square tile C[m, n] = sum_k A[m, k] B[n, k] whose operands lie in memory
+// either with k contiguous (a "row" operand: forward weights, activations as
+// the left factor) or with k as the row index and m or n contiguous (a
+// "column" operand: weights in the input gradients, where the sum runs over
+// their rows; both activations in the weight gradients, where it runs over
+// tokens).  No operand is transposed in memory beforehand.
+//
+//  * Tile 64F x 64F, F = 4 (256) or F = 2 (128); 256 threads as 2 x 2 waves,
+//    wave tile 32F x 32F of v_mfma_f32_32x32x16_bf16, fp32 accumulators.
+//  * K steps of 64 stream memory -> LDS with buffer_load_dwordx4 ... lds into a
+//    ring of five half-stages (A or B of one step; 32 KiB each at F = 4, 16 KiB
+//    at F = 2, so two F = 2 workgroups share a CU): while step t computes,
+//    steps t+1 and half of t+2 are in flight.  The refills are spread over the
+//    step, one instruction per F MFMAs.
+//  * The loads go through a buffer descriptor: a lane whose k lies past the end
+//    asks for an offset outside the descriptor and gets zeros in LDS, which is
+//    how K tails and ragged token counts end inside a step without a branch.
+//    Rows and columns of C past their end repeat a valid one and are not
+//    stored.
+//  * Row operand in LDS: 64F rows of 128 B, 16-byte chunks swizzled, fragments
+//    by ds_read_b128.  Column operand: 64 k rows of 128F B, 64-byte segments
+//    XORed with the k row, fragments by two ds_read_b64_tr_b16 (each 16 lanes
+//    read 4 k rows x 16 columns and receive them transposed: lane i column i,
+//    4 consecutive k).  The XOR puts the 4 rows a read touches on different
+//    banks.
+//  * A column operand may be gathered: k row t reads memory row idx[t].  A wave
+//    holds the indices of its 16 k rows of 32 steps in 8 registers and takes
+//    them by v_readlane; no LDS and no wait inside a step.
+#pragma once
+
+#include "common.h"
+
+namespace mt {
+
+constexpr int BK = 64;
+constexpr int SLOTS = 5;
+constexpr int THREADS = 256;
+// outside every descriptor below (their byte counts stay under it)
+constexpr uint32_t OUTSIDE = 0xfffffff0u;
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+template <int F>
+constexpr int half_elems() { return 64 * F * BK; }
+// the ring; the epilogue stages 128 rows x 64F fp32 in the same space
+template <int F>
+constexpr size_t lds_bytes() { return (size_t)SLOTS * half_elems<F>() * sizeof(uint16_t); }
+
+__device__ __forceinline__ i32x4_t descriptor(const void* p, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p);
+  i32x4_t r;
+  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  r.y = __builtin_amdgcn_readfirstlane((int)((b >> 32) & 0xffffu));
+  r.z = __builtin_amdgcn_readfirstlane((int)bytes);
+  r.w = 0x00020000;
+  return r;
+}
+
+// 16 bytes per lane, memory -> LDS: lane i lands at LDS byte address m0 + 16 i;
+// an offset outside the descriptor writes zeros.  M0 is a reserved register
+// (the build checks that no compiler code uses it).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16(uint32_t voff, i32x4_t srd, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(srd), "s"(m0)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Row operand: k contiguous.  DMA instruction j (0 .. 2F-1) of wave w fills
+// the 8 LDS rows (2F w + j) * 8 ..; lane l row l / 8 of them, slot l % 8, which
+// holds chunk slot ^ swizzle(row).
+template <int F>
+struct RowOp {
+  static constexpr bool COL = false;
+  i32x4_t srd;
+  uint32_t off[2 * F];
+  int ck[2];  // first k of this lane's chunk, even and odd instructions
+  int K;
+  // row(r): memory row of LDS row r, ld: elements per memory row
+  template <class Row>
+  __device__ __forceinline__ void init(const void* base, uint32_t bytes, int ld, int K_, Row row) {
+    srd = descriptor(base, bytes);
+    K = K_;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 2 * F; ++j) {
+      const int r = (wave * 2 * F + j) * 8 + (lane >> 3);
+      const int chunk = (lane & 7) ^ (((r >> 1) ^ (r << 2)) & 7);
+      if (j < 2) ck[j] = chunk * 8;
+      off[j] = ((uint32_t)row(r) * (uint32_t)ld + (uint32_t)chunk * 8u) * 2u;
+    }
+  }
+  __device__ __forceinline__ void begin(int) {}
+  __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
+    const uint32_t v = ck[j & 1] < K - t * BK ? off[j] + (uint32_t)t * (BK * 2) : OUTSIDE;
+    copy16(v, srd, m0);
+  }
+};
+
+// Column operand: memory row = k, columns contiguous.  DMA instruction j of
+// wave w fills k rows 16 w + j R .. (R = 1024 / (128 F) rows of 128F bytes);
+// a lane's 16-byte slot s of its row holds chunk s with its 64-byte segment
+// (s / 4) XORed with the k row.  With GATHER, k row t reads memory row
+// idx[t] clamped to [0, rows).
+template <int F, bool GATHER>
+struct ColOp {
+  static constexpr bool COL = true;
+  static constexpr int R = 8 / F;
+  i32x4_t srd;
+  uint32_t off0;  // byte offset of the lane's column chunk (+ its first k row, if not gathered)
+  uint32_t ld2;
+  int kr;         // this lane's k row in a step, instruction 0
+  int K;
+  const int32_t* idx;
+  int rows;
+  int gi[GATHER ? 8 : 1];
+  // columns c0 .. of N; K memory rows from `base` (or from idx)
+  __device__ __forceinline__ void init(const void* base, uint32_t bytes, int ld, int K_, int c0, int N,
+                                       const int32_t* idx_ = nullptr, int rows_ = 0) {
+    srd = descriptor(base, bytes);
+    ld2 = (uint32_t)ld * 2u;
+    K = K_;
+    idx = idx_;
+    rows = rows_;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int rr = lane / (64 / R), s = lane & (8 * F - 1);
+    kr = wave * 16 + rr;
+    // the k row of instruction j is kr + j R; its XOR bits: F = 4 (R = 2)
+    // needs k % 8, which changes with j, F = 2 (R = 4) k % 4, which does not
+    slot = s;
+    col0 = c0;
+    ncols = N;
+    off0 = GATHER ? 0u : (uint32_t)kr * ld2;
+  }
+  int slot, col0, ncols;
+  __device__ __forceinline__ uint32_t col_off(int j) const {
+    const int k = kr + j * R;
+    const int c = col0 + ((((slot >> 2) ^ (k & (2 * F - 1))) << 2) | (slot & 3)) * 8;
+    return (uint32_t)(c < ncols ? c : 0) * 2u;
+  }
+  // before the first instruction of step t: indices for 32 steps at a time,
+  // four steps a register (lane l: step l / 16, k row l % 16 of the wave)
+  __device__ __forceinline__ void begin(int t) {
+    if constexpr (GATHER) {
+      if ((t & 31) == 0) {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int k = (t + q * 4 + (lane >> 4)) * BK + wave * 16 + (lane & 15);
+          gi[q] = k < K ? min(max(idx[k], 0), rows - 1) : 0;
+        }
+      } else if ((t & 3) == 0) {
+#pragma unroll
+        for (int q = 0; q < 7; ++q) gi[q] = gi[q + 1];
+      }
+    }
+  }
+  __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
+    const bool in = kr + j * R < K - t * BK;
+    uint32_t v;
+    if constexpr (GATHER) {
+      const int l0 = (t & 3) * 16 + j * R;
+      const int lane = threadIdx.x & 63;
+      uint32_t o = (uint32_t)__builtin_amdgcn_readlane(gi[0], l0) * ld2;
+#pragma unroll
+      for (int q = 1; q < R; ++q) {
+        const uint32_t oq = (uint32_t)__builtin_amdgcn_readlane(gi[0], l0 + q) * ld2;
+        o = lane / (64 / R) >= q ? oq : o;
+      }
+      v = o + col_off(j);
+    } else {
+      v = off0 + (uint32_t)(t * BK + j * R) * ld2 + col_off(j);
+    }
+    copy16(in ? v : OUTSIDE, srd, m0);
+  }
+};
+
+// LDS element offset (inside a half-stage) of this lane's fragments.
+// Row operand: sub-step ks, block i = 32 rows: at[ks] + (row offset of block i) * 64.
+// Column operand: at[h * F + i] + ks * 16 * 64F, h = the k half of the fragment.
+template <int F, bool COL>
+struct FragAt {
+  int at[COL ? 2 * F : 4];
+  __device__ __forceinline__ void init(int w /* wave's index along this operand */, int row0 /* row operand: its first row */) {
+    const int lane = threadIdx.x & 63;
+    const int fr = lane & 31, fh = lane >> 5;
+    if constexpr (!COL) {
+      const int sw = ((fr >> 1) ^ (fr << 2)) & 7;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) at[ks] = (row0 + fr) * BK + (((ks * 2 + fh) ^ sw) * 8);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          const int k = fh * 8 + h * 4 + ((lane >> 2) & 3);
+          const int seg = (w * F + i) ^ (k & (2 * F - 1));
+          at[h * F + i] = k * 64 * F + seg * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+        }
+    }
+  }
+  __device__ __forceinline__ bf16x8_t read(const uint16_t* half, int ks, int i, int row_off) const {
+    if constexpr (!COL) {
+      return *reinterpret_cast<const bf16x8_t*>(half + at[ks] + row_off * BK);
+    } else {
+      typedef __attribute__((address_space(3))) s16x4_t lds4_t;
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(half + at[i] + ks * 16 * 64 * F));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4_t*)(half + at[F + i] + ks * 16 * 64 * F));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// Column (B row in LDS) offset of block ni of wave column wn.  GU: the first
+// half of the tile's B rows are gate rows, the second half the matching up
+// rows, and a wave takes the same columns of both.
+template <int F, bool GU>
+__device__ __forceinline__ int block_col(int wn, int ni) {
+  return GU ? wn * 16 * F + (ni % (F / 2)) * 32 + (ni / (F / 2)) * 32 * F : wn * 32 * F + ni * 32;
+}
+
+// The K loop: acc[mi][ni] += A block mi x B block ni over KT >= 1 steps.
+// acc holds each 32x32 block transposed (the B fragment is the MFMA's first
+// operand): lane -> row lane % 32 of block mi, element j -> column (j / 4) * 8 +
+// (lane / 32) * 4 + j % 4 of block ni.
+template <int F, bool GU, class OA, class OB>
+__device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f32x16_t (&acc)[F][F]) {
+  constexpr int HALF = half_elems<F>();
+  constexpr int NI = 2 * F;  // DMA instructions per half-stage and wave
+  const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  FragAt<F, OA::COL> fa;
+  FragAt<F, OB::COL> fb;
+  fa.init(wm, wm * 32 * F);
+  fb.init(wn, block_col<F, GU>(wn, 0));
+#pragma unroll
+  for (int mi = 0; mi < F; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < F; ++ni)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
+  const int nh = 2 * KT;
+  KT = __builtin_amdgcn_readfirstlane(KT);
+#define MT_DST(SLOT, JJ) (lds_u32 + (uint32_t)(((SLOT) * HALF + (wave * NI + (JJ)) * 512) * 2))
+#define MT_ISSUE(J, JJ)                                             \
+  {                                                                 \
+    const int j_ = (J);                                             \
+    if (j_ & 1)                                                     \
+      ob.issue(j_ >> 1, (JJ), MT_DST(j_ % SLOTS, JJ));              \
+    else                                                            \
+      oa.issue(j_ >> 1, (JJ), MT_DST(j_ % SLOTS, JJ));              \
+  }
+#define MT_RA(SA, KS, I) fa.read((SA), (KS), (I), (I) * 32)
+#define MT_RB(SB, KS, I) fb.read((SB), (KS), (I), block_col<F, GU>(0, I))
+  bf16x8_t xa[F], xb[F], ya[F], yb[F];
+  // one 16-wide k sub-step: per block row mi, read part of the next sub-step's
+  // fragments (B first), run F MFMAs, issue one DMA instruction
+#define MT_SUB(FA, FB, NA, NB, SA, SB, KS, RD, DO, J, J0)                                                     \
+  _Pragma("unroll") for (int mi = 0; mi < F; ++mi) {                                                          \
+    if (RD) {                                                                                                 \
+      if (mi < F / 2) {                                                                                       \
+        NB[2 * mi] = MT_RB(SB, KS, 2 * mi);                                                                   \
+        NB[2 * mi + 1] = MT_RB(SB, KS, 2 * mi + 1);                                                           \
+      } else {                                                                                                \
+        NA[2 * mi - F] = MT_RA(SA, KS, 2 * mi - F);                                                           \
+        NA[2 * mi - F + 1] = MT_RA(SA, KS, 2 * mi - F + 1);                                                   \
+      }                                                                                                       \
+    }                                                                                                         \
+    _Pragma("unroll") for (int ni = 0; ni < F; ++ni)                                                          \
+      acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(FB[ni], FA[mi], acc[mi][ni], 0, 0, 0);            \
+    if (DO) MT_ISSUE(J, (J0) + mi)                                                                            \
+    __builtin_amdgcn_sched_barrier(0);                                                                        \
+  }
+  for (int j = 0; j < SLOTS && j < nh; ++j) {
+    if (j & 1)
+      ob.begin(j >> 1);
+    else
+      oa.begin(j >> 1);
+#pragma unroll
+    for (int jj = 0; jj < NI; ++jj) MT_ISSUE(j, jj)
+  }
+  {
+    const int after = min(SLOTS, nh) - 2;  // half-stages that may still be in flight
+    if (after >= 3)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * NI) : "memory");
+    else if (after == 2)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NI) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < F; ++i) {
+    xa[i] = MT_RA(lds, 0, i);
+    xb[i] = MT_RB(lds + HALF, 0, i);
+  }
+  // One K step kt.  B1: issue the second half of B_kt+1; A2: issue A_kt+2;
+  // MORE: a step follows; B2: issue the first half of B_kt+2.
+#define MT_STEP(KT_, B1, A2, MORE, B2)                                                                        \
+  {                                                                                                           \
+    const int kt_ = (KT_);                                                                                    \
+    int o0 = ((2 * kt_) % SLOTS) * HALF, o1 = ((2 * kt_ + 1) % SLOTS) * HALF;                                 \
+    int o2 = ((2 * kt_ + 2) % SLOTS) * HALF, o3 = ((2 * kt_ + 3) % SLOTS) * HALF;                             \
+    /* opaque: the fragment addresses of every slot would otherwise be held */                                \
+    asm volatile("" : "+s"(o0), "+s"(o1), "+s"(o2), "+s"(o3));                                                \
+    const uint16_t* sa = lds + o0;                                                                            \
+    const uint16_t* sb = lds + o1;                                                                            \
+    MT_SUB(xa, xb, ya, yb, sa, sb, 1, true, B1, 2 * kt_ + 3, F)                                               \
+    if (A2) oa.begin(kt_ + 2);                                                                                \
+    MT_SUB(ya, yb, xa, xb, sa, sb, 2, true, A2, 2 * kt_ + 4, 0)                                               \
+    MT_SUB(xa, xb, ya, yb, sa, sb, 3, true, A2, 2 * kt_ + 4, F)                                               \
+    if (MORE) {                                                                                               \
+      /* A_kt+2 is the only half-stage issued after B_kt+1; lgkmcnt(0): this                                  \
+         wave's reads of step kt are done before any wave refills its slots */                                \
+      if (B2)                                                                                                 \
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(NI) : "memory");                                  \
+      else                                                                                                    \
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");                                           \
+      __builtin_amdgcn_s_barrier();                                                                           \
+      asm volatile("" ::: "memory");                                                                          \
+    }                                                                                                         \
+    const uint16_t* na = lds + o2;                                                                            \
+    const uint16_t* nb = lds + o3;                                                                            \
+    if (B2) ob.begin(kt_ + 2);                                                                                \
+    MT_SUB(ya, yb, xa, xb, na, nb, 0, MORE, B2, 2 * kt_ + 5, 0)                                               \
+  }
+  if (KT >= 4) {
+    MT_STEP(0, false, false, true, true)
+    for (int kt = 1; kt + 2 < KT; ++kt) MT_STEP(kt, true, true, true, true)
+    MT_STEP(KT - 2, true, false, true, false)
+    MT_STEP(KT - 1, false, false, false, false)
+  } else {
+    for (int kt = 0; kt < KT; ++kt)
+      MT_STEP(kt, kt >= 1 && kt + 1 < KT, kt >= 1 && kt + 2 < KT, kt + 1 < KT, kt + 2 < KT)
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#undef MT_STEP
+#undef MT_SUB
+#undef MT_RA
+#undef MT_RB
+#undef MT_ISSUE
+#undef MT_DST
+}
+
+// After the K loop: the tile leaves the accumulators through LDS as fp32, 128
+// rows at a time, and store(row, col, v) gets 8 adjacent columns of a row; with
+// GU, store(row, col, gate, up) gets the matching 8 columns of both halves.
+// 16-byte chunks are XORed with the row, so the writes (32 rows, one chunk) and
+// the reads (one row, consecutive chunks) are both free of bank conflicts.
+template <int F, bool GU, class Store>
+__device__ __forceinline__ void drain(uint16_t* lds, const f32x16_t (&acc)[F][F], Store store) {
+  constexpr int B = 64 * F;
+  float* st = reinterpret_cast<float*>(lds);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int fr = lane & 31, fh = lane >> 5;
+#pragma unroll
+  for (int rd = 0; rd < F / 2; ++rd) {
+    __syncthreads();
+#pragma unroll
+    for (int m2 = 0; m2 < 2; ++m2) {
+      const int row = wm * 64 + m2 * 32 + fr;
+#pragma unroll
+      for (int ni = 0; ni < F; ++ni)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c4 = (block_col<F, GU>(wn, ni) + q * 8 + fh * 4) / 4;
+          const f32x16_t& a = acc[2 * rd + m2][ni];
+          const f32x4_t v = {a[q * 4], a[q * 4 + 1], a[q * 4 + 2], a[q * 4 + 3]};
+          *reinterpret_cast<f32x4_t*>(st + row * B + ((c4 ^ (row & 15)) * 4)) = v;
+        }
+    }
+    __syncthreads();
+    constexpr int W = GU ? B / 2 : B;  // columns a row gives out
+    for (int c = tid; c < 128 * (W / 8); c += THREADS) {
+      const int row = c / (W / 8), col = (c % (W / 8)) * 8;
+      const int tr = (row >> 6) * 32 * F + rd * 64 + (row & 63);  // row of the tile
+      auto get = [&](int col_, float* v) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + row * B + (((col_ / 4 + h) ^ (row & 15)) * 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[h * 4 + i] = x[i];
+        }
+      };
+      float v[8];
+      get(col, v);
+      if constexpr (GU) {
+        float u[8];
+        get(col + B / 2, u);
+        store(tr, col, v, u);
+      } else {
+        store(tr, col, v);
+      }
+    }
+  }
+}
+
+// Eight values to memory in the storage type (each rounded once, to nearest even).
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_pack(v[0], v[1]), bf16x2_pack(v[2], v[3]), bf16x2_pack(v[4], v[5]),
+                                            bf16x2_pack(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// ---------------------------------------------------------------- fp32 tile
+//
+// The same products for fp32 storage: tile 64 x 64, 4 waves of one
+// v_mfma_f32_32x32x2_f32 block each, K steps of 16 staged through registers
+// into LDS as [k][m] (stride 68 floats).  a(r, k) / b(r, k) give the address
+// of 4 consecutive floats (along k for a row operand, along r for a column
+// operand) or null for zeros.
+constexpr int S_BM = 64, S_BK = 16, S_LD = 68;
+constexpr int S_FLOATS = 2 * S_BK * S_LD > 64 * 64 ? 2 * S_BK * S_LD : 64 * 64;
+
+template <bool CA, bool CB, class PA, class PB>
+__device__ __forceinline__ void k_loop_f32(float* lds, PA pa, PB pb, int K, f32x16_t& acc) {
+  float* As = lds;
+  float* Bs = lds + S_BK * S_LD;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  // 256 threads x 4 floats = 64 x 16: row operand thread -> (row tid / 4, k 4 (tid % 4)),
+  // column operand thread -> (k tid / 16, row 4 (tid % 16))
+  auto fetch = [&](auto p, bool col, int k0) {
+    const int r = col ? (tid & 15) * 4 : tid >> 2, k = k0 + (col ? tid >> 4 : (tid & 3) * 4);
+    const float* q = k < K ? p(r, k) : nullptr;
+    return q ? *reinterpret_cast<const float4*>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  auto put = [&](float* s, bool col, float4 v) {
+    if (col) {
+      *reinterpret_cast<float4*>(s + (tid >> 4) * S_LD + (tid & 15) * 4) = v;
+    } else {
+      float* q = s + (tid & 3) * 4 * S_LD + (tid >> 2);
+      q[0] = v.x, q[S_LD] = v.y, q[2 * S_LD] = v.z, q[3 * S_LD] = v.w;
+    }
+  };
+  float4 ra = fetch(pa, CA, 0), rb = fetch(pb, CB, 0);
+  for (int k0 = 0; k0 < K; k0 += S_BK) {
+    __syncthreads();
+    put(As, CA, ra);
+    put(Bs, CB, rb);
+    __syncthreads();
+    if (k0 + S_BK < K) {
+      ra = fetch(pa, CA, k0 + S_BK);
+      rb = fetch(pb, CB, k0 + S_BK);
+    }
+#pragma unroll
+    for (int k = 0; k < S_BK; k += 2) {
+      const float a = As[(k + (lane >> 5)) * S_LD + wm * 32 + (lane & 31)];
+      const float b = Bs[(k + (lane >> 5)) * S_LD + wn * 32 + (lane & 31)];
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a, acc, 0, 0, 0);
+    }
+  }
+}
+
+template <bool GU, class Store>
+__device__ __forceinline__ void drain_f32(float* st, const f32x16_t& acc, Store store) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = (wave >> 1) * 32 + (lane & 31);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int c4 = ((wave & 1) * 32 + q * 8 + (lane >> 5) * 4) / 4;
+    const f32x4_t v = {acc[q * 4], acc[q * 4 + 1], acc[q * 4 + 2], acc[q * 4 + 3]};
+    *reinterpret_cast<f32x4_t*>(st + row * 64 + ((c4 ^ (row & 15)) * 4)) = v;
+  }
+  __syncthreads();
+  constexpr int W = GU ? 32 : 64;
+  for (int c = tid; c < 64 * (W / 8); c += THREADS) {
+    const int r = c / (W / 8), col = (c % (W / 8)) * 8;
+    auto get = [&](int col_, float* v) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + r * 64 + (((col_ / 4 + h) ^ (r & 15)) * 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[h * 4 + i] = x[i];
+      }
+    };
+    float v[8];
+    get(col, v);
+    if constexpr (GU) {
+      float u[8];
+      get(col + 32, u);
+      store(r, col, v, u);
+    } else {
+      store(r, col, v);
+    }
+  }
+}
+
+}  // namespace mt

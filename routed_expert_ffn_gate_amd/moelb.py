@@ -45,6 +45,10 @@ SIGNATURES = {
     "moelb_grouped_ffn": (_I, [_P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _SZ, _P, _P]),
     "moelb_grouped_ffn_stages": (_I, [_I, _P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _SZ, _P,
                                       _P]),
+    "moelb_grouped_ffn_train": (_I, [_P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _SZ, _P, _P, _P]),
+    "moelb_grouped_ffn_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moelb_grouped_ffn_backward": (_I, [_P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _SZ,
+                                        _P, _P, _P, _P]),
     "moelb_combine": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
     "moelb_pack_weights": (_I, [_P, _I, _I, _I, _I, _P, _P]),
 }
@@ -266,6 +270,56 @@ def moelb_grouped_ffn_stages(stages, x, rows, group_off, E, w13, w2, ws, y, G=1,
                                           _p(gather), gather_k, d, inter, dtype_code(x), _p(w13), _p(w2), _p(ws),
                                           ws.numel() * ws.element_size(), _p(y), _stream(stream)),
            "moelb_grouped_ffn_stages")
+
+
+def _check_shapes(name, *pairs):
+    """Each (tensor, shape, dtype) as the entry point addresses it; None is skipped."""
+    for what, t, shape, dtype in pairs:
+        if t is None:
+            continue
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+            raise MoelbError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+
+
+def _check_ffn(name, x, rows, group_off, E, w13, w2, gather, extra):
+    d, inter = x.shape[1], w2.shape[-1]
+    _check_shapes(name, ("w13", w13.reshape(-1, *w13.shape[-2:]), (E, 2 * inter, d), x.dtype),
+                  ("w2", w2.reshape(-1, *w2.shape[-2:]), (E, d, inter), x.dtype),
+                  ("group_off", group_off, (group_off.numel(),), torch.int32), *extra)
+    if gather is not None and (gather.dtype != torch.int32 or gather.numel() < rows):
+        raise MoelbError(f"{name}: gather holds {gather.numel()} {gather.dtype}, not {rows} int32")
+    if gather is None and rows > x.shape[0]:
+        raise MoelbError(f"{name}: {rows} rows of {x.shape[0]} without a gather")
+    return d, inter
+
+
+def moelb_grouped_ffn_train(x, rows, group_off, E, w13, w2, ws, z, y, G=1, rank=-1, gather=None, gather_k=1,
+                            stream=None):
+    """The grouped FFN keeping its projections: z [rows, 2*inter] fp32, y [rows, d]."""
+    name = "moelb_grouped_ffn_train"
+    d, inter = _check_ffn(name, x, rows, group_off, E, w13, w2, gather,
+                          (("z", z, (rows, 2 * w2.shape[-1]), torch.float32), ("y", y, (rows, x.shape[1]), x.dtype)))
+    _check(lib().moelb_grouped_ffn_train(_p(x), x.shape[0], rows, _p(group_off), group_off.numel() - 1, E, G, rank,
+                                         _p(gather), gather_k, d, inter, dtype_code(x), _p(w13), _p(w2), _p(ws),
+                                         ws.numel() * ws.element_size(), _p(z), _p(y), _stream(stream)), name)
+
+
+def moelb_grouped_ffn_backward_workspace_bytes(rows, num_groups, E, d, inter, dtype) -> int:
+    return int(lib().moelb_grouped_ffn_backward_workspace_bytes(rows, num_groups, E, d, inter, dtype))
+
+
+def moelb_grouped_ffn_backward(dy, x, rows, group_off, E, w13, w2, z, ws, dx=None, dw13=None, dw2=None, G=1, rank=-1,
+                               gather=None, gather_k=1, stream=None):
+    """Gradients of moelb_grouped_ffn_train's y: dx [rows, d], dw13 and dw2 as the weights (None: not computed)."""
+    name = "moelb_grouped_ffn_backward"
+    d, inter = _check_ffn(name, x, rows, group_off, E, w13, w2, gather,
+                          (("z", z, (rows, 2 * w2.shape[-1]), torch.float32), ("dy", dy, (rows, x.shape[1]), x.dtype),
+                           ("dx", dx, (rows, x.shape[1]), x.dtype), ("dw13", dw13, w13.shape, x.dtype),
+                           ("dw2", dw2, w2.shape, x.dtype)))
+    _check(lib().moelb_grouped_ffn_backward(_p(dy), _p(x), x.shape[0], rows, _p(group_off), group_off.numel() - 1, E,
+                                            G, rank, _p(gather), gather_k, d, inter, dtype_code(x), _p(w13), _p(w2),
+                                            _p(z), _p(ws), ws.numel() * ws.element_size(), _p(dx), _p(dw13), _p(dw2),
+                                            _stream(stream)), name)
 
 
 def moelb_combine(y, pos, wts, out, shared=None, stream=None):

@@ -17,6 +17,7 @@ struct FfnSched {
   int32_t* rowmap;    // [rows] physical row of each virtual row
   int32_t* asrc;      // [rows] row of x the gate/up GEMM reads for each virtual row
   void* amid;         // [rows][inter] SwiGLU activations, virtual row order
+  int32_t* order;     // [E] experts by rows, most first (ties: lower id), or null: not wanted
   int wpacked;        // W13 and W2 in the packed layout (moelb_pack_weights)
 };
 
@@ -47,11 +48,26 @@ inline size_t sched_layout(int rows, int num_groups, int E, int inter, int dtype
     s->rowmap = reinterpret_cast<int32_t*>(p_rm);
     s->asrc = reinterpret_cast<int32_t*>(p_as);
     s->amid = p_am;
+    s->order = nullptr;
   }
   return off;
 }
 
 // ---------------------------------------------------------------- schedule
+
+// Experts by their rows (eoff in LDS), most first: each thread counts the
+// experts before its own.
+__device__ __forceinline__ void write_order(const int* eoff, int E, int32_t* order) {
+  const int e = threadIdx.x;
+  if (e >= E) return;
+  const int n = eoff[e + 1] - eoff[e];
+  int before = 0;
+  for (int f = 0; f < E; ++f) {
+    const int m = eoff[f + 1] - eoff[f];
+    before += m > n || (m == n && f < e);
+  }
+  order[before] = e;
+}
 
 // Expert-major virtual row order: every selected group of expert e gets a
 // contiguous range inside e's range [eoff[e], eoff[e+1]); M tiles of BM rows
@@ -133,6 +149,7 @@ __global__ __launch_bounds__(256) void sched_kernel(const int32_t* __restrict__ 
     }
   }
   if (e == 0) s.eoff[E] = eoff[E];
+  if (s.order) write_order(eoff, E, s.order);
 }
 
 // Inclusive prefix of v over the 256 threads of a workgroup (4 waves):
@@ -222,6 +239,7 @@ __global__ __launch_bounds__(256) void sched_rowmap_kernel(const int32_t* __rest
       s.mt_e[i] = lo;
       s.mt_v0[i] = eoff[lo] + (i - toff[lo]) * BM;
     }
+    if (s.order) write_order(eoff, E, s.order);
   }
   const int v = blockIdx.x * blockDim.x + tid;
   if (v >= eoff[E]) return;
@@ -281,9 +299,8 @@ __global__ __launch_bounds__(256) void rowmap_kernel(const int32_t* __restrict__
 
 // XCD-aware tile id: workgroups go round-robin over 8 XCDs; give each XCD a
 // contiguous range of tiles.  Returns -1 for workgroups with no tile.
-__device__ __forceinline__ int xcd_tile(int total) {
+__device__ __forceinline__ int xcd_tile(int bid, int total) {
   const int per = (total + 7) / 8;
-  const int bid = blockIdx.x;
   const int t = (bid & 7) * per + (bid >> 3);
   return ((bid >> 3) < per && t < total) ? t : -1;
 }

@@ -47,6 +47,7 @@ struct TrainArgs {
   T* out;      // y or dx, physical rows; dW13 or dW2
   float* part; // weight gradients: [splits][E][M][N] partial sums
   int splits;
+  int chunks;  // weight gradients: units an expert's tiles are cut into
   int rows, d, inter, E, ntn, ntm;
   FfnSched s;
 };
@@ -92,12 +93,11 @@ __device__ __forceinline__ void put_da(const TrainArgs<T>& p, int v, int n, cons
 
 // ---------------------------------------------------------------- row-tiled products
 
+// Workgroup `block` of the product OP.
 template <int F, int OP>
-__global__ __launch_bounds__(mt::THREADS) void train_rows_kernel(TrainArgs<uint16_t> p) {
-  extern __shared__ __align__(16) char smem[];
-  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+__device__ __forceinline__ void rows_tile(const TrainArgs<uint16_t>& p, int block, uint16_t* lds) {
   const int n_mtiles = *p.s.n_mtiles;
-  const int tile = xcd_tile(n_mtiles * p.ntn);
+  const int tile = xcd_tile(block, n_mtiles * p.ntn);
   if (tile < 0) return;
   int mti, nt;
   grouped_tile(tile, n_mtiles, p.ntn, mti, nt);
@@ -153,10 +153,9 @@ __global__ __launch_bounds__(mt::THREADS) void train_rows_kernel(TrainArgs<uint1
 }
 
 template <int OP>
-__global__ __launch_bounds__(mt::THREADS) void train_rows_f32_kernel(TrainArgs<float> p) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
+__device__ __forceinline__ void rows_tile(const TrainArgs<float>& p, int block, float* lds) {
   const int n_mtiles = *p.s.n_mtiles;
-  const int tile = xcd_tile(n_mtiles * p.ntn);
+  const int tile = xcd_tile(block, n_mtiles * p.ntn);
   if (tile < 0) return;
   const int mti = tile / p.ntn, nt = tile % p.ntn;
   const int e = p.s.mt_e[mti], v0 = p.s.mt_v0[mti], vend = p.s.eoff[e + 1];
@@ -202,26 +201,34 @@ __global__ __launch_bounds__(mt::THREADS) void train_rows_f32_kernel(TrainArgs<f
 
 // ---------------------------------------------------------------- weight gradients
 
-// Tile t -> expert, split of its rows, tile of its gradient.
+// Workgroup -> expert, split of its rows, tile of its gradient.  An expert's
+// tiles are cut into `chunks` units; the units, most rows first, go to the 8
+// XCDs in turn, and the workgroups of an XCD (every eighth) take its units one
+// after another.  So the tiles running at once on an XCD share an expert's
+// rows in its L2, and however uneven the experts are (all rows on a few of
+// them included) the XCDs get like amounts of work.
 struct WTile {
-  int e, mi, ni, split, k0, n, v0;
+  int e, mi, ni, split, n, v0;
 };
 template <typename T>
-__device__ __forceinline__ bool w_tile(const TrainArgs<T>& p, WTile& w) {
+__device__ __forceinline__ bool w_tile(const TrainArgs<T>& p, int block, WTile& w) {
   const int per = p.ntm * p.ntn * p.splits;
-  int t = xcd_tile(p.E * per);
-  if (t < 0) return false;
-  w.e = t / per;
-  t -= w.e * per;
+  const int u = (per + p.chunks - 1) / p.chunks;
+  const int j = block >> 3;
+  const int unit = (j / u) * 8 + (block & 7);
+  if (unit >= p.E * p.chunks) return false;
+  int t = (unit % p.chunks) * u + j % u;
+  if (t >= per) return false;
+  w.e = p.s.order[unit / p.chunks];
   w.split = t / (p.ntm * p.ntn);
   t -= w.split * p.ntm * p.ntn;
   grouped_tile(t, p.ntm, p.ntn, w.mi, w.ni);
   const int vb = p.s.eoff[w.e], n = p.s.eoff[w.e + 1] - vb;
   const int steps = (n + mt::BK - 1) / mt::BK;
   const int ps = (steps + p.splits - 1) / p.splits * mt::BK;  // rows of a split
-  w.k0 = min(n, w.split * ps);
-  w.n = min(n, w.k0 + ps) - w.k0;
-  w.v0 = vb + w.k0;
+  const int k0 = min(n, w.split * ps);
+  w.n = min(n, k0 + ps) - k0;
+  w.v0 = vb + k0;
   return true;
 }
 
@@ -236,16 +243,26 @@ __device__ __forceinline__ void put_w(const TrainArgs<T>& p, const WTile& w, int
     mt::store8(p.out + at, v);
 }
 
+// A tile of B x B zeros, for an expert (or a split) without rows.
+template <int B, typename T>
+__device__ __forceinline__ void zero_w(const TrainArgs<T>& p, const WTile& w, int M, int N) {
+  const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int c = threadIdx.x; c < B * (B / 8); c += mt::THREADS)
+    put_w(p, w, M, N, w.mi * B + c / (B / 8), w.ni * B + (c % (B / 8)) * 8, v);
+}
+
 template <int F, int OP>
-__global__ __launch_bounds__(mt::THREADS) void train_weights_kernel(TrainArgs<uint16_t> p) {
-  extern __shared__ __align__(16) char smem[];
-  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+__device__ __forceinline__ void weights_tile(const TrainArgs<uint16_t>& p, int block, uint16_t* lds) {
   WTile w;
-  if (!w_tile(p, w)) return;
+  if (!w_tile(p, block, w)) return;
   const int d = p.d, I = p.inter;
   const int M = OP == OP_DW13 ? 2 * I : d, N = OP == OP_DW13 ? d : I;
+  if (w.n == 0) {
+    zero_w<64 * F>(p, w, M, N);
+    return;
+  }
   const int m0 = w.mi * 64 * F, n0 = w.ni * 64 * F;
-  const int KT = max(1, (w.n + mt::BK - 1) / mt::BK);  // no rows: one step of zeros
+  const int KT = (w.n + mt::BK - 1) / mt::BK;
   f32x16_t acc[F][F];
   if constexpr (OP == OP_DW13) {
     mt::ColOp<F, false> oa;
@@ -264,12 +281,15 @@ __global__ __launch_bounds__(mt::THREADS) void train_weights_kernel(TrainArgs<ui
 }
 
 template <int OP>
-__global__ __launch_bounds__(mt::THREADS) void train_weights_f32_kernel(TrainArgs<float> p) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
+__device__ __forceinline__ void weights_tile(const TrainArgs<float>& p, int block, float* lds) {
   WTile w;
-  if (!w_tile(p, w)) return;
+  if (!w_tile(p, block, w)) return;
   const int d = p.d, I = p.inter;
   const int M = OP == OP_DW13 ? 2 * I : d, N = OP == OP_DW13 ? d : I;
+  if (w.n == 0) {
+    zero_w<mt::S_BM>(p, w, M, N);
+    return;
+  }
   const int m0 = w.mi * 64, n0 = w.ni * 64;
   f32x16_t acc;
   auto pa = [&](int r, int k) -> const float* {
@@ -284,6 +304,50 @@ __global__ __launch_bounds__(mt::THREADS) void train_weights_f32_kernel(TrainArg
   };
   mt::k_loop_f32<true, true>(lds, pa, pb, w.n, acc);
   mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) { put_w(p, w, M, N, m0 + r, n0 + c, v); });
+}
+
+// ---------------------------------------------------------------- kernels
+
+template <int F, int OP>
+__global__ __launch_bounds__(mt::THREADS) void train_rows_kernel(TrainArgs<uint16_t> p) {
+  extern __shared__ __align__(16) char smem[];
+  rows_tile<F, OP>(p, blockIdx.x, reinterpret_cast<uint16_t*>(smem));
+}
+template <int OP>
+__global__ __launch_bounds__(mt::THREADS) void train_rows_f32_kernel(TrainArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::S_FLOATS];
+  rows_tile<OP>(p, blockIdx.x, lds);
+}
+
+// dW13, dW2 and dx all follow from [dg, du], a and dy: one launch, so the last
+// round of one product's tiles runs beside the next product's.  Each block
+// range starts at a multiple of 8 (the XCD of a block is its id mod 8).
+template <typename T>
+struct GradArgs {
+  TrainArgs<T> w13, w2, x;
+  int n13, n2;  // blocks of the first two
+};
+template <int F>
+__global__ __launch_bounds__(mt::THREADS) void train_grads_kernel(GradArgs<uint16_t> g) {
+  extern __shared__ __align__(16) char smem[];
+  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+  const int b = blockIdx.x;
+  if (b < g.n13)
+    weights_tile<F, OP_DW13>(g.w13, b, lds);
+  else if (b < g.n13 + g.n2)
+    weights_tile<F, OP_DW2>(g.w2, b - g.n13, lds);
+  else
+    rows_tile<F, OP_DX>(g.x, b - g.n13 - g.n2, lds);
+}
+__global__ __launch_bounds__(mt::THREADS) void train_grads_f32_kernel(GradArgs<float> g) {
+  __shared__ __align__(16) float lds[mt::S_FLOATS];
+  const int b = blockIdx.x;
+  if (b < g.n13)
+    weights_tile<OP_DW13>(g.w13, b, lds);
+  else if (b < g.n13 + g.n2)
+    weights_tile<OP_DW2>(g.w2, b - g.n13, lds);
+  else
+    rows_tile<OP_DX>(g.x, b - g.n13 - g.n2, lds);
 }
 
 // out[i] = sum over splits, in order, of part[s][i]; 8 values per thread.
@@ -305,20 +369,18 @@ __global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict
 
 // ---------------------------------------------------------------- host
 
-// Row tile of a call (64 F, or 64 for fp32): 256 rows where the experts
-// average enough of them and the tiles still cover the compute units.
-int row_f(int rows, int E, int d, int inter) {
+// Tile height of a call (64 F, or 64 for fp32): 256 where the experts average
+// enough rows and the tiles still cover the compute units.
+int tile_rows(int rows, int E, int d, int inter, int dtype) {
+  if (dtype != MOELB_BF16) return mt::S_BM;
   const int least = d < inter ? d : inter;
   const size_t tiles = (size_t)(rows + 255) / 256 * ((least + 255) / 256);
-  return (size_t)rows >= (size_t)192 * E && tiles >= 192 ? 4 : 2;
+  return (size_t)rows >= (size_t)192 * E && tiles >= 192 ? 256 : 128;
 }
-
-int weight_f(int E, int M, int N) { return (size_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= 64 ? 4 : 2; }
 
 // Parts the rows of every expert are cut into for the weight gradients: enough
 // workgroups for the compute units, at least 512 rows each on average.
-int weight_splits(int rows, int E, int M, int N, int dtype) {
-  const int b = dtype == MOELB_BF16 ? 64 * weight_f(E, M, N) : mt::S_BM;
+int weight_splits(int rows, int E, int M, int N, int b) {
   const int slots = b == 256 ? 256 : 512;
   const size_t tiles = (size_t)E * ((M + b - 1) / b) * ((N + b - 1) / b);
   const size_t want = slots / tiles, most = (size_t)rows / E / 512;
@@ -327,26 +389,46 @@ int weight_splits(int rows, int E, int M, int N, int dtype) {
 }
 
 struct BackLayout {
-  size_t dz, part, total;
+  size_t order, dz, part13, part2, total;
 };
 BackLayout back_layout(int rows, int num_groups, int E, int d, int inter, int dtype) {
   BackLayout l;
   const size_t eb = moelb_elem_bytes(dtype);
-  l.dz = sched_layout(rows, num_groups, E, inter, dtype, nullptr, nullptr);  // schedule tables and a
-  l.part = l.dz + moelb_align256((size_t)rows * 2 * inter * eb);
-  const size_t s13 = weight_splits(rows, E, 2 * inter, d, dtype), s2 = weight_splits(rows, E, d, inter, dtype);
-  const size_t p13 = s13 > 1 ? s13 * E * 2 * inter * d * 4 : 0, p2 = s2 > 1 ? s2 * E * inter * d * 4 : 0;
-  l.total = l.part + moelb_align256(p13 > p2 ? p13 : p2);
+  const int tile = tile_rows(rows, E, d, inter, dtype);
+  l.order = sched_layout(rows, num_groups, E, inter, dtype, nullptr, nullptr);  // schedule tables and a
+  l.dz = l.order + moelb_align256((size_t)E * 4);
+  l.part13 = l.dz + moelb_align256((size_t)rows * 2 * inter * eb);
+  const size_t s13 = weight_splits(rows, E, 2 * inter, d, tile), s2 = weight_splits(rows, E, d, inter, tile);
+  l.part2 = l.part13 + (s13 > 1 ? moelb_align256(s13 * E * 2 * inter * d * 4) : 0);
+  l.total = l.part2 + (s2 > 1 ? moelb_align256(s2 * E * inter * d * 4) : 0);
   return l;
+}
+
+// Blocks of a row-tiled product; sets its column tiles.
+template <typename T>
+size_t rows_grid(TrainArgs<T>& p, int BM, int bn, int N) {
+  p.ntn = (N + bn - 1) / bn;
+  return ((size_t)(p.rows + BM - 1) / BM + p.E) * p.ntn + 8;
+}
+
+// Blocks of a weight gradient; sets its tiles, splits and units: about 32
+// tiles a unit (the compute units of an XCD), at least 32 units in all.
+template <typename T>
+size_t weights_grid(TrainArgs<T>& p, int BM, int M, int N) {
+  p.splits = weight_splits(p.rows, p.E, M, N, BM);
+  p.ntm = (M + BM - 1) / BM;
+  p.ntn = (N + BM - 1) / BM;
+  const int per = p.ntm * p.ntn * p.splits;
+  const int c = per / 32, least = (32 + p.E - 1) / p.E;
+  p.chunks = c > least ? c : least;
+  if (p.chunks > per) p.chunks = per;
+  const int u = (per + p.chunks - 1) / p.chunks;
+  return (size_t)((p.E * p.chunks + 7) / 8) * 8 * u;
 }
 
 template <typename T, int OP>
 int launch_rows(TrainArgs<T> p, int BM, hipStream_t s) {
-  if (p.rows == 0) return MOELB_OK;
-  const int bn = OP == OP_UP ? BM / 2 : BM;
-  const int N = (OP == OP_UP || OP == OP_DA) ? p.inter : p.d;
-  p.ntn = (N + bn - 1) / bn;
-  const size_t grid = ((size_t)(p.rows + BM - 1) / BM + p.E) * p.ntn + 8;
+  const size_t grid = rows_grid(p, BM, OP == OP_UP ? BM / 2 : BM, (OP == OP_UP || OP == OP_DA) ? p.inter : p.d);
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
   if constexpr (sizeof(T) == 4) {
     hipLaunchKernelGGL((train_rows_f32_kernel<OP>), dim3((unsigned)grid), dim3(mt::THREADS), 0, s, p);
@@ -361,35 +443,12 @@ int launch_rows(TrainArgs<T> p, int BM, hipStream_t s) {
   return MOELB_OK;
 }
 
-template <typename T, int OP>
-int launch_weights(TrainArgs<T> p, T* out, hipStream_t s) {
-  const int M = OP == OP_DW13 ? 2 * p.inter : p.d, N = OP == OP_DW13 ? p.d : p.inter;
-  const int dtype = sizeof(T) == 4 ? MOELB_F32 : MOELB_BF16;
-  const int b = sizeof(T) == 4 ? mt::S_BM : 64 * weight_f(p.E, M, N);
-  p.out = out;
-  p.splits = weight_splits(p.rows, p.E, M, N, dtype);
-  p.ntm = (M + b - 1) / b;
-  p.ntn = (N + b - 1) / b;
-  const size_t grid = (size_t)p.E * p.ntm * p.ntn * p.splits + 8;
-  if (grid > 0x7fffffffull) return MOELB_EINVAL;
-  if constexpr (sizeof(T) == 4) {
-    hipLaunchKernelGGL((train_weights_f32_kernel<OP>), dim3((unsigned)grid), dim3(mt::THREADS), 0, s, p);
-  } else if (b == 256) {
-    if (!moelb_allow_lds(train_weights_kernel<4, OP>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL((train_weights_kernel<4, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<4>(), s,
-                       p);
-  } else {
-    if (!moelb_allow_lds(train_weights_kernel<2, OP>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL((train_weights_kernel<2, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<2>(), s,
-                       p);
-  }
+template <typename T>
+int launch_sum(const TrainArgs<T>& p, int M, int N, hipStream_t s) {
+  const size_t n8 = (size_t)p.E * M * N / 8;
+  hipLaunchKernelGGL((sum_splits_kernel<T>), dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, p.part, p.splits, n8,
+                     p.out);
   MOELB_CHECK_LAUNCH();
-  if (p.splits > 1) {
-    const size_t n8 = (size_t)p.E * M * N / 8;
-    hipLaunchKernelGGL((sum_splits_kernel<T>), dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, p.part, p.splits,
-                       n8, out);
-    MOELB_CHECK_LAUNCH();
-  }
   return MOELB_OK;
 }
 
@@ -415,15 +474,37 @@ int run_forward(TrainArgs<T> p, int BM, hipStream_t s) {
 }
 
 template <typename T>
-int run_backward(TrainArgs<T> p, int BM, T* dx, T* dw13, T* dw2, hipStream_t s) {
-  int st = launch_rows<T, OP_DA>(p, BM, s);
-  if (st == MOELB_OK && dx) {
-    p.out = dx;
-    st = launch_rows<T, OP_DX>(p, BM, s);
+int run_backward(TrainArgs<T> p, int BM, T* dx, T* dw13, T* dw2, float* part2, hipStream_t s) {
+  if (p.rows > 0) {
+    const int st = launch_rows<T, OP_DA>(p, BM, s);
+    if (st != MOELB_OK) return st;
   }
-  if (st == MOELB_OK && dw13) st = launch_weights<T, OP_DW13>(p, dw13, s);
-  if (st == MOELB_OK && dw2) st = launch_weights<T, OP_DW2>(p, dw2, s);
-  return st;
+  GradArgs<T> g = {p, p, p, 0, 0};
+  size_t n13 = 0, n2 = 0, nx = 0;
+  g.w13.out = dw13, g.w2.out = dw2, g.x.out = dx;
+  g.w2.part = part2;
+  if (dw13) n13 = weights_grid(g.w13, BM, 2 * p.inter, p.d);
+  if (dw2) n2 = weights_grid(g.w2, BM, p.d, p.inter);
+  if (dx && p.rows > 0) nx = rows_grid(g.x, BM, BM, p.d);
+  const size_t grid = n13 + n2 + nx;
+  if (grid > 0x7fffffffull) return MOELB_EINVAL;
+  if (grid == 0) return MOELB_OK;
+  g.n13 = (int)n13, g.n2 = (int)n2;
+  if constexpr (sizeof(T) == 4) {
+    hipLaunchKernelGGL(train_grads_f32_kernel, dim3((unsigned)grid), dim3(mt::THREADS), 0, s, g);
+  } else if (BM == 256) {
+    if (!moelb_allow_lds(train_grads_kernel<4>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_grads_kernel<4>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<4>(), s, g);
+  } else {
+    if (!moelb_allow_lds(train_grads_kernel<2>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_grads_kernel<2>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<2>(), s, g);
+  }
+  MOELB_CHECK_LAUNCH();
+  if (dw13 && g.w13.splits > 1) {
+    const int st = launch_sum(g.w13, 2 * p.inter, p.d, s);
+    if (st != MOELB_OK) return st;
+  }
+  return dw2 && g.w2.splits > 1 ? launch_sum(g.w2, p.d, p.inter, s) : MOELB_OK;
 }
 
 }  // namespace
@@ -442,7 +523,7 @@ extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, cons
   sched_layout(rows, num_groups, E, inter, dtype, &sc, static_cast<char*>(ws));
   sc.wpacked = 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int BM = dtype == MOELB_BF16 ? 64 * row_f(rows, E, d, inter) : mt::S_BM;
+  const int BM = tile_rows(rows, E, d, inter, dtype);
   const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, sc, s);
   if (st != MOELB_OK) return st;
   auto run = [&](auto* t) {
@@ -484,8 +565,9 @@ extern "C" int moelb_grouped_ffn_backward(const void* dy, const void* x, int row
   FfnSched sc;
   sched_layout(rows, num_groups, E, inter, dtype, &sc, base);
   sc.wpacked = 0;
+  sc.order = reinterpret_cast<int32_t*>(base + l.order);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int BM = dtype == MOELB_BF16 ? 64 * row_f(rows, E, d, inter) : mt::S_BM;
+  const int BM = tile_rows(rows, E, d, inter, dtype);
   const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, sc, s);
   if (st != MOELB_OK) return st;
   auto run = [&](auto* t) {
@@ -499,9 +581,10 @@ extern "C" int moelb_grouped_ffn_backward(const void* dy, const void* x, int row
     p.z = const_cast<float*>(z);
     p.a = static_cast<T*>(sc.amid);
     p.dz = reinterpret_cast<T*>(base + l.dz);
-    p.part = reinterpret_cast<float*>(base + l.part);
+    p.part = reinterpret_cast<float*>(base + l.part13);
     p.rows = rows, p.d = d, p.inter = inter, p.E = E, p.s = sc;
-    return run_backward<T>(p, BM, static_cast<T*>(dx), static_cast<T*>(dw13), static_cast<T*>(dw2), s);
+    return run_backward<T>(p, BM, static_cast<T*>(dx), static_cast<T*>(dw13), static_cast<T*>(dw2),
+                           reinterpret_cast<float*>(base + l.part2), s);
   };
   return dtype == MOELB_BF16 ? run(static_cast<uint16_t*>(nullptr)) : run(static_cast<float*>(nullptr));
 }

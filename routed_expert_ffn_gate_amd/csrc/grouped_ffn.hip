@@ -64,7 +64,7 @@ __global__ __launch_bounds__(MF_THREADS) void ffn_mfma_kernel(const uint16_t* __
                                                                int inter, int ntn, uint16_t* __restrict__ y) {
   extern __shared__ __align__(16) char smem[];
   const int n_mtiles = *s.n_mtiles;
-  const int tile = xcd_tile(n_mtiles * ntn);
+  const int tile = xcd_tile(blockIdx.x, n_mtiles * ntn);
   if (tile < 0) return;
   int mt, nt;
   grouped_tile(tile, n_mtiles, ntn, mt, nt);
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(MF_THREADS) void ffn_mfma_dma_kernel(const uint16_t
                                                                    uint16_t* __restrict__ y) {
   extern __shared__ __align__(16) char smem[];
   const int n_mtiles = *s.n_mtiles;
-  const int tile = xcd_tile(n_mtiles * ntn);
+  const int tile = xcd_tile(blockIdx.x, n_mtiles * ntn);
   if (tile < 0) return;
   int mt, nt;
   grouped_tile(tile, n_mtiles, ntn, mt, nt);
@@ -957,7 +957,7 @@ __global__ __launch_bounds__(MF_THREADS) void ffn_skinny_kernel(const uint16_t* 
                                                                 uint16_t* __restrict__ y) {
   extern __shared__ __align__(16) char smem[];
   const int n_mtiles = *s.n_mtiles;
-  const int tile = xcd_tile(n_mtiles * ntn);
+  const int tile = xcd_tile(blockIdx.x, n_mtiles * ntn);
   if (tile < 0) return;
   int mt, nt;
   grouped_tile(tile, n_mtiles, ntn, mt, nt);
@@ -1115,7 +1115,7 @@ __global__ __launch_bounds__(256) void ffn_simt_kernel(const float* __restrict__
   __shared__ float Bs[SF_BK][SF_BN + 1];
   __shared__ const float* arow[SF_BM];
   __shared__ const float* brow[SF_BN];
-  const int tile = xcd_tile(*s.n_mtiles * ntn);
+  const int tile = xcd_tile(blockIdx.x, *s.n_mtiles * ntn);
   if (tile < 0) return;
   const int mt = tile / ntn, nt = tile % ntn;
   const int e = s.mt_e[mt];

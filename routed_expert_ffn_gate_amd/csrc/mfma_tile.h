@@ -420,23 +420,23 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
 // ---------------------------------------------------------------- fp32 tile
 //
 // The same products for fp32 storage: tile 64 x 64, 4 waves of one
-// v_mfma_f32_32x32x2_f32 block each, K steps of 16 staged through registers
-// into LDS as [k][m] (stride 68 floats).  a(r, k) / b(r, k) give the address
-// of 4 consecutive floats (along k for a row operand, along r for a column
-// operand) or null for zeros.
-constexpr int S_BM = 64, S_BK = 16, S_LD = 68;
-constexpr int S_FLOATS = 2 * S_BK * S_LD > 64 * 64 ? 2 * S_BK * S_LD : 64 * 64;
+// v_mfma_f32_32x32x2_f32 block each.  K steps of 32 are loaded two ahead into
+// registers and written to one of two LDS buffers as [k][m] (stride 68
+// floats), so a step has one barrier.  a(r, k) / b(r, k) give the address of 4
+// consecutive floats (along k for a row operand, along r for a column operand)
+// or null for zeros.
+constexpr int S_BM = 64, S_BK = 32, S_LD = 68;
+constexpr int S_BUF = 2 * S_BK * S_LD;  // floats of one buffer: A, then B
+constexpr int S_FLOATS = 2 * S_BUF;     // 34 KiB; the epilogue stages 64 x 64 in it
 
 template <bool CA, bool CB, class PA, class PB>
 __device__ __forceinline__ void k_loop_f32(float* lds, PA pa, PB pb, int K, f32x16_t& acc) {
-  float* As = lds;
-  float* Bs = lds + S_BK * S_LD;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
 #pragma unroll
   for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  // 256 threads x 4 floats = 64 x 16: row operand thread -> (row tid / 4, k 4 (tid % 4)),
-  // column operand thread -> (k tid / 16, row 4 (tid % 16))
+  // 256 threads x 4 floats = 64 x 16, twice a step: row operand thread -> (row
+  // tid / 4, k 4 (tid % 4)), column operand thread -> (k tid / 16, row 4 (tid % 16))
   auto fetch = [&](auto p, bool col, int k0) {
     const int r = col ? (tid & 15) * 4 : tid >> 2, k = k0 + (col ? tid >> 4 : (tid & 3) * 4);
     const float* q = k < K ? p(r, k) : nullptr;
@@ -450,21 +450,37 @@ __device__ __forceinline__ void k_loop_f32(float* lds, PA pa, PB pb, int K, f32x
       q[0] = v.x, q[S_LD] = v.y, q[2 * S_LD] = v.z, q[3 * S_LD] = v.w;
     }
   };
-  float4 ra = fetch(pa, CA, 0), rb = fetch(pb, CB, 0);
-  for (int k0 = 0; k0 < K; k0 += S_BK) {
-    __syncthreads();
-    put(As, CA, ra);
-    put(Bs, CB, rb);
-    __syncthreads();
-    if (k0 + S_BK < K) {
-      ra = fetch(pa, CA, k0 + S_BK);
-      rb = fetch(pb, CB, k0 + S_BK);
-    }
+  float4 ra[2][2], rb[2][2];  // [step parity][half of the step]
 #pragma unroll
-    for (int k = 0; k < S_BK; k += 2) {
-      const float a = As[(k + (lane >> 5)) * S_LD + wm * 32 + (lane & 31)];
-      const float b = Bs[(k + (lane >> 5)) * S_LD + wn * 32 + (lane & 31)];
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a, acc, 0, 0, 0);
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ra[s][h] = fetch(pa, CA, s * S_BK + h * 16);
+      rb[s][h] = fetch(pb, CB, s * S_BK + h * 16);
+    }
+  for (int k0 = 0; k0 < K; k0 += 2 * S_BK) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      // buffer s: the reads of two steps ago are behind the last barrier
+      float* As = lds + s * S_BUF;
+      float* Bs = As + S_BK * S_LD;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        put(As + h * 16 * S_LD, CA, ra[s][h]);
+        put(Bs + h * 16 * S_LD, CB, rb[s][h]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ra[s][h] = fetch(pa, CA, k0 + (s + 2) * S_BK + h * 16);
+        rb[s][h] = fetch(pb, CB, k0 + (s + 2) * S_BK + h * 16);
+      }
+#pragma unroll
+      for (int k = 0; k < S_BK; k += 2) {
+        const float a = As[(k + (lane >> 5)) * S_LD + wm * 32 + (lane & 31)];
+        const float b = Bs[(k + (lane >> 5)) * S_LD + wn * 32 + (lane & 31)];
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a, acc, 0, 0, 0);
+      }
     }
   }
 }

@@ -21,7 +21,12 @@
  * for the FFN's weight streams (moelb_pack_weights).
  *
  * For training: the FFN's forward that keeps its projections and its gradients
- * (moelb_grouped_ffn_train, moelb_grouped_ffn_backward).
+ * (moelb_grouped_ffn_train, moelb_grouped_ffn_backward), and the gradients of
+ * the combine (moelb_combine_backward) and of the router
+ * (moelb_gate_backward).
+ *
+ * For serving requests with adapters of their own: a shared projection with
+ * low-rank adapters beside it (moelb_adapter_projection).
  *
  * Conventions for every entry point:
  *  - Plain C ABI.  Every pointer argument is DEVICE memory owned by the caller
@@ -508,6 +513,78 @@ int moelb_grouped_ffn_backward(const void* dy, const void* x, int rows_x, int ro
  */
 int moelb_combine(const void* y, int rows_y, const int32_t* pos, const float* wts, int T, int k,
                   int d, int dtype, const void* shared, void* out, void* stream);
+
+/*
+ * Gradients of moelb_combine, for dout the gradient of its out:
+ *   dy[pos[t*k+j]] = wts[t,j] * dout[t]            (rounded to dtype once)
+ *   dwts[t,j]      = <dout[t], y[pos[t*k+j]]>      (fp32; 0 for a left-out pair)
+ * The gradient of `shared` is dout itself.
+ *  dout   [T,d] dtype
+ *  y      [rows_y,d] dtype, pos [T*k] int32, wts [T*k] fp32: the forward's
+ *  dy     [rows_y,d] dtype out: rows that no pair names are not written
+ *  dwts   [T*k] fp32 out
+ * Pairs with pos < 0 or pos >= rows_y are left out.  The named rows must be
+ * distinct, as moelb_permute's are: of several pairs naming one row, its dy
+ * holds one's share (all memory safe).  dy must not overlap the inputs.
+ * Same requirements as moelb_combine.
+ */
+int moelb_combine_backward(const void* dout, const void* y, int rows_y, const int32_t* pos,
+                           const float* wts, int T, int k, int d, int dtype, void* dy, float* dwts,
+                           void* stream);
+
+/*
+ * Gradients of moelb_gate_topk's weights (the current router; idx and gap have
+ * none), for dwts the gradient of its wts:
+ *   p = softmax(h[t] . w^T + b), q_e = sum of dwts[t,j] over the j with
+ *   idx[t,j] = e, dz_e = p_e (q_e - sum_f p_f q_f)
+ *   dh[t] = dz . w, dw[e] = sum_t dz_e h[t], db[e] = sum_t dz_e
+ * The logits are formed again (fp32 accumulation), so nothing is kept from
+ * the forward but idx.  dh and dw are rounded to dtype once, and so is dz as
+ * the operand of their products; db is summed from the fp32 dz.  Results do
+ * not depend on the order of execution.
+ *  h [T,d], w [E,d] dtype; b [E] fp32; idx [T,k] int32; dwts [T,k] fp32
+ *  ws   workspace of moelb_gate_backward_workspace_bytes(...) bytes
+ *  dh   [T,d] dtype out or NULL;  dw [E,d] dtype out or NULL;  db [E] fp32 out
+ *       or NULL (T = 0: dw and db are zero)
+ * Ids outside [0,E) are left out; an id listed twice counts twice.
+ * Requires 1 <= k <= min(E, 16), E <= 256, d % 8 == 0, T >= 0, T*d elements
+ * below 2^32 - 65536 bytes; h, w, ws, dh and dw 16-byte aligned.
+ */
+size_t moelb_gate_backward_workspace_bytes(int T, int d, int E, int dtype);
+int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, const void* w,
+                        const float* b, const int32_t* idx, const float* dwts, void* ws,
+                        size_t ws_bytes, void* dh, void* dw, float* db, void* stream);
+
+/*
+ * A shared projection with the low-rank adapters of many requests beside it:
+ *   y[t] = x[t] w^T + scale[i] (x[t] a[i]^T) b[i]^T,  i = ids[t]
+ * with fp32 accumulation, y rounded to dtype once (and the r values x[t]
+ * a[i]^T once, as the operand of their second product).  gated: w and every
+ * b[i] hold d_out / 2 gate rows and then d_out / 2 up rows, and y[t] =
+ * SiLU(gate) * up.  Two calls, gated with w13 and plain with w2, are the
+ * layer's shared expert with adapters; n = 0 is the bare projection.
+ *  x      [T,d_in]         dtype
+ *  w      [d_out,d_in]     dtype, row-major
+ *  ids    [T] int32        adapter of each token; outside [0,n): none.  Tokens
+ *                          may come in any order; those of one adapter next to
+ *                          each other run fastest.  A token's y depends on its
+ *                          own x and adapter only
+ *  a      [n,r,d_in], b [n,d_out,r]  dtype; an adapter of a smaller rank is
+ *                          padded with zero rows of a
+ *  scale  [n] fp32
+ *  ws     workspace of moelb_adapter_projection_workspace_bytes(...) bytes
+ *  y      [T,d_out]  (gated: [T,d_out/2])  dtype out
+ * ids, a, b, scale and ws may be NULL where n = 0.  Requires d_in % 8 == 0,
+ * d_out % 8 == 0 (gated: % 16), n >= 0, r % 8 == 0 and 8 <= r <= 256
+ * (n > 0), and T*d_in, d_out*d_in, n*d_out*r and T*r elements each below 2^32 -
+ * 65536 bytes; x, w, a, b, ws and y 16-byte aligned.  y must not overlap the
+ * inputs.
+ */
+size_t moelb_adapter_projection_workspace_bytes(int T, int d_in, int d_out, int n, int r, int dtype);
+int moelb_adapter_projection(const void* x, int T, int d_in, int d_out, int dtype, const void* w,
+                             const int32_t* ids, const void* a, const void* b, const float* scale,
+                             int n, int r, int gated, void* ws, size_t ws_bytes, void* y,
+                             void* stream);
 
 #ifdef __cplusplus
 }

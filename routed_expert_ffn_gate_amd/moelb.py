@@ -50,6 +50,11 @@ SIGNATURES = {
     "moelb_grouped_ffn_backward": (_I, [_P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _SZ,
                                         _P, _P, _P, _P]),
     "moelb_combine": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moelb_combine_backward": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moelb_gate_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moelb_gate_backward": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P]),
+    "moelb_adapter_projection_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moelb_adapter_projection": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P, _P]),
     "moelb_pack_weights": (_I, [_P, _I, _I, _I, _I, _P, _P]),
 }
 
@@ -327,3 +332,55 @@ def moelb_combine(y, pos, wts, out, shared=None, stream=None):
     k = wts.shape[1]
     _check(lib().moelb_combine(_p(y), y.shape[0], _p(pos), _p(wts), T, k, d, dtype_code(out), _p(shared), _p(out),
                                _stream(stream)), "moelb_combine")
+
+
+def moelb_combine_backward(dout, y, pos, wts, dy, dwts, stream=None):
+    """Gradients of moelb_combine: dy as y (rows no pair names as they were), dwts [T, k] fp32."""
+    name = "moelb_combine_backward"
+    T, d = dout.shape
+    k = wts.shape[1]
+    _check_shapes(name, ("y", y, (y.shape[0], d), dout.dtype), ("dy", dy, y.shape, dout.dtype),
+                  ("wts", wts, (T, k), torch.float32), ("dwts", dwts, (T, k), torch.float32),
+                  ("pos", pos.reshape(-1), (T * k,), torch.int32))
+    _check(lib().moelb_combine_backward(_p(dout), _p(y), y.shape[0], _p(pos), _p(wts), T, k, d, dtype_code(dout),
+                                        _p(dy), _p(dwts), _stream(stream)), name)
+
+
+def moelb_gate_backward_workspace_bytes(T, d, E, dtype) -> int:
+    return int(lib().moelb_gate_backward_workspace_bytes(T, d, E, dtype))
+
+
+def moelb_gate_backward(h, w, b, idx, dwts, ws, dh=None, dw=None, db=None, stream=None):
+    """Gradients of moelb_gate_topk's weights: dh as h, dw as w, db as b (None: not computed)."""
+    name = "moelb_gate_backward"
+    T, d = h.shape
+    E = w.shape[0]
+    k = idx.shape[1]
+    _check_shapes(name, ("w", w, (E, d), h.dtype), ("b", b, (E,), torch.float32), ("idx", idx, (T, k), torch.int32),
+                  ("dwts", dwts, (T, k), torch.float32), ("dh", dh, (T, d), h.dtype), ("dw", dw, (E, d), h.dtype),
+                  ("db", db, (E,), torch.float32))
+    _check(lib().moelb_gate_backward(_p(h), T, d, E, k, dtype_code(h), _p(w), _p(b), _p(idx), _p(dwts), _p(ws),
+                                     ws.numel() * ws.element_size(), _p(dh), _p(dw), _p(db), _stream(stream)), name)
+
+
+def moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype) -> int:
+    return int(lib().moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype))
+
+
+def moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=False, stream=None):
+    """y = x w^T plus each token's adapter; ids, a, b, scale and ws None: the bare projection."""
+    name = "moelb_adapter_projection"
+    T, d_in = x.shape
+    d_out = w.shape[0]
+    n, r = (a.shape[0], a.shape[1]) if a is not None else (0, 0)
+    _check_shapes(name, ("w", w, (d_out, d_in), x.dtype), ("y", y, (T, d_out // 2 if gated else d_out), x.dtype),
+                  ("a", a, (n, r, d_in), x.dtype))
+    if a is not None:
+        if ids is None or b is None or scale is None or ws is None:
+            raise MoelbError(f"{name}: adapters need ids, a, b, scale and ws")
+        _check_shapes(name, ("ids", ids, (T,), torch.int32), ("b", b, (n, d_out, r), x.dtype),
+                      ("scale", scale, (n,), torch.float32))
+    _check(lib().moelb_adapter_projection(_p(x), T, d_in, d_out, dtype_code(x), _p(w), _p(ids), _p(a), _p(b),
+                                          _p(scale), n, r, int(gated), _p(ws),
+                                          ws.numel() * ws.element_size() if ws is not None else 0, _p(y),
+                                          _stream(stream)), name)

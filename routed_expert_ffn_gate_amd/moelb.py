@@ -277,36 +277,72 @@ def moelb_grouped_ffn_stages(stages, x, rows, group_off, E, w13, w2, ws, y, G=1,
            "moelb_grouped_ffn_stages")
 
 
-def _check_shapes(name, *pairs):
-    """Each (tensor, shape, dtype) as the entry point addresses it; None is skipped."""
-    for what, t, shape, dtype in pairs:
-        if t is None:
-            continue
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            raise MoelbError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+def _device(name, t) -> int:
+    """The current device, which the call's tensors have to be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise MoelbError(f"{name}: tensors on {t.device}, not on the current GPU")
+    return dev
 
 
-def _check_ffn(name, x, rows, group_off, E, w13, w2, gather, extra):
-    d, inter = x.shape[1], w2.shape[-1]
-    _check_shapes(name, ("w13", w13.reshape(-1, *w13.shape[-2:]), (E, 2 * inter, d), x.dtype),
-                  ("w2", w2.reshape(-1, *w2.shape[-2:]), (E, d, inter), x.dtype),
-                  ("group_off", group_off, (group_off.numel(),), torch.int32), *extra)
+def _arg(name, what, t, shape, dtype, dev):
+    """The data pointer of a tensor the entry point takes as `shape`, `dtype`, contiguous, on device `dev`."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype:
+        raise MoelbError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+    if t.get_device() != dev:
+        raise MoelbError(f"{name}: {what} is on {t.device}")
+    if not t.is_contiguous():
+        raise MoelbError(f"{name}: {what} must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(name, ws, dev):
+    """(pointer, bytes) of a workspace; None where there is none."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise MoelbError(f"{name}: the workspace must be contiguous, on the current GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _queue(stream, dev):
+    """The stream's handle; default: PyTorch's current stream of the device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ffn_args(name, x, rows, group_off, E, w13, w2, gather, dev):
+    rows_x, d = x.shape
+    inter = w2.shape[-1]
+    one = w13.dim() == 2  # one expert's weights without the leading dimension
+    if one and E != 1:
+        raise MoelbError(f"{name}: weights of one expert for E = {E}")
     if gather is not None and (gather.dtype != torch.int32 or gather.numel() < rows):
         raise MoelbError(f"{name}: gather holds {gather.numel()} {gather.dtype}, not {rows} int32")
-    if gather is None and rows > x.shape[0]:
-        raise MoelbError(f"{name}: {rows} rows of {x.shape[0]} without a gather")
-    return d, inter
+    if gather is None and rows > rows_x:
+        raise MoelbError(f"{name}: {rows} rows of {rows_x} without a gather")
+    t = x.dtype
+    return (d, inter, dtype_code(x), _arg(name, "x", x, (rows_x, d), t, dev),
+            _arg(name, "group_off", group_off, (group_off.numel(),), torch.int32, dev),
+            _arg(name, "gather", gather, gather.shape if gather is not None else None, torch.int32, dev),
+            _arg(name, "w13", w13, (2 * inter, d) if one else (E, 2 * inter, d), t, dev),
+            _arg(name, "w2", w2, (d, inter) if one else (E, d, inter), t, dev))
 
 
 def moelb_grouped_ffn_train(x, rows, group_off, E, w13, w2, ws, z, y, G=1, rank=-1, gather=None, gather_k=1,
                             stream=None):
     """The grouped FFN keeping its projections: z [rows, 2*inter] fp32, y [rows, d]."""
     name = "moelb_grouped_ffn_train"
-    d, inter = _check_ffn(name, x, rows, group_off, E, w13, w2, gather,
-                          (("z", z, (rows, 2 * w2.shape[-1]), torch.float32), ("y", y, (rows, x.shape[1]), x.dtype)))
-    _check(lib().moelb_grouped_ffn_train(_p(x), x.shape[0], rows, _p(group_off), group_off.numel() - 1, E, G, rank,
-                                         _p(gather), gather_k, d, inter, dtype_code(x), _p(w13), _p(w2), _p(ws),
-                                         ws.numel() * ws.element_size(), _p(z), _p(y), _stream(stream)), name)
+    dev = _device(name, x)
+    d, inter, code, px, poff, pg, p13, p2 = _ffn_args(name, x, rows, group_off, E, w13, w2, gather, dev)
+    pws, nws = _workspace(name, ws, dev)
+    _check(lib().moelb_grouped_ffn_train(px, x.shape[0], rows, poff, group_off.numel() - 1, E, G, rank, pg, gather_k,
+                                         d, inter, code, p13, p2, pws, nws,
+                                         _arg(name, "z", z, (rows, 2 * inter), torch.float32, dev),
+                                         _arg(name, "y", y, (rows, d), x.dtype, dev), _queue(stream, dev)), name)
 
 
 def moelb_grouped_ffn_backward_workspace_bytes(rows, num_groups, E, d, inter, dtype) -> int:
@@ -317,14 +353,16 @@ def moelb_grouped_ffn_backward(dy, x, rows, group_off, E, w13, w2, z, ws, dx=Non
                                gather=None, gather_k=1, stream=None):
     """Gradients of moelb_grouped_ffn_train's y: dx [rows, d], dw13 and dw2 as the weights (None: not computed)."""
     name = "moelb_grouped_ffn_backward"
-    d, inter = _check_ffn(name, x, rows, group_off, E, w13, w2, gather,
-                          (("z", z, (rows, 2 * w2.shape[-1]), torch.float32), ("dy", dy, (rows, x.shape[1]), x.dtype),
-                           ("dx", dx, (rows, x.shape[1]), x.dtype), ("dw13", dw13, w13.shape, x.dtype),
-                           ("dw2", dw2, w2.shape, x.dtype)))
-    _check(lib().moelb_grouped_ffn_backward(_p(dy), _p(x), x.shape[0], rows, _p(group_off), group_off.numel() - 1, E,
-                                            G, rank, _p(gather), gather_k, d, inter, dtype_code(x), _p(w13), _p(w2),
-                                            _p(z), _p(ws), ws.numel() * ws.element_size(), _p(dx), _p(dw13), _p(dw2),
-                                            _stream(stream)), name)
+    dev = _device(name, x)
+    d, inter, code, px, poff, pg, p13, p2 = _ffn_args(name, x, rows, group_off, E, w13, w2, gather, dev)
+    pws, nws = _workspace(name, ws, dev)
+    t = x.dtype
+    _check(lib().moelb_grouped_ffn_backward(_arg(name, "dy", dy, (rows, d), t, dev), px, x.shape[0], rows, poff,
+                                            group_off.numel() - 1, E, G, rank, pg, gather_k, d, inter, code, p13, p2,
+                                            _arg(name, "z", z, (rows, 2 * inter), torch.float32, dev), pws, nws,
+                                            _arg(name, "dx", dx, (rows, d), t, dev),
+                                            _arg(name, "dw13", dw13, w13.shape, t, dev),
+                                            _arg(name, "dw2", dw2, w2.shape, t, dev), _queue(stream, dev)), name)
 
 
 def moelb_combine(y, pos, wts, out, shared=None, stream=None):
@@ -337,13 +375,17 @@ def moelb_combine(y, pos, wts, out, shared=None, stream=None):
 def moelb_combine_backward(dout, y, pos, wts, dy, dwts, stream=None):
     """Gradients of moelb_combine: dy as y (rows no pair names as they were), dwts [T, k] fp32."""
     name = "moelb_combine_backward"
+    dev = _device(name, dout)
     T, d = dout.shape
-    k = wts.shape[1]
-    _check_shapes(name, ("y", y, (y.shape[0], d), dout.dtype), ("dy", dy, y.shape, dout.dtype),
-                  ("wts", wts, (T, k), torch.float32), ("dwts", dwts, (T, k), torch.float32),
-                  ("pos", pos.reshape(-1), (T * k,), torch.int32))
-    _check(lib().moelb_combine_backward(_p(dout), _p(y), y.shape[0], _p(pos), _p(wts), T, k, d, dtype_code(dout),
-                                        _p(dy), _p(dwts), _stream(stream)), name)
+    rows, k = y.shape[0], wts.shape[1]
+    t, f = dout.dtype, torch.float32
+    if pos.numel() != T * k:
+        raise MoelbError(f"{name}: pos holds {pos.numel()} entries, not {T * k}")
+    _check(lib().moelb_combine_backward(_arg(name, "dout", dout, (T, d), t, dev), _arg(name, "y", y, (rows, d), t, dev),
+                                        rows, _arg(name, "pos", pos, pos.shape, torch.int32, dev),
+                                        _arg(name, "wts", wts, (T, k), f, dev), T, k, d, dtype_code(dout),
+                                        _arg(name, "dy", dy, (rows, d), t, dev),
+                                        _arg(name, "dwts", dwts, (T, k), f, dev), _queue(stream, dev)), name)
 
 
 def moelb_gate_backward_workspace_bytes(T, d, E, dtype) -> int:
@@ -353,14 +395,17 @@ def moelb_gate_backward_workspace_bytes(T, d, E, dtype) -> int:
 def moelb_gate_backward(h, w, b, idx, dwts, ws, dh=None, dw=None, db=None, stream=None):
     """Gradients of moelb_gate_topk's weights: dh as h, dw as w, db as b (None: not computed)."""
     name = "moelb_gate_backward"
+    dev = _device(name, h)
     T, d = h.shape
-    E = w.shape[0]
-    k = idx.shape[1]
-    _check_shapes(name, ("w", w, (E, d), h.dtype), ("b", b, (E,), torch.float32), ("idx", idx, (T, k), torch.int32),
-                  ("dwts", dwts, (T, k), torch.float32), ("dh", dh, (T, d), h.dtype), ("dw", dw, (E, d), h.dtype),
-                  ("db", db, (E,), torch.float32))
-    _check(lib().moelb_gate_backward(_p(h), T, d, E, k, dtype_code(h), _p(w), _p(b), _p(idx), _p(dwts), _p(ws),
-                                     ws.numel() * ws.element_size(), _p(dh), _p(dw), _p(db), _stream(stream)), name)
+    E, k = w.shape[0], idx.shape[1]
+    t, f = h.dtype, torch.float32
+    pws, nws = _workspace(name, ws, dev)
+    _check(lib().moelb_gate_backward(_arg(name, "h", h, (T, d), t, dev), T, d, E, k, dtype_code(h),
+                                     _arg(name, "w", w, (E, d), t, dev), _arg(name, "b", b, (E,), f, dev),
+                                     _arg(name, "idx", idx, (T, k), torch.int32, dev),
+                                     _arg(name, "dwts", dwts, (T, k), f, dev), pws, nws,
+                                     _arg(name, "dh", dh, (T, d), t, dev), _arg(name, "dw", dw, (E, d), t, dev),
+                                     _arg(name, "db", db, (E,), f, dev), _queue(stream, dev)), name)
 
 
 def moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype) -> int:
@@ -370,17 +415,21 @@ def moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype) -> int
 def moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=False, stream=None):
     """y = x w^T plus each token's adapter; ids, a, b, scale and ws None: the bare projection."""
     name = "moelb_adapter_projection"
+    dev = _device(name, x)
     T, d_in = x.shape
     d_out = w.shape[0]
-    n, r = (a.shape[0], a.shape[1]) if a is not None else (0, 0)
-    _check_shapes(name, ("w", w, (d_out, d_in), x.dtype), ("y", y, (T, d_out // 2 if gated else d_out), x.dtype),
-                  ("a", a, (n, r, d_in), x.dtype))
+    t = x.dtype
+    n = r = 0
     if a is not None:
+        n, r = a.shape[0], a.shape[1]
         if ids is None or b is None or scale is None or ws is None:
             raise MoelbError(f"{name}: adapters need ids, a, b, scale and ws")
-        _check_shapes(name, ("ids", ids, (T,), torch.int32), ("b", b, (n, d_out, r), x.dtype),
-                      ("scale", scale, (n,), torch.float32))
-    _check(lib().moelb_adapter_projection(_p(x), T, d_in, d_out, dtype_code(x), _p(w), _p(ids), _p(a), _p(b),
-                                          _p(scale), n, r, int(gated), _p(ws),
-                                          ws.numel() * ws.element_size() if ws is not None else 0, _p(y),
-                                          _stream(stream)), name)
+    pws, nws = _workspace(name, ws, dev)
+    _check(lib().moelb_adapter_projection(_arg(name, "x", x, (T, d_in), t, dev), T, d_in, d_out, dtype_code(x),
+                                          _arg(name, "w", w, (d_out, d_in), t, dev),
+                                          _arg(name, "ids", ids, (T,), torch.int32, dev),
+                                          _arg(name, "a", a, (n, r, d_in), t, dev),
+                                          _arg(name, "b", b, (n, d_out, r), t, dev),
+                                          _arg(name, "scale", scale, (n,), torch.float32, dev), n, r, int(gated), pws,
+                                          nws, _arg(name, "y", y, (T, d_out // 2 if gated else d_out), t, dev),
+                                          _queue(stream, dev)), name)

@@ -6,22 +6,28 @@
 // layer's always-on shared expert stands, whose projections every request
 // shares while its adapter is the request's own.
 //
-// Two launches.  The first forms low[t] = scale_a x[t] A_a^T (r values a
-// token, in the storage type: an operand of the second product, off by half a
-// step of the adapter's small share of y).  The second is the projection, with
-// the adapters inside its sum:
+// The low products low[t] = scale_a x[t] A_a^T (r values a token) are formed
+// first, then y:
 //  * Prompts (adapter_tile_kernel): the product x W^T on the tile of
-//    mfma_tile.h.  Then, into the same accumulators, low B_a^T for every adapter
-//    that occurs among a wave's rows, fragments straight from memory (r values
-//    a row: they sit in L2).  An accumulator lane belongs to one token, so a
-//    lane whose token has another adapter keeps its old value: nothing of one
-//    request's adapter, NaN or infinity included, reaches another's tokens.
-//    Rows of one request take one such product; mixed rows take one for each
-//    adapter among them.
-//  * Few tokens (adapter_few_kernel): the weights' bytes bound it, so a
-//    workgroup takes 16 rows of W and 8 waves cut the sum over k between them,
-//    v_mfma_f32_16x16x32_bf16 straight from registers; partial sums meet in LDS
-//    in wave order, and each thread adds the rank-r product of its outputs.
+//    mfma_tile.h.  Where all tokens of a tile have one adapter, low and B_a are
+//    further K steps of it (one, up to rank 64).  Elsewhere low B_a^T is added to
+//    the accumulators afterwards for every adapter that occurs among a wave's
+//    rows, fragments straight from memory.  An accumulator lane belongs to one
+//    token, so a lane whose token has another adapter keeps its value: nothing
+//    of one request's adapter, NaN or infinity included, reaches another's
+//    tokens (as a shared K step with zeros for the other tokens would let it).
+//    Its low products come from a launch of their own, in the storage type (an
+//    operand of the second product, off by half a step of the adapter's small
+//    share of y).
+//  * Few tokens (up to 64): the bytes of W and of the adapters in use bound it,
+//    so the work is cut for many loads in flight: 64 rows of W x a part of k a
+//    workgroup, v_mfma_f32_16x16x32_bf16 straight from registers, with the low
+//    products' workgroups in the same launch; fp32 partial sums and low products
+//    go through the workspace to a second launch, which adds them in order and
+//    forms the rank-r products.
+//  * One to four tokens with few ranks: one launch.  Every workgroup takes 16
+//    rows of W and forms the low products itself (A_a of a token is as small as
+//    its rows of W, and comes from L2).
 #include "mfma_tile.h"
 
 namespace {
@@ -33,9 +39,10 @@ struct AdapterArgs {
   const void* a;
   const void* b;
   const float* scale;
-  void* low;  // [T][r]
+  void* low;    // [T][r]; fp32 for few tokens, else the storage type
+  float* part;  // few tokens: [splits][T][d_out]; prompts: [splits][T][r]
   void* y;
-  int Ttok, d_in, d_out, n, r, ntn;
+  int Ttok, d_in, d_out, n, r, ntn, splits, nbase;
 };
 
 __device__ __forceinline__ uint32_t bytes32(size_t n) { return n < mt::OUTSIDE ? (uint32_t)n : mt::OUTSIDE; }
@@ -66,9 +73,10 @@ __device__ __forceinline__ bf16x8_t frag_at(const uint16_t* row, int k, int kc, 
 // ---------------------------------------------------------------- low = scale x A^T
 
 // A wave per (token, rank): a dot product over d_in, 8 values a lane and step.
-template <typename T>
-__global__ __launch_bounds__(256) void adapter_low_rows_kernel(AdapterArgs p) {
-  const long long wv = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+// `L`: the type low is kept in.
+template <typename T, typename L>
+__device__ __forceinline__ void low_rows(const AdapterArgs& p, int block) {
+  const long long wv = (long long)block * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int t = (int)(wv / p.r), rr = (int)(wv % p.r);
   if (t >= p.Ttok) return;
@@ -77,7 +85,7 @@ __global__ __launch_bounds__(256) void adapter_low_rows_kernel(AdapterArgs p) {
   const T* x = static_cast<const T*>(p.x) + (size_t)t * p.d_in;
   const T* a = static_cast<const T*>(p.a) + ((size_t)id * p.r + rr) * p.d_in;
   float s0 = 0.f, s1 = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = lane * 8; k < p.d_in; k += MOELB_WAVE * 8) {
     float u[8], v[8];
     load_vec(x + k, u);
@@ -91,81 +99,135 @@ __global__ __launch_bounds__(256) void adapter_low_rows_kernel(AdapterArgs p) {
   s0 += s1;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s0 += __shfl_xor(s0, o, MOELB_WAVE);
-  if (lane == 0) Elem<T>::store(static_cast<T*>(p.low), (size_t)t * p.r + rr, s0 * p.scale[id]);
+  if (lane == 0) Elem<L>::store(static_cast<L*>(p.low), (size_t)t * p.r + rr, s0 * p.scale[id]);
 }
 
-// 32 tokens x 64 ranks of the blockIdx.y-th adapter among the tile's tokens;
-// 8 waves cut the sum over k, partial sums meet in LDS in wave order.  Rows of
-// tokens with another adapter are formed and dropped: tokens of a request are
-// neighbours, so a tile has one or two adapters.
-constexpr int LOW_TOK = 32, LOW_WAVES = 8;
+__global__ __launch_bounds__(256) void adapter_low_rows_f32_kernel(AdapterArgs p) {
+  low_rows<float, float>(p, blockIdx.x);
+}
 
-__global__ __launch_bounds__(MOELB_WAVE * LOW_WAVES) void adapter_low_tile_kernel(AdapterArgs p) {
-  __shared__ float part[LOW_WAVES][LOW_TOK * 64];
+// The adapter of all tokens t0 .. t0 + rows - 1 (up to T), -1 if they differ or
+// have none.  Wave-uniform.
+__device__ __forceinline__ int same_id(const AdapterArgs& p, int t0, int rows) {
+  if (p.n <= 0) return -1;
+  const int id = __builtin_amdgcn_readfirstlane(id_of(p, t0));
+  bool other = id < 0;
+  for (int i = threadIdx.x & 63; i < rows; i += MOELB_WAVE)
+    if (t0 + i < p.Ttok && id_of(p, t0 + i) != id) other = true;
+  return __ballot(other) ? -1 : id;
+}
+
+// Prompts: a workgroup takes 128 tokens (32 a wave), 64 ranks (blockIdx.z) and
+// one part of k (blockIdx.y); its waves read the same rows of A_a together.
+// Tokens of one adapter: the tile of mfma_tile.h (half its columns unused up to
+// rank 64; fragments straight from memory, a row a lane, are served 16 bytes a
+// cycle: 30 us against 13 at 8192 tokens, d_in = 4096, r = 64).  Others: a wave
+// walks the adapters among its tokens, in token order, with such fragments, and
+// keeps of each product the rows of that adapter's tokens.  Partial sums go to
+// part[split][T][r].
+constexpr int LOW_TOK = 128;
+
+__global__ __launch_bounds__(256) void adapter_low_tile_kernel(AdapterArgs p) {
+  extern __shared__ __align__(16) char smem[];
+  const int steps64 = (p.d_in + 63) / 64, per64 = (steps64 + p.splits - 1) / p.splits;
+  const int k0 = min(p.d_in, (int)blockIdx.y * per64 * 64), k1 = min(p.d_in, k0 + per64 * 64);
+  const int same = same_id(p, blockIdx.x * LOW_TOK, LOW_TOK);
+  if (same >= 0) {
+    const int t0 = blockIdx.x * LOW_TOK, n0 = blockIdx.z * 64;
+    mt::RowOp<2> oa, ob;
+    oa.init(static_cast<const uint16_t*>(p.x) + k0, bytes32(((size_t)p.Ttok * p.d_in - k0) * 2), p.d_in, k1 - k0,
+            [&](int i) { return min(t0 + i, p.Ttok - 1); });
+    ob.init(static_cast<const uint16_t*>(p.a) + (size_t)same * p.r * p.d_in + k0,
+            bytes32(((size_t)p.r * p.d_in - k0) * 2), p.d_in, k1 - k0,
+            [&](int i) { return min(n0 + (i & 63), p.r - 1); });
+    f32x16_t acc[2][2];
+    mt::k_loop<2, false>(reinterpret_cast<uint16_t*>(smem), oa, ob, max(1, (k1 - k0 + 63) / 64), acc);
+    mt::drain<2, false>(reinterpret_cast<uint16_t*>(smem), acc, [&](int i, int c, const float* v) {
+      if (t0 + i < p.Ttok && c < 64 && n0 + c < p.r)
+        mt::store8(p.part + ((size_t)blockIdx.y * p.Ttok + t0 + i) * p.r + n0 + c, v);
+    });
+    return;
+  }
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = blockIdx.x * LOW_TOK, r0 = blockIdx.z * 64;
-  const int mine = t0 + (lane & 31) < p.Ttok ? id_of(p, t0 + (lane & 31)) : -1;
-  uint64_t left = __ballot(mine >= 0);
-  int id = -1;
-  for (int i = 0; i <= (int)blockIdx.y; ++i) {  // the blockIdx.y-th distinct id, in token order
-    if (!left) return;
-    id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-    left &= ~__ballot(mine == id);
-  }
-  const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  const uint16_t* a = static_cast<const uint16_t*>(p.a) + (size_t)id * p.r * p.d_in;
-  const int steps = (p.d_in + 15) / 16, per = (steps + LOW_WAVES - 1) / LOW_WAVES;
-  const int k0 = wave * per * 16, k1 = min(p.d_in, k0 + per * 16);
-  const uint16_t* xr = x + (size_t)min(t0 + (lane & 31), p.Ttok - 1) * p.d_in + (lane >> 5) * 8;
-  const uint16_t* ar[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    ar[i] = a + (size_t)min(r0 + i * 32 + (lane & 31), p.r - 1) * p.d_in + (lane >> 5) * 8;
-  f32x16_t acc[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) acc[i][q] = 0.f;
-  const bool two = p.r - r0 > 32;
+  const int t = blockIdx.x * LOW_TOK + (threadIdx.x >> 6) * 32 + (lane & 31), r0 = blockIdx.z * 64;
+  const int mine = t < p.Ttok ? id_of(p, t) : -1;
   const int kc = (lane >> 5) * 8;
-  for (int k = k0; k < k1; k += 64) {  // four steps' loads in flight
-    bf16x8_t fx[4], f0[4], f1[4];
+  const uint16_t* xr = static_cast<const uint16_t*>(p.x) + (size_t)min(t, p.Ttok - 1) * p.d_in + kc;
+  const bool two = p.r - r0 > 32;
+  uint64_t left = __ballot(mine >= 0);
+  while (left) {
+    const int id = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    left &= ~__ballot(mine == id);
+    const uint16_t* a = static_cast<const uint16_t*>(p.a) + (size_t)id * p.r * p.d_in + kc;
+    const uint16_t* a0 = a + (size_t)min(r0 + (lane & 31), p.r - 1) * p.d_in;
+    const uint16_t* a1 = a + (size_t)min(r0 + 32 + (lane & 31), p.r - 1) * p.d_in;
+    f32x16_t acc[2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      fx[u] = frag_at(xr, k + u * 16, kc, k1);
-      f0[u] = frag_at(ar[0], k + u * 16, kc, k1);
-      if (two) f1[u] = frag_at(ar[1], k + u * 16, kc, k1);
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[j][q] = 0.f;
+    for (int k = k0; k < k1; k += 64) {  // four steps' loads in flight
+      bf16x8_t fx[4], f0[4], f1[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        fx[u] = frag_at(xr, k + u * 16, kc, k1);
+        f0[u] = frag_at(a0, k + u * 16, kc, k1);
+        if (two) f1[u] = frag_at(a1, k + u * 16, kc, k1);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0[u], fx[u], acc[0], 0, 0, 0);
+        if (two) acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1[u], fx[u], acc[1], 0, 0, 0);
+      }
     }
+    // lane: token lane % 32; element j: rank (j / 4) * 8 + (lane / 32) * 4 + j % 4
+    if (mine == id) {
+      float* o = p.part + ((size_t)blockIdx.y * p.Ttok + t) * p.r;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0[u], fx[u], acc[0], 0, 0, 0);
-      if (two) acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1[u], fx[u], acc[1], 0, 0, 0);
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rr = r0 + j * 32 + q * 8 + (lane >> 5) * 4;
+          const f32x4_t v = {acc[j][q * 4], acc[j][q * 4 + 1], acc[j][q * 4 + 2], acc[j][q * 4 + 3]};
+          if (rr < p.r) *reinterpret_cast<f32x4_t*>(o + rr) = v;
+        }
     }
   }
-  // lane: token lane % 32; element j: rank (j / 4) * 8 + (lane / 32) * 4 + j % 4
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4_t v = {acc[i][q * 4], acc[i][q * 4 + 1], acc[i][q * 4 + 2], acc[i][q * 4 + 3]};
-      const int c4 = i * 8 + q * 2 + (lane >> 5);
-      *reinterpret_cast<f32x4_t*>(&part[wave][(lane & 31) * 64 + ((c4 ^ (lane & 15)) * 4)]) = v;
-    }
-  __syncthreads();
-  const int tok = threadIdx.x >> 4, c4 = threadIdx.x & 15;
+}
+
+// low = scale x the parts' sum, in order; four values a thread.
+__global__ __launch_bounds__(256) void adapter_low_sum_kernel(AdapterArgs p) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(i / (p.r / 4)), c = (int)(i % (p.r / 4)) * 4;
+  if (t >= p.Ttok) return;
+  const int id = id_of(p, t);
+  if (id < 0) return;
+  const float* o = p.part + (size_t)t * p.r + c;
+  const float sc = p.scale[id];
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int w = 0; w < LOW_WAVES; ++w)
-    v += *reinterpret_cast<const f32x4_t*>(&part[w][tok * 64 + ((c4 ^ (tok & 15)) * 4)]);
-  const int t = t0 + tok, rr = r0 + c4 * 4;
-  if (t >= p.Ttok || rr >= p.r || id_of(p, t) != id) return;
-  const float s = p.scale[id];
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.low) + (size_t)t * p.r + rr) =
-      make_uint2(bf16x2_pack(v[0] * s, v[1] * s), bf16x2_pack(v[2] * s, v[3] * s));
+#pragma unroll 8
+  for (int s = 0; s < p.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(o + (size_t)s * p.Ttok * p.r);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.low) + (size_t)t * p.r + c) =
+      make_uint2(bf16x2_pack(v[0] * sc, v[1] * sc), bf16x2_pack(v[2] * sc, v[3] * sc));
 }
 
 // ---------------------------------------------------------------- prompts
+
+// A row operand that goes on, after its own K steps, with the r columns of a
+// second matrix (low, or B_a).
+template <int F>
+struct LongRowOp {
+  static constexpr bool COL = false;
+  mt::RowOp<F> own, more;
+  int first;
+  __device__ __forceinline__ void begin(int) {}
+  __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
+    if (t < first)
+      own.issue(t, j, m0);
+    else
+      more.issue(t - first, j, m0);
+  }
+};
 
 // acc += low B^T for the adapters among this wave's 32 F rows.  own[mi]: the
 // adapter of row block mi's lane % 32-th token, -1: none.  brow(ni): row of B
@@ -266,12 +328,18 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
     const int c = n0 + (GU ? i % (B / 2) : i);
     return (c < out ? c : 0) + (GU && i >= B / 2 ? out : 0);
   };
-  mt::RowOp<F> oa, ob;
-  oa.init(p.x, bytes32((size_t)p.Ttok * p.d_in * 2), p.d_in, p.d_in, trow);
-  ob.init(p.w, bytes32((size_t)p.d_out * p.d_in * 2), p.d_in, p.d_in, wrow);
+  // a tile of one adapter takes its ranks as further K steps
+  const int id = same_id(p, t0, B);
+  LongRowOp<F> oa, ob;
+  oa.own.init(p.x, bytes32((size_t)p.Ttok * p.d_in * 2), p.d_in, p.d_in, trow);
+  ob.own.init(p.w, bytes32((size_t)p.d_out * p.d_in * 2), p.d_in, p.d_in, wrow);
+  oa.more.init(p.low, bytes32((size_t)p.Ttok * p.r * 2), p.r, p.r, trow);
+  ob.more.init(static_cast<const uint16_t*>(p.b) + (size_t)max(id, 0) * p.d_out * p.r,
+               bytes32((size_t)p.d_out * p.r * 2), p.r, p.r, wrow);
+  oa.first = ob.first = (p.d_in + mt::BK - 1) / mt::BK;
   f32x16_t acc[F][F];
-  mt::k_loop<F, GU>(lds, oa, ob, (p.d_in + mt::BK - 1) / mt::BK, acc);
-  if (p.n > 0) {
+  mt::k_loop<F, GU>(lds, oa, ob, oa.first + (id >= 0 ? (p.r + mt::BK - 1) / mt::BK : 0), acc);
+  if (p.n > 0 && id < 0) {
     const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
     const uint16_t* low[F];
     int own[F];
@@ -352,94 +420,237 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_f32_kernel(AdapterAr
 
 // ---------------------------------------------------------------- few tokens
 
-// 16 rows of W (GU: 8 gate rows and their 8 up rows) x 16 NB tokens
-// (blockIdx.y: which 16 NB).  8 waves cut k; each lane holds row (or token)
-// lane % 16 and k (lane / 16) * 8 .. of a 32-wide step.
-constexpr int FEW_WAVES = 8;
+// Base part: 64 rows of W x all tokens (16 NB of them) x one part of k.  W and
+// x stream memory -> LDS in 64-wide K steps, three ahead (a row's 128 bytes by 8
+// neighbouring lanes: read as fragments, a row a lane, they come at a quarter of
+// the rate), the slots of a row XORed so that 16 rows' fragments lie on
+// different banks; wave w takes rows 16 w .., all tokens.  Blocks from nbase on
+// form the low products.
+constexpr int FEW_STAGES = 4;
 
-template <int NB, bool GU>
-__global__ __launch_bounds__(MOELB_WAVE * FEW_WAVES) void adapter_few_kernel(AdapterArgs p) {
-  constexpr int TOK = 16 * NB;
-  __shared__ f32x4_t part[FEW_WAVES][TOK * 4];
+template <int NB>
+__global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
+  if ((int)blockIdx.x >= p.nbase) {
+    low_rows<uint16_t, float>(p, blockIdx.x - p.nbase);
+    return;
+  }
+  constexpr int TOK = 16 * NB, STAGE = (64 + TOK) * 64;  // elements
+  constexpr int NX = NB > 1 ? NB / 2 : 1;                // DMA instructions of x a wave and stage
+  __shared__ __align__(16) uint16_t lds[FEW_STAGES * STAGE];
+  const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x % p.splits, n0 = blockIdx.x / p.splits * 64;
+  const int steps = (p.d_in + 63) / 64, per = (steps + p.splits - 1) / p.splits;
+  const int s0 = min(steps, split * per), n = min(steps, s0 + per) - s0;
+  const mt::i32x4_t ws = mt::descriptor(p.w, bytes32((size_t)p.d_out * p.d_in * 2));
+  const mt::i32x4_t xs = mt::descriptor(p.x, bytes32((size_t)p.Ttok * p.d_in * 2));
+  // DMA block b (8 rows): lane -> row lane / 8, slot lane % 8 <- chunk slot ^ swizzle
+  uint32_t woff[2], xoff[NX];
+  int wck[2], xck[NX], xblk[NX];
+  auto chunk = [&](int r) { return (lane & 7) ^ (((r >> 1) ^ (r << 2)) & 7); };
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = (wave * 2 + j) * 8 + (lane >> 3);
+    wck[j] = chunk(r) * 8;
+    woff[j] = ((uint32_t)min(n0 + r, p.d_out - 1) * (uint32_t)p.d_in + wck[j]) * 2u;
+  }
+#pragma unroll
+  for (int j = 0; j < NX; ++j) {
+    xblk[j] = NB > 1 ? wave * NX + j : wave & 1;  // NB = 1: waves 2, 3 write what 0, 1 write
+    const int r = xblk[j] * 8 + (lane >> 3);
+    xck[j] = chunk(r) * 8;
+    xoff[j] = ((uint32_t)min(r, p.Ttok - 1) * (uint32_t)p.d_in + xck[j]) * 2u;
+  }
+  auto issue = [&](int i) {
+    const uint32_t st = lds_u32 + (uint32_t)((i % FEW_STAGES) * STAGE) * 2u;
+    const int k = (s0 + i) * 64;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      mt::copy16(wck[j] + k < p.d_in ? woff[j] + (uint32_t)k * 2u : mt::OUTSIDE, ws,
+                 st + (uint32_t)((wave * 2 + j) * 512) * 2u);
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+      mt::copy16(xck[j] + k < p.d_in ? xoff[j] + (uint32_t)k * 2u : mt::OUTSIDE, xs,
+                 st + (uint32_t)(64 * 64 + xblk[j] * 512) * 2u);
+  };
+  f32x4_t acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < FEW_STAGES - 1 && i < n; ++i) issue(i);
+  const int fr = lane & 15, fc = lane >> 4, sw = ((fr >> 1) ^ (fr << 2)) & 7;
+  for (int i = 0; i < n; ++i) {
+    // stage i landed (at most the two after it are in flight), and every wave
+    // has read stage i - 1, whose place the next load takes
+    constexpr int V = 2 + NX;
+    if (i + 2 < n)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * V) : "memory");
+    else if (i + 1 < n)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(V) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (i + FEW_STAGES - 1 < n) issue(i + FEW_STAGES - 1);
+    const uint16_t* st = lds + (i % FEW_STAGES) * STAGE;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = ((h * 4 + fc) ^ sw) * 8;
+      const bf16x8_t fw = *reinterpret_cast<const bf16x8_t*>(st + (wave * 16 + fr) * 64 + c);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const bf16x8_t fx = *reinterpret_cast<const bf16x8_t*>(st + (64 + j * 16 + fr) * 64 + c);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx, acc[j], 0, 0, 0);
+      }
+    }
+  }
+  // lane: token lane % 16 of block j, rows 16 wave + (lane / 16) * 4 ..
+  const int c0 = n0 + wave * 16 + fc * 4;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int tok = j * 16 + fr;
+    if (tok < p.Ttok && c0 < p.d_out)
+      *reinterpret_cast<f32x4_t*>(p.part + ((size_t)split * p.Ttok + tok) * p.d_out + c0) = acc[j];
+  }
+}
+
+// Two rows of W a thread (a gate and its up row, or two neighbours): their
+// partial sums in order, and low . B rows.
+template <bool GU>
+__global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
+  const int out = GU ? p.d_out / 2 : p.d_out, per = GU ? out : out / 2;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(i / per), c = (int)(i % per);
+  if (t >= p.Ttok) return;
+  const int c0 = GU ? c : 2 * c, c1 = GU ? out + c : 2 * c + 1;
+  const int id = id_of(p, t);
+  const float* part = p.part + (size_t)t * p.d_out;
+  float v0 = 0.f, v1 = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < p.splits; ++s) {
+    const float* q = part + (size_t)s * p.Ttok * p.d_out;
+    v0 += q[c0];
+    v1 += q[c1];
+  }
+  if (id >= 0) {
+    const float* low = static_cast<const float*>(p.low) + (size_t)t * p.r;
+    const uint16_t* b = static_cast<const uint16_t*>(p.b) + (size_t)id * p.d_out * p.r;
+#pragma unroll 2
+    for (int k = 0; k < p.r; k += 8) {
+      float l[8], u[8], w[8];
+      mt::load8(low + k, l);
+      load_vec(b + (size_t)c0 * p.r + k, u);
+      load_vec(b + (size_t)c1 * p.r + k, w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v0 = fmaf(l[q], u[q], v0);
+        v1 = fmaf(l[q], w[q], v1);
+      }
+    }
+  }
+  uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t * out;
+  if (GU)
+    y[c] = f32_to_bf16(silu_f32(v0) * v1);
+  else
+    *reinterpret_cast<uint32_t*>(y + 2 * c) = bf16x2_pack(v0, v1);
+}
+
+// One launch for NT <= ONE_TOKENS tokens with at most ONE_LOW low products in
+// all: 16 rows of W (GU: 8 gate rows and their 8 up rows), a row a wave, as dot
+// products with every token; the low products, a row of A_a each, are dealt to
+// the same waves.  Whole rows by neighbouring lanes, and up to d_in = 2048 all
+// loads of a wave at once.
+constexpr int ONE_TOKENS = 4, ONE_LOW = 64, ONE_WAVES = 16;
+
+template <int NT, bool GU>
+__global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(AdapterArgs p) {
+  __shared__ float base[16][NT];
+  __shared__ float low[ONE_LOW];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int out = GU ? p.d_out / 2 : p.d_out;
-  const int n0 = blockIdx.x * (GU ? 8 : 16), t0 = blockIdx.y * TOK;
-  auto wrow = [&](int i) {  // row of W for tile row i
+  const int n0 = blockIdx.x * (GU ? 8 : 16);
+  auto wrow = [&](int i) {  // row of W for row i of the workgroup
     const int c = n0 + (GU ? i & 7 : i);
     return (c < out ? c : 0) + (GU && i >= 8 ? out : 0);
   };
-  const uint16_t* w = static_cast<const uint16_t*>(p.w) + (size_t)wrow(lane & 15) * p.d_in + (lane >> 4) * 8;
-  const uint16_t* x[NB];
+  const uint16_t* x = static_cast<const uint16_t*>(p.x);
+  const uint16_t* w = static_cast<const uint16_t*>(p.w) + (size_t)wrow(wave) * p.d_in;
+  // the output of this thread: token, row (GU: gate row and its up row)
+  const int rows = GU ? 8 : 16;
+  const int tt = threadIdx.x / rows, tj = threadIdx.x % rows;
+  const bool mine = tt < p.Ttok && n0 + tj < out;
+  const int own = mine ? id_of(p, tt) : -1;
+  float acc[NT];
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
-    x[i] = static_cast<const uint16_t*>(p.x) + (size_t)min(t0 + i * 16 + (lane & 15), p.Ttok - 1) * p.d_in +
-           (lane >> 4) * 8;
-  const int steps = (p.d_in + 31) / 32, per = (steps + FEW_WAVES - 1) / FEW_WAVES;
-  const int k0 = wave * per * 32, k1 = min(p.d_in, k0 + per * 32);
-  f32x4_t acc[NB];
+  for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+#pragma unroll 4
+  for (int k = lane * 8; k < p.d_in; k += MOELB_WAVE * 8) {
+    float a[8];
+    load_vec(w + k, a);
 #pragma unroll
-  for (int i = 0; i < NB; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int kc = (lane >> 4) * 8;
-  for (int k = k0; k < k1; k += 128) {  // four steps' loads in flight
-    bf16x8_t fw[4], fx[4][NB];
+    for (int t = 0; t < NT; ++t) {
+      float v[8];
+      load_vec(x + (size_t)min(t, p.Ttok - 1) * p.d_in + k, v);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      fw[u] = frag_at(w, k + u * 32, kc, k1);
+      for (int q = 0; q < 8; ++q) acc[t] = fmaf(a[q], v[q], acc[t]);
+    }
+  }
+  const int nlow = p.n > 0 ? p.Ttok * p.r : 0;
+  for (int i = wave; i < nlow; i += ONE_WAVES) {
+    const int t = i / p.r, id = __builtin_amdgcn_readfirstlane(id_of(p, t));
+    if (id < 0) continue;
+    const uint16_t* a = static_cast<const uint16_t*>(p.a) + ((size_t)id * p.r + i % p.r) * p.d_in;
+    float v = 0.f;
+#pragma unroll 4
+    for (int k = lane * 8; k < p.d_in; k += MOELB_WAVE * 8) {
+      float u[8], s[8];
+      load_vec(a + k, u);
+      load_vec(x + (size_t)t * p.d_in + k, s);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) fx[u][i] = frag_at(x[i], k + u * 32, kc, k1);
+      for (int q = 0; q < 8; ++q) v = fmaf(u[q], s[q], v);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[u], fx[u][i], acc[i], 0, 0, 0);
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, MOELB_WAVE);
+    if (lane == 0) low[i] = v * p.scale[id];
   }
-  // lane: token lane % 16 of block i, rows (lane / 16) * 4 ..
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int tok = i * 16 + (lane & 15);
-    part[wave][tok * 4 + ((lane >> 4) ^ ((tok >> 1) & 3))] = acc[i];
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) acc[t] += __shfl_xor(acc[t], o, MOELB_WAVE);
+    if (lane == 0) base[wave][t] = acc[t];
+  }
+  // the first 16 ranks of this thread's B rows, on their way while the sums meet
+  const uint16_t* b0 = static_cast<const uint16_t*>(p.b) + ((size_t)max(own, 0) * p.d_out + wrow(tj)) * p.r;
+  const uint16_t* b1 = static_cast<const uint16_t*>(p.b) + ((size_t)max(own, 0) * p.d_out + wrow(tj + 8)) * p.r;
+  float u0[2][8], u1[2][8];
+  if (own >= 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load_vec(b0 + min(h * 8, p.r - 8), u0[h]);
+      if (GU) load_vec(b1 + min(h * 8, p.r - 8), u1[h]);
+    }
   }
   __syncthreads();
-  // thread -> token, two rows: gate and up row j, or rows 2 j and 2 j + 1
-  for (int c = threadIdx.x; c < TOK * 8; c += MOELB_WAVE * FEW_WAVES) {
-    const int tok = c >> 3, j = c & 7, t = t0 + tok;
-    if (t >= p.Ttok) continue;
-    const int i0 = GU ? j : 2 * j, i1 = GU ? j + 8 : 2 * j + 1;
-    if (n0 + (GU ? j : 2 * j) >= out) continue;
-    float v0 = 0.f, v1 = 0.f;
-    const int sw = (tok >> 1) & 3;
+  if (!mine) return;
+  float v0 = base[tj][tt], v1 = GU ? base[tj + 8][tt] : 0.f;
+  if (own >= 0) {
+    const float* l = low + tt * p.r;
+    for (int k = 0; k < p.r; k += 8) {
+      if (k >= 16) {
+        load_vec(b0 + k, u0[0]);
+        if (GU) load_vec(b1 + k, u1[0]);
+      }
+      const bool h = k == 8;
 #pragma unroll
-    for (int q = 0; q < FEW_WAVES; ++q) {
-      const float* f = reinterpret_cast<const float*>(&part[q][tok * 4]);
-      v0 += f[((i0 >> 2) ^ sw) * 4 + (i0 & 3)];
-      v1 += f[((i1 >> 2) ^ sw) * 4 + (i1 & 3)];
-    }
-    const int id = id_of(p, t);
-    if (id >= 0) {
-      const uint16_t* low = static_cast<const uint16_t*>(p.low) + (size_t)t * p.r;
-      const uint16_t* b = static_cast<const uint16_t*>(p.b) + (size_t)id * p.d_out * p.r;
-      const uint16_t* b0 = b + (size_t)wrow(i0) * p.r;
-      const uint16_t* b1 = b + (size_t)wrow(i1) * p.r;
-      for (int k = 0; k < p.r; k += 8) {
-        float s[8], u[8], v[8];
-        load_vec(low + k, s);
-        load_vec(b0 + k, u);
-        load_vec(b1 + k, v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v0 = fmaf(s[q], u[q], v0);
-          v1 = fmaf(s[q], v[q], v1);
-        }
+      for (int q = 0; q < 8; ++q) {
+        v0 = fmaf(l[k + q], h ? u0[1][q] : u0[0][q], v0);
+        if (GU) v1 = fmaf(l[k + q], h ? u1[1][q] : u1[0][q], v1);
       }
     }
-    uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t * out + n0;
-    if (GU)
-      y[j] = f32_to_bf16(silu_f32(v0) * v1);
-    else
-      *reinterpret_cast<uint32_t*>(y + 2 * j) = bf16x2_pack(v0, v1);
   }
+  if (GU) v0 = silu_f32(v0) * v1;
+  static_cast<uint16_t*>(p.y)[(size_t)tt * out + n0 + tj] = f32_to_bf16(v0);
 }
 
 // ---------------------------------------------------------------- host
@@ -469,20 +680,66 @@ int launch_f32(AdapterArgs p, hipStream_t s) {
   return MOELB_OK;
 }
 
-template <int NB, bool GU>
-int launch_few(const AdapterArgs& p, hipStream_t s) {
+// Parts of k for few tokens: about a workgroup a compute unit, at least 256 wide
+// (twice as many cost more in partial sums than they gain).
+int few_splits(int d_in, int d_out) {
+  const int blocks = (d_out + 63) / 64, want = 256 / blocks, most = d_in / 256;
+  const int s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : s;
+}
+
+// Likewise for the low products of prompts.
+int low_splits(int T, int d_in) {
+  const int blocks = (T + LOW_TOK - 1) / LOW_TOK, want = 512 / blocks, most = d_in / 256;
+  const int s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : s;
+}
+
+bool one_launch(int T, int n, int r) { return T <= ONE_TOKENS && (n == 0 || T * r <= ONE_LOW); }
+
+template <int NT, bool GU>
+int launch_one(const AdapterArgs& p, hipStream_t s) {
   const int out = GU ? p.d_out / 2 : p.d_out, rows = GU ? 8 : 16;
-  hipLaunchKernelGGL((adapter_few_kernel<NB, GU>), dim3((out + rows - 1) / rows, (p.Ttok + 16 * NB - 1) / (16 * NB)),
-                     dim3(MOELB_WAVE * FEW_WAVES), 0, s, p);
+  hipLaunchKernelGGL((adapter_one_kernel<NT, GU>), dim3((out + rows - 1) / rows), dim3(MOELB_WAVE * ONE_WAVES), 0, s,
+                     p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
 
 template <bool GU>
-int launch_bf16(const AdapterArgs& p, hipStream_t s) {
-  if (p.Ttok <= 16) return launch_few<1, GU>(p, s);
-  if (p.Ttok <= 32) return launch_few<2, GU>(p, s);
-  if (p.Ttok <= FEW_TOKENS) return launch_few<4, GU>(p, s);
+int launch_few(AdapterArgs p, hipStream_t s) {
+  const int out = GU ? p.d_out / 2 : p.d_out;
+  if (one_launch(p.Ttok, p.n, p.r)) {
+    return p.Ttok == 1 ? launch_one<1, GU>(p, s) : p.Ttok == 2 ? launch_one<2, GU>(p, s) : launch_one<4, GU>(p, s);
+  }
+  p.splits = few_splits(p.d_in, p.d_out);
+  p.nbase = (p.d_out + 63) / 64 * p.splits;
+  const dim3 grid(p.nbase + (p.n > 0 ? (p.Ttok * p.r + 3) / 4 : 0));
+  if (p.Ttok <= 16)
+    hipLaunchKernelGGL(adapter_few_kernel<1>, grid, dim3(256), 0, s, p);
+  else if (p.Ttok <= 32)
+    hipLaunchKernelGGL(adapter_few_kernel<2>, grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL(adapter_few_kernel<4>, grid, dim3(256), 0, s, p);
+  MOELB_CHECK_LAUNCH();
+  const long long threads = (long long)p.Ttok * (GU ? out : out / 2);
+  hipLaunchKernelGGL((adapter_few_sum_kernel<GU>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+  MOELB_CHECK_LAUNCH();
+  return MOELB_OK;
+}
+
+template <bool GU>
+int launch_prompts(AdapterArgs p, hipStream_t s) {
+  if (p.n > 0) {
+    p.splits = low_splits(p.Ttok, p.d_in);
+    if (!moelb_allow_lds(adapter_low_tile_kernel, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL(adapter_low_tile_kernel, dim3((p.Ttok + LOW_TOK - 1) / LOW_TOK, p.splits, (p.r + 63) / 64),
+                       dim3(256), mt::lds_bytes<2>(), s, p);
+    MOELB_CHECK_LAUNCH();
+    const long long threads = (long long)p.Ttok * (p.r / 4);
+    hipLaunchKernelGGL(adapter_low_sum_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+    MOELB_CHECK_LAUNCH();
+  }
   const size_t tiles = (size_t)((p.Ttok + 255) / 256) * ((p.d_out + 255) / 256);
   return tiles >= 192 ? launch_tile<4, GU>(p, s) : launch_tile<2, GU>(p, s);
 }
@@ -491,7 +748,12 @@ int launch_bf16(const AdapterArgs& p, hipStream_t s) {
 
 extern "C" size_t moelb_adapter_projection_workspace_bytes(int T, int d_in, int d_out, int n, int r, int dtype) {
   if (T < 0 || d_in < 1 || d_out < 1 || n < 0 || r < 0 || !moelb_dtype_ok(dtype)) return 0;
-  return n > 0 ? moelb_align256((size_t)T * r * moelb_elem_bytes(dtype)) : 0;
+  const bool few = dtype == MOELB_BF16 && T <= FEW_TOKENS;
+  if (few && one_launch(T, n, r)) return 0;
+  // low, and behind it the partial sums of few tokens, or of low itself
+  const size_t low = n > 0 ? moelb_align256((size_t)T * r * (few ? 4 : moelb_elem_bytes(dtype))) : 0;
+  if (few) return low + (size_t)few_splits(d_in, d_out) * T * d_out * 4;
+  return low + (dtype == MOELB_BF16 && n > 0 && T > 0 ? (size_t)low_splits(T, d_in) * T * r * 4 : 0);
 }
 
 extern "C" int moelb_adapter_projection(const void* x, int T, int d_in, int d_out, int dtype, const void* w,
@@ -511,24 +773,23 @@ extern "C" int moelb_adapter_projection(const void* x, int T, int d_in, int d_ou
   const size_t need = moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype);
   if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < need)) return MOELB_EWORKSPACE;
   if (T == 0) return MOELB_OK;
-  AdapterArgs p = {x, w, ids, a, b, scale, ws, y, T, d_in, d_out, n, n > 0 ? r : 8, 0};
-  hipStream_t s = static_cast<hipStream_t>(stream);
   const bool bf = dtype == MOELB_BF16;
+  const size_t low = n > 0 ? moelb_align256((size_t)T * r * (bf && T <= FEW_TOKENS ? 4 : eb)) : 0;
+  AdapterArgs p = {};
+  p.x = x, p.w = w, p.ids = ids, p.a = a, p.b = b, p.scale = scale, p.low = ws;
+  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + low);
+  p.y = y;
+  p.Ttok = T, p.d_in = d_in, p.d_out = d_out, p.n = n, p.r = n > 0 ? r : 8;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (bf) {
+    if (T <= FEW_TOKENS) return gated ? launch_few<true>(p, s) : launch_few<false>(p, s);
+    return gated ? launch_prompts<true>(p, s) : launch_prompts<false>(p, s);
+  }
   if (n > 0) {
-    if (!bf || T <= FEW_TOKENS) {
-      const long long blocks = ((long long)T * r + 3) / 4;
-      if (blocks > 0x7fffffffll) return MOELB_EINVAL;
-      if (bf)
-        hipLaunchKernelGGL(adapter_low_rows_kernel<uint16_t>, dim3((unsigned)blocks), dim3(256), 0, s, p);
-      else
-        hipLaunchKernelGGL(adapter_low_rows_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, s, p);
-    } else {
-      const int slots = n < LOW_TOK ? n : LOW_TOK;
-      hipLaunchKernelGGL(adapter_low_tile_kernel, dim3((T + LOW_TOK - 1) / LOW_TOK, slots, (r + 63) / 64),
-                         dim3(MOELB_WAVE * LOW_WAVES), 0, s, p);
-    }
+    const long long blocks = ((long long)T * r + 3) / 4;
+    if (blocks > 0x7fffffffll) return MOELB_EINVAL;
+    hipLaunchKernelGGL(adapter_low_rows_f32_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p);
     MOELB_CHECK_LAUNCH();
   }
-  if (!bf) return gated ? launch_f32<true>(p, s) : launch_f32<false>(p, s);
-  return gated ? launch_bf16<true>(p, s) : launch_bf16<false>(p, s);
+  return gated ? launch_f32<true>(p, s) : launch_f32<false>(p, s);
 }

@@ -413,7 +413,7 @@ def moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype) -> int
 
 
 def moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=False, stream=None):
-    """y = x w^T plus each token's adapter; ids, a, b, scale and ws None: the bare projection."""
+    """y = x w^T plus each token's adapter; ids, a, b and scale None: the bare projection."""
     name = "moelb_adapter_projection"
     dev = _device(name, x)
     T, d_in = x.shape
@@ -422,8 +422,8 @@ def moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=False, stream=
     n = r = 0
     if a is not None:
         n, r = a.shape[0], a.shape[1]
-        if ids is None or b is None or scale is None or ws is None:
-            raise MoelbError(f"{name}: adapters need ids, a, b, scale and ws")
+        if ids is None or b is None or scale is None:
+            raise MoelbError(f"{name}: adapters need ids, a, b and scale")
     pws, nws = _workspace(name, ws, dev)
     _check(lib().moelb_adapter_projection(_arg(name, "x", x, (T, d_in), t, dev), T, d_in, d_out, dtype_code(x),
                                           _arg(name, "w", w, (d_out, d_in), t, dev),

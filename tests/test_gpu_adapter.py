@@ -34,11 +34,9 @@ def run(x, w, ids, a, b, scale, gated):
     T, d_in = x.shape
     d_out = w.shape[0]
     y = torch.full((T, d_out // 2 if gated else d_out), 7.0, dtype=x.dtype, device="cuda")
-    ws = None
-    if a is not None:
-        ws = torch.full((M.moelb_adapter_projection_workspace_bytes(T, d_in, d_out, a.shape[0], a.shape[1],
-                                                                    M.dtype_code(x)),), 0xff, dtype=torch.uint8,
-                        device="cuda")
+    n, r = a.shape[:2] if a is not None else (0, 0)
+    ws = torch.full((M.moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, M.dtype_code(x)),), 0xff,
+                    dtype=torch.uint8, device="cuda")
     M.moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=gated)
     torch.cuda.synchronize()
     return y
@@ -78,7 +76,8 @@ def check(x, w, ids, a, b, scale, gated, y):
 
 SHAPES = [
     # T, d_in, d_out, n, r
-    (1, 8, 16, 1, 8), (1, 2048, 2048, 8, 16), (2, 72, 80, 3, 24), (16, 264, 48, 5, 16), (17, 200, 208, 40, 8),
+    (1, 8, 16, 1, 8), (1, 2048, 2048, 8, 16), (4, 264, 272, 3, 16), (3, 1000, 528, 2, 8), (1, 136, 48, 2, 64),
+    (2, 520, 80, 5, 32), (1, 264, 272, 3, 72), (5, 4096, 144, 2, 16), (2, 72, 80, 3, 24), (16, 264, 48, 5, 16), (17, 200, 208, 40, 8),
     (33, 1000, 528, 64, 32), (64, 4096, 512, 64, 16), (65, 136, 144, 7, 64), (100, 512, 272, 9, 40),
     (129, 328, 272, 3, 72), (300, 264, 1040, 50, 256), (700, 520, 1040, 5, 128), (513, 64, 64, 2048, 8),
 ]

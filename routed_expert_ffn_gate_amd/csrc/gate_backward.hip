@@ -8,14 +8,17 @@
 //   dz_e = p_e (q_e - S), S = sum_f p_f q_f
 //   dh = dz W, dW = sum_t dz h[t]^T, db = sum_t dz
 //
-// Four steps on the tile of mfma_tile.h:
-//   1. z (fp32), h and W both read along d
-//   2. a wave per token: softmax, q from the token's k ids, dz in the storage
-//      type (E padded to 64 with zeros), db partials per workgroup
-//   3. dh = dz W (W read as columns, the sum runs over its rows) and dW = dz^T h
-//      (both read as columns, the sum runs over tokens, cut into parts), one
-//      launch
-//   4. the parts of dW and db, added in order
+// On the tile of mfma_tile.h (bf16; fp32 on its fp32 tile):
+//   1. z = h W^T, both read along d; up to 128 experts a tile holds whole rows
+//      of z, so its epilogue goes on to dz and z never leaves LDS
+//   2. dz: softmax, q from the token's k ids, dz in the storage type (E padded
+//      to 64 with zeros), db partials per workgroup
+//   3. dW = dz^T h (both read as columns, the sum runs over tokens, cut into
+//      parts)
+//   4. dh = dz W: a workgroup keeps its tokens' dz in registers and streams
+//      tiles of W (read as columns) past them, storing as it goes; the bytes of
+//      dh bound it
+//   5. the parts of dW and db, added in order
 #include "mfma_tile.h"
 
 namespace {
@@ -58,6 +61,118 @@ __global__ __launch_bounds__(mt::THREADS) void gate_logits_kernel(GateArgs<uint1
   mt::drain<GF, false>(lds, acc, [&](int r, int c, const float* v) {
     if (m0 + r < p.Ttok && n0 + c < p.Ep) mt::store8(p.z + (size_t)(m0 + r) * p.Ep + n0 + c, v);
   });
+}
+
+// A row operand whose K steps start at step `first` of n and wrap.  Rows a
+// multiple of 4 KiB apart have the same k on the same memory channel, so
+// workgroups that all read k = 0, then k = 64, ... queue there; started at
+// different steps they spread over the channels.
+struct TurnedRowOp {
+  static constexpr bool COL = false;
+  mt::RowOp<GF> own;
+  int first, n;
+  __device__ __forceinline__ void begin(int) {}
+  __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
+    t += first;
+    own.issue(t < n ? t : t - n, j, m0);
+  }
+};
+
+// All-reduce over 16 neighbouring lanes by row rotations.
+template <class Op>
+__device__ __forceinline__ float row_reduce(float v, Op op) {
+  auto ror = [](float x, auto n) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x120 + decltype(n)::value, 0xf, 0xf, true));
+  };
+  v = op(v, ror(v, std::integral_constant<int, 8>{}));
+  v = op(v, ror(v, std::integral_constant<int, 4>{}));
+  v = op(v, ror(v, std::integral_constant<int, 2>{}));
+  return op(v, ror(v, std::integral_constant<int, 1>{}));
+}
+
+// Steps 1 and 2 for Ep <= 128: 128 tokens a workgroup.  The logits go through
+// LDS (fp32, 16-byte chunks XORed with the row); then 16 lanes take a row, 8
+// experts a lane, 16 rows at a time.
+__global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t> p) {
+  extern __shared__ __align__(16) char smem[];
+  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+  const int m0 = blockIdx.x * GB;
+  {
+    TurnedRowOp oa, ob;
+    oa.own.init(p.h, bytes32((size_t)p.Ttok * p.d * 2), p.d, p.d, [&](int r) { return min(m0 + r, p.Ttok - 1); });
+    ob.own.init(p.w, bytes32((size_t)p.E * p.d * 2), p.d, p.d, [&](int r) { return min(r, p.E - 1); });
+    oa.n = ob.n = (p.d + mt::BK - 1) / mt::BK;
+    oa.first = ob.first = blockIdx.x % oa.n;
+    f32x16_t acc[GF][GF];
+    mt::k_loop<GF, false>(lds, oa, ob, oa.n, acc);
+    mt::stage<GF, false, 0>(lds, acc);
+  }
+  const float* st = reinterpret_cast<const float*>(smem);
+  const int tid = threadIdx.x, lane = tid & 63, s = tid & 15, c = s * 8;
+  float bias[8], db[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bias[i] = c + i < p.E ? p.b[c + i] : 0.f;
+    db[i] = 0.f;
+  }
+  __syncthreads();
+  for (int pass = 0; pass < GB / 16; ++pass) {
+    const int r = pass * 16 + (tid >> 4), t = m0 + r;
+    const bool on = t < p.Ttok;
+    const int id = on && s < p.k ? p.idx[(size_t)t * p.k + s] : -1;
+    const float g = on && s < p.k ? p.dwts[(size_t)t * p.k + s] : 0.f;
+    float z[8], q[8];
+    float m = -INFINITY, sum = 0.f, pq = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + r * GB + (((2 * s + h) ^ (r & 15)) * 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[h * 4 + i] = x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] = c + i < p.E ? z[i] + bias[i] : -INFINITY;
+      m = fmaxf(m, z[i]);
+      q[i] = 0.f;
+    }
+    m = row_reduce(m, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] = c + i < p.E ? __expf(z[i] - m) : 0.f;
+      sum += z[i];
+    }
+    sum = 1.0f / row_reduce(sum, [](float a, float b) { return a + b; });
+    for (int j = 0; j < p.k; ++j) {
+      const int e = __shfl(id, (lane & 48) + j, 64) - c;
+      const float gj = __shfl(g, (lane & 48) + j, 64);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] += e == i ? gj : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] *= sum;
+      pq += z[i] * q[i];
+    }
+    pq = row_reduce(pq, [](float a, float b) { return a + b; });
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] = on && c + i < p.E ? z[i] * (q[i] - pq) : 0.f;
+      db[i] += z[i];
+    }
+    if (on && c < p.Ep) mt::store8(p.dz + (size_t)t * p.Ep + c, z);
+  }
+  // db: 16 rows' lanes per expert, added in order
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[(tid >> 4) * GB + c + i] = db[i];
+  __syncthreads();
+  if (tid < p.Ep) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += part[i * GB + tid];
+    p.pdb[(size_t)blockIdx.x * p.Ep + tid] = v;
+  }
 }
 
 __global__ __launch_bounds__(mt::THREADS) void gate_logits_f32_kernel(GateArgs<float> p) {
@@ -179,28 +294,114 @@ __device__ __forceinline__ void dw_part(const GateArgs<T>& p, int b, int B, int&
   n = min(p.Ttok, k0 + ps) - k0;
 }
 
-__global__ __launch_bounds__(mt::THREADS) void gate_grads_kernel(GateArgs<uint16_t> p) {
+__global__ __launch_bounds__(mt::THREADS) void gate_dw_kernel(GateArgs<uint16_t> p) {
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
   f32x16_t acc[GF][GF];
-  if ((int)blockIdx.x < p.nh) {
-    const int ntn = (p.d + GB - 1) / GB;
-    const int m0 = blockIdx.x / ntn * GB, n0 = blockIdx.x % ntn * GB;
-    mt::RowOp<GF> oa;
-    mt::ColOp<GF, false> ob;
-    oa.init(p.dz, bytes32((size_t)p.Ttok * p.Ep * 2), p.Ep, p.Ep, [&](int r) { return min(m0 + r, p.Ttok - 1); });
-    ob.init(p.w, bytes32((size_t)p.E * p.d * 2), p.d, p.E, n0, p.d);
-    mt::k_loop<GF, false>(lds, oa, ob, p.Ep / mt::BK, acc);
-    mt::drain<GF, false>(lds, acc, [&](int r, int c, const float* v) { put_dh(p, m0 + r, n0 + c, v); });
-    return;
-  }
   int mi, ni, split, k0, n;
-  dw_part(p, blockIdx.x - p.nh, GB, mi, ni, split, k0, n);
+  dw_part(p, blockIdx.x, GB, mi, ni, split, k0, n);
   mt::ColOp<GF, false> oa, ob;
   oa.init(p.dz + (size_t)k0 * p.Ep, bytes32((size_t)n * p.Ep * 2), p.Ep, n, mi * GB, p.Ep);
   ob.init(p.h + (size_t)k0 * p.d, bytes32((size_t)n * p.d * 2), p.d, n, ni * GB, p.d);
   mt::k_loop<GF, false>(lds, oa, ob, max(1, (n + mt::BK - 1) / mt::BK), acc);
   mt::drain<GF, false>(lds, acc, [&](int r, int c, const float* v) { put_dw(p, split, mi * GB + r, ni * GB + c, v); });
+}
+
+// dh for 128 tokens and every gridDim.y-th 128-column tile.  Wave (wm, wn): 64
+// tokens, whose dz it keeps as fragments, x 64 columns.  A tile of W (Ep rows
+// x 128 columns, KB half-stages) is loaded NBUF - 1 tiles ahead.  The wait at
+// its use lets as many later operations be outstanding as one tile has loads:
+// later are at least those, so the tile itself has landed, however many stores
+// lie between.  The two lane halves trade 4-column runs, so that a lane stores
+// 8 adjacent columns of its token.
+template <int KB>
+__global__ __launch_bounds__(mt::THREADS) void gate_dh_kernel(GateArgs<uint16_t> p) {
+  constexpr int NBUF = KB <= 3 ? 3 : 2;
+  constexpr int HALF = mt::half_elems<GF>(), TILE = KB * HALF, NI = 2 * GF;
+  extern __shared__ __align__(16) char smem[];
+  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+  const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fh = lane >> 5;
+  const int m0 = blockIdx.x * GB + wm * 64;
+  const int ntn = (p.d + GB - 1) / GB, n = (ntn - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
+  const uint32_t bytes = bytes32((size_t)p.E * p.d * 2);
+  // the tiles in turn, each workgroup from another one on (the same columns of
+  // rows 4 KiB apart lie on one memory channel)
+  auto col = [&](int i) { return ((int)blockIdx.y + (i + (int)blockIdx.x) % n * (int)gridDim.y) * GB; };
+  auto issue = [&](int i) {
+    mt::ColOp<GF, false> ob;
+    ob.init(p.w, bytes, p.d, p.E, col(i), p.d);
+#pragma unroll
+    for (int h = 0; h < KB; ++h)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        ob.issue(h, j, lds_u32 + (uint32_t)((i % NBUF) * TILE + h * HALF + (wave * NI + j) * 512) * 2u);
+  };
+  bf16x8_t fa[2][KB * 4];
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi) {
+    const uint16_t* row = p.dz + (size_t)min(m0 + mi * 32 + fr, p.Ttok - 1) * p.Ep + fh * 8;
+#pragma unroll
+    for (int k = 0; k < KB * 4; ++k) fa[mi][k] = *reinterpret_cast<const bf16x8_t*>(row + k * 16);
+  }
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+    for (int k = 0; k < KB * 4; ++k) asm volatile("" : "+v"(fa[mi][k]));  // landed before the first DMA
+  mt::FragAt<GF, true> fb;
+  fb.init(wn, 0);
+  for (int i = 0; i < NBUF - 1 && i < n; ++i) issue(i);
+  for (int i = 0; i < n; ++i) {
+    if (NBUF == 3 && i + 1 < n)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(KB * NI) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (i + NBUF - 1 < n) issue(i + NBUF - 1);
+    f32x16_t acc[2][2];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[mi][ni][q] = 0.f;
+#pragma unroll
+    for (int h = 0; h < KB; ++h) {
+      const uint16_t* half = lds + (i % NBUF) * TILE + h * HALF;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int ni = 0; ni < 2; ++ni) {
+          const bf16x8_t f = fb.read(half, k, ni, 0);
+#pragma unroll
+          for (int mi = 0; mi < 2; ++mi)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, fa[mi][h * 4 + k], acc[mi][ni], 0, 0, 0);
+        }
+    }
+    const int c0 = col(i) + wn * 64 + fh * 8;
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi) {
+      const int t = m0 + mi * 32 + fr;
+      uint16_t* o = p.dh + (size_t)min(t, p.Ttok - 1) * p.d + c0;
+#pragma unroll
+      for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const f32x16_t& a = acc[mi][ni];
+          uint32_t x0 = bf16x2_pack(a[q * 4], a[q * 4 + 1]), x1 = bf16x2_pack(a[q * 4 + 2], a[q * 4 + 3]);
+          uint32_t y0 = bf16x2_pack(a[q * 4 + 4], a[q * 4 + 5]), y1 = bf16x2_pack(a[q * 4 + 6], a[q * 4 + 7]);
+          // lane halves: columns 8q + 0..3 | 4..7 and 8q + 8..11 | 12..15
+          const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+          const int c = ni * 32 + q * 8;
+          if (t < p.Ttok && c0 + c < p.d)
+            *reinterpret_cast<uint4*>(o + c) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+        }
+    }
+  }
 }
 
 __global__ __launch_bounds__(mt::THREADS) void gate_grads_f32_kernel(GateArgs<float> p) {
@@ -256,15 +457,19 @@ __global__ __launch_bounds__(256) void gate_sums_kernel(GateArgs<T> p, int nw) {
 struct GateLayout {
   size_t z, dz, pdb, pdw, total;
   int Ep, blocks, splits;
+  bool fused;
 };
 GateLayout gate_layout(int T, int d, int E, int dtype) {
   GateLayout l;
   const size_t eb = moelb_elem_bytes(dtype);
   l.Ep = (E + 63) & ~63;
-  // step 2: 16 tokens a workgroup, at most 1024 of them
-  l.blocks = (T + 15) / 16;
-  l.blocks = l.blocks < 1 ? 1 : l.blocks > 1024 ? 1024 : l.blocks;
-  // dW: parts of at least 256 tokens, enough for two workgroups a CU
+  // db partials: one a 128-token tile (bf16, E <= 128), else 16 tokens a
+  // workgroup, at most 1024 of them
+  l.fused = dtype == MOELB_BF16 && l.Ep <= GB;
+  l.blocks = l.fused ? (T + GB - 1) / GB : (T + 15) / 16;
+  l.blocks = l.blocks < 1 ? 1 : !l.fused && l.blocks > 1024 ? 1024 : l.blocks;
+  // dW: parts of at least 256 tokens, about a workgroup a compute unit (bf16:
+  // they run beside nothing else, so two)
   const int B = dtype == MOELB_BF16 ? GB : 64;
   const int tiles = ((d + B - 1) / B) * ((E + B - 1) / B);
   const int want = 512 / tiles, most = T / 256;
@@ -298,37 +503,76 @@ int launch_softmax(const GateArgs<T>& p, hipStream_t s) {
   return MOELB_OK;
 }
 
-template <typename T>
-int run(GateArgs<T> p, hipStream_t s) {
-  constexpr bool BF = sizeof(T) == 2;
-  constexpr int B = BF ? GB : 64;
-  if constexpr (BF) {
-    if (!moelb_allow_lds(gate_logits_kernel, mt::lds_bytes<GF>()) ||
-        !moelb_allow_lds(gate_grads_kernel, mt::lds_bytes<GF>()))
-      return MOELB_ELAUNCH;
+template <int KB>
+int launch_dh(const GateArgs<uint16_t>& p, hipStream_t s) {
+  constexpr size_t lds = (size_t)(KB <= 3 ? 3 : 2) * KB * mt::half_elems<GF>() * sizeof(uint16_t);
+  if (!moelb_allow_lds(gate_dh_kernel<KB>, lds)) return MOELB_ELAUNCH;
+  const int m = (p.Ttok + GB - 1) / GB, ntn = (p.d + GB - 1) / GB;
+  int parts = (512 + m - 1) / m;  // about two workgroups a compute unit where there are few tokens
+  if (m >= 256) parts = 1;
+  hipLaunchKernelGGL((gate_dh_kernel<KB>), dim3(m, parts < ntn ? parts : ntn), dim3(mt::THREADS), lds, s, p);
+  MOELB_CHECK_LAUNCH();
+  return MOELB_OK;
+}
+
+int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
+  constexpr size_t lds = mt::lds_bytes<GF>();
+  if (p.Ttok > 0 && fused) {
+    if (!moelb_allow_lds(gate_dz_kernel, lds)) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL(gate_dz_kernel, dim3(p.blocks), dim3(mt::THREADS), lds, s, p);
+    MOELB_CHECK_LAUNCH();
+  } else {
+    if (p.Ttok > 0) {
+      if (!moelb_allow_lds(gate_logits_kernel, lds)) return MOELB_ELAUNCH;
+      hipLaunchKernelGGL(gate_logits_kernel, dim3((p.Ttok + GB - 1) / GB, (p.E + GB - 1) / GB), dim3(mt::THREADS), lds,
+                         s, p);
+      MOELB_CHECK_LAUNCH();
+    }
+    const int st = launch_softmax(p, s);
+    if (st != MOELB_OK) return st;
   }
+  if (p.dw) {
+    if (!moelb_allow_lds(gate_dw_kernel, lds)) return MOELB_ELAUNCH;
+    const int tiles = ((p.E + GB - 1) / GB) * ((p.d + GB - 1) / GB);
+    hipLaunchKernelGGL(gate_dw_kernel, dim3(tiles * p.splits), dim3(mt::THREADS), lds, s, p);
+    MOELB_CHECK_LAUNCH();
+  }
+  if (!p.dh || p.Ttok == 0) return MOELB_OK;
+  switch (p.Ep / 64) {
+    case 1:
+      return launch_dh<1>(p, s);
+    case 2:
+      return launch_dh<2>(p, s);
+    case 3:
+      return launch_dh<3>(p, s);
+    default:
+      return launch_dh<4>(p, s);
+  }
+}
+
+int run(GateArgs<float> p, bool, hipStream_t s) {
   if (p.Ttok > 0) {
-    const dim3 grid((p.Ttok + B - 1) / B, (p.E + B - 1) / B);
-    if constexpr (BF)
-      hipLaunchKernelGGL(gate_logits_kernel, grid, dim3(mt::THREADS), mt::lds_bytes<GF>(), s, p);
-    else
-      hipLaunchKernelGGL(gate_logits_f32_kernel, grid, dim3(mt::THREADS), 0, s, p);
+    hipLaunchKernelGGL(gate_logits_f32_kernel, dim3((p.Ttok + 63) / 64, (p.E + 63) / 64), dim3(mt::THREADS), 0, s, p);
     MOELB_CHECK_LAUNCH();
   }
   const int st = launch_softmax(p, s);
   if (st != MOELB_OK) return st;
-  const size_t ntn = (p.d + B - 1) / B;
-  const size_t nh = p.dh && p.Ttok > 0 ? (size_t)((p.Ttok + B - 1) / B) * ntn : 0;
-  const size_t nw = p.dw ? (size_t)((p.E + B - 1) / B) * ntn * p.splits : 0;
+  const size_t ntn = (p.d + 63) / 64;
+  const size_t nh = p.dh && p.Ttok > 0 ? (size_t)((p.Ttok + 63) / 64) * ntn : 0;
+  const size_t nw = p.dw ? (size_t)((p.E + 63) / 64) * ntn * p.splits : 0;
   if (nh + nw > 0x7fffffffull) return MOELB_EINVAL;
   p.nh = (int)nh;
   if (nh + nw > 0) {
-    if constexpr (BF)
-      hipLaunchKernelGGL(gate_grads_kernel, dim3((unsigned)(nh + nw)), dim3(mt::THREADS), mt::lds_bytes<GF>(), s, p);
-    else
-      hipLaunchKernelGGL(gate_grads_f32_kernel, dim3((unsigned)(nh + nw)), dim3(mt::THREADS), 0, s, p);
+    hipLaunchKernelGGL(gate_grads_f32_kernel, dim3((unsigned)(nh + nw)), dim3(mt::THREADS), 0, s, p);
     MOELB_CHECK_LAUNCH();
   }
+  return MOELB_OK;
+}
+
+template <typename T>
+int run_all(const GateArgs<T>& p, bool fused, hipStream_t s) {
+  const int st = run(p, fused, s);
+  if (st != MOELB_OK) return st;
   const int sw = p.dw && p.splits > 1 ? (int)(((size_t)p.E * p.d / 8 + 255) / 256) : 0;
   const int sb = p.db ? (p.E + 3) / 4 : 0;
   if (sw + sb > 0) {
@@ -375,7 +619,7 @@ extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, in
     p.dw = static_cast<U*>(dw);
     p.db = db;
     p.Ttok = T, p.d = d, p.E = E, p.Ep = l.Ep, p.k = k, p.splits = l.splits, p.blocks = l.blocks;
-    return run<U>(p, static_cast<hipStream_t>(stream));
+    return run_all<U>(p, l.fused && T > 0, static_cast<hipStream_t>(stream));
   };
   return dtype == MOELB_BF16 ? go(static_cast<uint16_t*>(nullptr)) : go(static_cast<float*>(nullptr));
 }

@@ -348,59 +348,67 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
 #undef MT_DST
 }
 
+// Row blocks 2 RD, 2 RD + 1 of every wave (128 rows) from the accumulators into
+// LDS as fp32: staging row r, 16-byte chunk c at c ^ (r & 15), so that the
+// writes (32 rows, one chunk) and the reads (one row, consecutive chunks) are
+// both free of bank conflicts.  Every wave is past its K loop afterwards; the
+// caller synchronises before it reads.
+template <int F, bool GU, int RD>
+__device__ __forceinline__ void stage(uint16_t* lds, const f32x16_t (&acc)[F][F]) {
+  constexpr int B = 64 * F;
+  float* st = reinterpret_cast<float*>(lds);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int fr = lane & 31, fh = lane >> 5;
+  __syncthreads();
+#pragma unroll
+  for (int m2 = 0; m2 < 2; ++m2) {
+    const int row = wm * 64 + m2 * 32 + fr;
+#pragma unroll
+    for (int ni = 0; ni < F; ++ni)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c4 = (block_col<F, GU>(wn, ni) + q * 8 + fh * 4) / 4;
+        const f32x16_t& a = acc[2 * RD + m2][ni];
+        const f32x4_t v = {a[q * 4], a[q * 4 + 1], a[q * 4 + 2], a[q * 4 + 3]};
+        *reinterpret_cast<f32x4_t*>(st + row * B + ((c4 ^ (row & 15)) * 4)) = v;
+      }
+  }
+}
+
 // After the K loop: the tile leaves the accumulators through LDS as fp32, 128
 // rows at a time, and store(row, col, v) gets 8 adjacent columns of a row; with
 // GU, store(row, col, gate, up) gets the matching 8 columns of both halves.
-// 16-byte chunks are XORed with the row, so the writes (32 rows, one chunk) and
-// the reads (one row, consecutive chunks) are both free of bank conflicts.
-template <int F, bool GU, class Store>
+template <int F, bool GU, int RD = 0, class Store>
 __device__ __forceinline__ void drain(uint16_t* lds, const f32x16_t (&acc)[F][F], Store store) {
   constexpr int B = 64 * F;
-  float* st = reinterpret_cast<float*>(lds);
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  const int fr = lane & 31, fh = lane >> 5;
+  const float* st = reinterpret_cast<const float*>(lds);
+  stage<F, GU, RD>(lds, acc);
+  __syncthreads();
+  constexpr int W = GU ? B / 2 : B;  // columns a row gives out
+  for (int c = threadIdx.x; c < 128 * (W / 8); c += THREADS) {
+    const int row = c / (W / 8), col = (c % (W / 8)) * 8;
+    const int tr = (row >> 6) * 32 * F + RD * 64 + (row & 63);  // row of the tile
+    auto get = [&](int col_, float* v) {
 #pragma unroll
-  for (int rd = 0; rd < F / 2; ++rd) {
-    __syncthreads();
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + row * B + (((col_ / 4 + h) ^ (row & 15)) * 4));
 #pragma unroll
-    for (int m2 = 0; m2 < 2; ++m2) {
-      const int row = wm * 64 + m2 * 32 + fr;
-#pragma unroll
-      for (int ni = 0; ni < F; ++ni)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c4 = (block_col<F, GU>(wn, ni) + q * 8 + fh * 4) / 4;
-          const f32x16_t& a = acc[2 * rd + m2][ni];
-          const f32x4_t v = {a[q * 4], a[q * 4 + 1], a[q * 4 + 2], a[q * 4 + 3]};
-          *reinterpret_cast<f32x4_t*>(st + row * B + ((c4 ^ (row & 15)) * 4)) = v;
-        }
-    }
-    __syncthreads();
-    constexpr int W = GU ? B / 2 : B;  // columns a row gives out
-    for (int c = tid; c < 128 * (W / 8); c += THREADS) {
-      const int row = c / (W / 8), col = (c % (W / 8)) * 8;
-      const int tr = (row >> 6) * 32 * F + rd * 64 + (row & 63);  // row of the tile
-      auto get = [&](int col_, float* v) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + row * B + (((col_ / 4 + h) ^ (row & 15)) * 4));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[h * 4 + i] = x[i];
-        }
-      };
-      float v[8];
-      get(col, v);
-      if constexpr (GU) {
-        float u[8];
-        get(col + B / 2, u);
-        store(tr, col, v, u);
-      } else {
-        store(tr, col, v);
+        for (int i = 0; i < 4; ++i) v[h * 4 + i] = x[i];
       }
+    };
+    float v[8];
+    get(col, v);
+    if constexpr (GU) {
+      float u[8];
+      get(col + B / 2, u);
+      store(tr, col, v, u);
+    } else {
+      store(tr, col, v);
     }
   }
+  if constexpr (RD + 1 < F / 2) drain<F, GU, RD + 1>(lds, acc, store);
 }
 
 // Eight values to memory in the storage type (each rounded once, to nearest even).

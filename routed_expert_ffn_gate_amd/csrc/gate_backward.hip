@@ -63,21 +63,6 @@ __global__ __launch_bounds__(mt::THREADS) void gate_logits_kernel(GateArgs<uint1
   });
 }
 
-// A row operand whose K steps start at step `first` of n and wrap.  Rows a
-// multiple of 4 KiB apart have the same k on the same memory channel, so
-// workgroups that all read k = 0, then k = 64, ... queue there; started at
-// different steps they spread over the channels.
-struct TurnedRowOp {
-  static constexpr bool COL = false;
-  mt::RowOp<GF> own;
-  int first, n;
-  __device__ __forceinline__ void begin(int) {}
-  __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
-    t += first;
-    own.issue(t < n ? t : t - n, j, m0);
-  }
-};
-
 // All-reduce over 16 neighbouring lanes by row rotations.
 template <class Op>
 __device__ __forceinline__ float row_reduce(float v, Op op) {
@@ -98,13 +83,12 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
   const int m0 = blockIdx.x * GB;
   {
-    TurnedRowOp oa, ob;
-    oa.own.init(p.h, bytes32((size_t)p.Ttok * p.d * 2), p.d, p.d, [&](int r) { return min(m0 + r, p.Ttok - 1); });
-    ob.own.init(p.w, bytes32((size_t)p.E * p.d * 2), p.d, p.d, [&](int r) { return min(r, p.E - 1); });
-    oa.n = ob.n = (p.d + mt::BK - 1) / mt::BK;
-    oa.first = ob.first = blockIdx.x % oa.n;
+    mt::RowOp<GF> oa, ob;
+    oa.init(p.h, bytes32((size_t)p.Ttok * p.d * 2), p.d, p.d, [&](int r) { return min(m0 + r, p.Ttok - 1); });
+    ob.init(p.w, bytes32((size_t)p.E * p.d * 2), p.d, p.d, [&](int r) { return min(r, p.E - 1); });
+    const int KT = (p.d + mt::BK - 1) / mt::BK;
     f32x16_t acc[GF][GF];
-    mt::k_loop<GF, false>(lds, oa, ob, oa.n, acc);
+    mt::k_loop<GF, false>(lds, oa, ob, KT, acc, blockIdx.x % KT);
     mt::stage<GF, false, 0>(lds, acc);
   }
   const float* st = reinterpret_cast<const float*>(smem);

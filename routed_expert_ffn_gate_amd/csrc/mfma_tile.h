@@ -223,12 +223,16 @@ __device__ __forceinline__ int block_col(int wn, int ni) {
   return GU ? wn * 16 * F + (ni % (F / 2)) * 32 + (ni / (F / 2)) * 32 * F : wn * 32 * F + ni * 32;
 }
 
-// The K loop: acc[mi][ni] += A block mi x B block ni over KT >= 1 steps.
+// The K loop: acc[mi][ni] += A block mi x B block ni over KT >= 1 steps, from
+// step `turn` (< KT) on and around.  Rows a multiple of 4 KiB apart have the
+// same k on the same memory channel: workgroups that all read k = 0, then k =
+// 64, ... queue there, started at different steps they spread over the
+// channels (a gathered operand takes its steps in order: turn = 0).
 // acc holds each 32x32 block transposed (the B fragment is the MFMA's first
 // operand): lane -> row lane % 32 of block mi, element j -> column (j / 4) * 8 +
 // (lane / 32) * 4 + j % 4 of block ni.
 template <int F, bool GU, class OA, class OB>
-__device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f32x16_t (&acc)[F][F]) {
+__device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f32x16_t (&acc)[F][F], int turn = 0) {
   constexpr int HALF = half_elems<F>();
   constexpr int NI = 2 * F;  // DMA instructions per half-stage and wave
   const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
@@ -246,14 +250,16 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
       for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
   const int nh = 2 * KT;
   KT = __builtin_amdgcn_readfirstlane(KT);
+  turn = __builtin_amdgcn_readfirstlane(turn);
 #define MT_DST(SLOT, JJ) (lds_u32 + (uint32_t)(((SLOT) * HALF + (wave * NI + (JJ)) * 512) * 2))
 #define MT_ISSUE(J, JJ)                                             \
   {                                                                 \
     const int j_ = (J);                                             \
+    const int t_ = (j_ >> 1) + turn;                                \
     if (j_ & 1)                                                     \
-      ob.issue(j_ >> 1, (JJ), MT_DST(j_ % SLOTS, JJ));              \
+      ob.issue(t_ < KT ? t_ : t_ - KT, (JJ), MT_DST(j_ % SLOTS, JJ)); \
     else                                                            \
-      oa.issue(j_ >> 1, (JJ), MT_DST(j_ % SLOTS, JJ));              \
+      oa.issue(t_ < KT ? t_ : t_ - KT, (JJ), MT_DST(j_ % SLOTS, JJ)); \
   }
 #define MT_RA(SA, KS, I) fa.read((SA), (KS), (I), (I) * 32)
 #define MT_RB(SB, KS, I) fb.read((SB), (KS), (I), block_col<F, GU>(0, I))

@@ -15,6 +15,13 @@ The hidden-state rows are read by the gate/up GEMM straight from ``h``
 through the permutation (``gather_rows=True``, the default; the permutation
 then moves indices only), or from a materialised ``x_perm``
 (``gather_rows=False``).  ``materialize_x`` only allocates ``x_perm``.
+
+Training: ``step(..., train=True)`` runs the same step with the FFN's
+projections kept, and ``backward`` returns the gradients of its output with
+respect to the hidden states, the router and the experts (shared expert
+included).  Serving requests with adapters of their own: ``step(...,
+shared_adapters=...)`` runs the shared expert's two projections with each
+token's low-rank adapters beside them.
 """
 from __future__ import annotations
 
@@ -107,6 +114,33 @@ class StepOut:
     home_next: Optional[torch.Tensor] = None  # FreeBalance: the next layer's placement
 
 
+@dataclass
+class SharedAdapters:
+    """Low-rank adapters beside the shared expert's projections: n adapters of
+    rank r13 (gate and up) and r2 (down), and the adapter of every token
+    (outside [0, n): none)."""
+    ids: torch.Tensor       # [T] int32
+    a13: torch.Tensor       # [n, r13, d]
+    b13: torch.Tensor       # [n, 2 * shared_inter, r13]
+    scale13: torch.Tensor   # [n] fp32
+    a2: torch.Tensor        # [n, r2, shared_inter]
+    b2: torch.Tensor        # [n, d, r2]
+    scale2: torch.Tensor    # [n] fp32
+
+
+@dataclass
+class Gradients:
+    """Gradients of one step's output, in the layer's buffers (overwritten by
+    the next ``backward``)."""
+    h: torch.Tensor
+    w_cur: torch.Tensor
+    b_cur: torch.Tensor
+    w13: torch.Tensor
+    w2: torch.Tensor
+    shared_w13: Optional[torch.Tensor]
+    shared_w2: Optional[torch.Tensor]
+
+
 class MoELayer:
     """Device buffers and the stage sequence of one layer step.
 
@@ -190,6 +224,8 @@ class MoELayer:
             self.swaps_next = torch.empty((E // 2 + 1, 2), **i32)
             self.n_swaps_next = torch.empty((1,), **i32)
             self.home_base = None
+        self._train = None      # buffers of the training form, made at its first step
+        self._adapter_ws = None
         self.ws_shared = None
         if shared_inter > 0:
             self.ws_shared = torch.empty((M.moelb_grouped_ffn_workspace_bytes(T, 1, 1, d, shared_inter, code),),
@@ -239,13 +275,52 @@ class MoELayer:
         self.sched_cur, self.sched_next = self.sched_next, self.sched_cur
         return self.replica_spare
 
-    def _ffn(self, h, w13, w2, mark=None, stream=None):
+    def _train_buffers(self):
+        """What the training form keeps between step and backward, and the
+        gradients."""
+        if self._train is None:
+            T, P, d, E, i, si = self.T, self.P, self.d, self.E, self.inter, self.shared_inter
+            code = M.MOELB_BF16 if self.dtype == "bf16" else M.MOELB_F32
+            t = dict(dtype=self.tdtype, device=self.dev)
+            f = dict(dtype=torch.float32, device=self.dev)
+
+            def bytes_(n):
+                return torch.empty((max(1, n),), dtype=torch.uint8, device=self.dev)
+            b = dict(z=torch.empty((P, 2 * i), **f), dy=torch.empty((P, d), **t), dx=torch.empty((P, d), **t),
+                     dwts=torch.empty((T, self.k), **f), ones=torch.ones((T, self.k), **f),
+                     dh_router=torch.empty((T, d), **t), dh=torch.empty((T, d), **t),
+                     dw=torch.empty((E, d), **t), db=torch.empty((E,), **f),
+                     dw13=torch.empty((E, 2 * i, d), **t), dw2=torch.empty((E, d, i), **t),
+                     ws=bytes_(M.moelb_grouped_ffn_backward_workspace_bytes(P, 2 * self.G * E, E, d, i, code)),
+                     ws_gate=bytes_(M.moelb_gate_backward_workspace_bytes(T, d, E, code)))
+            if si > 0:
+                b.update(z_shared=torch.empty((T, 2 * si), **f), dx_shared=torch.empty((T, d), **t),
+                         dw13_shared=torch.empty((2 * si, d), **t), dw2_shared=torch.empty((d, si), **t),
+                         ws_shared=bytes_(M.moelb_grouped_ffn_backward_workspace_bytes(T, 1, 1, d, si, code)),
+                         own_row=torch.arange(T, dtype=torch.int32, device=self.dev), one=torch.ones((T, 1), **f))
+            self._train = b
+        return self._train
+
+    def _gather(self):
+        """The grouped FFN's row source: h through the permutation, or x_perm."""
+        return dict(gather=self.perm, gather_k=self.k) if self.gather_rows else {}
+
+    def _ffn(self, h, w13, w2, mark=None, stream=None, train=False):
         """The grouped FFN over every group; with ``mark``, its three stages
-        are launched apart and marks 8..11 recorded around them."""
+        are launched apart and marks 8..11 recorded around them (train: the
+        whole call between marks 9 and 10)."""
         x = h if self.gather_rows else self.x_perm
-        kw = dict(G=self.G, stream=stream)
-        if self.gather_rows:
-            kw.update(gather=self.perm, gather_k=self.k)
+        kw = dict(G=self.G, stream=stream, **self._gather())
+        if train:
+            b = self._train_buffers()
+            if mark is not None:
+                mark(8)
+                mark(9)
+            M.moelb_grouped_ffn_train(x, self.P, self.group_off, self.E, w13, w2, self.ws_ffn, b["z"], self.y, **kw)
+            if mark is not None:
+                mark(10)
+                mark(11)
+            return
         if mark is None:
             M.moelb_grouped_ffn_stages(M.MOELB_FFN_ALL | self.ffn_opt, x, self.P, self.group_off, self.E, w13, w2,
                                        self.ws_ffn, self.y, **kw)
@@ -256,9 +331,33 @@ class MoELayer:
                                        self.ws_ffn, self.y, **kw)
         mark(11)
 
-    def _shared_ffn(self, h, shared_w13, shared_w2, stream):
+    def _shared_ffn(self, h, shared_w13, shared_w2, stream, train=False, adapters=None):
+        if adapters is not None:
+            self._shared_with_adapters(h, shared_w13, shared_w2, adapters, stream)
+            return
+        if train:
+            M.moelb_grouped_ffn_train(h, self.T, self.shared_off, 1, shared_w13, shared_w2, self.ws_shared,
+                                      self._train_buffers()["z_shared"], self.shared, stream=stream)
+            return
         M.moelb_grouped_ffn_stages(M.MOELB_FFN_ALL | self.ffn_opt, h, self.T, self.shared_off, 1, shared_w13,
                                    shared_w2, self.ws_shared, self.shared, stream=stream)
+
+    def _shared_with_adapters(self, h, shared_w13, shared_w2, ad: SharedAdapters, stream):
+        """The shared expert as two projections with each token's adapters
+        beside them: gate and up gated into the activations, then down."""
+        T, d, si = self.T, self.d, self.shared_inter
+        code = M.dtype_code(h)
+        n, r13, r2 = ad.a13.shape[0], ad.a13.shape[1], ad.a2.shape[1]
+        need = max(M.moelb_adapter_projection_workspace_bytes(T, d, 2 * si, n, r13, code),
+                   M.moelb_adapter_projection_workspace_bytes(T, si, d, n, r2, code))
+        if self._adapter_ws is None or self._adapter_ws[0].numel() < need:
+            self._adapter_ws = (torch.empty((max(1, need),), dtype=torch.uint8, device=self.dev),
+                                torch.empty((T, si), dtype=self.tdtype, device=self.dev))
+        ws, mid = self._adapter_ws
+        M.moelb_adapter_projection(h, shared_w13.reshape(2 * si, d), ad.ids, ad.a13, ad.b13, ad.scale13, ws, mid,
+                                   gated=True, stream=stream)
+        M.moelb_adapter_projection(mid, shared_w2.reshape(d, si), ad.ids, ad.a2, ad.b2, ad.scale2, ws, self.shared,
+                                   stream=stream)
 
     def _out(self):
         return StepOut(self.idx, self.wts, self.gap, self.idx_next, self.counts, self.counts_next, self.replica_next,
@@ -267,13 +366,21 @@ class MoELayer:
                        self.home_next if self.balancer == "freebalance" else None)
 
     def step(self, h, w_cur, b_cur, w_next, b_next, home, replica_cur, w13, w2, shared_w13=None, shared_w2=None,
-             stream=None, events: Optional[HipEvents] = None, ev_base: int = 0, sched=None) -> StepOut:
-        """One layer step.  With ``events``, marks ev_base+0..7 bracket the
+             stream=None, events: Optional[HipEvents] = None, ev_base: int = 0, sched=None, train: bool = False,
+             shared_adapters: Optional[SharedAdapters] = None) -> StepOut:
+        """One layer step.  ``train``: keep what ``backward`` needs (row-major
+        weights only).  ``shared_adapters``: the shared expert with each
+        token's low-rank adapters (row-major weights only; not with
+        ``train``).  With ``events``, marks ev_base+0..7 bracket the
         stages of STAGES on the step's stream, ev_base+8..11 bracket the
         grouped FFN's three stages (schedule, gate/up GEMM, down GEMM, each
         launched on its own), ev_base+12..13 bracket the side stream's work.
         ``sched``: the split's round schedule for ``replica_cur`` (default: the
         one ``predict_plan`` or ``advance`` left in force)."""
+        if self.ffn_opt and (train or shared_adapters is not None):
+            raise ValueError("train and shared_adapters take row-major weights")
+        if shared_adapters is not None and (train or self.shared is None):
+            raise ValueError("shared_adapters need a shared expert, and are not trained")
         ev = events
         s0 = stream if stream is not None else torch.cuda.current_stream()
 
@@ -322,15 +429,43 @@ class MoELayer:
             M.moelb_permute(hr, self.idx, self.G, home, replica_cur, self.host_count, self.ws_perm, self.group_off,
                             self.perm, self.pos, xr, d=self.d, dtype=code, stream=s0)
         mark(4)
-        self._ffn(h, w13, w2, mark if ev is not None else None, stream=s0)
+        self._ffn(h, w13, w2, mark if ev is not None else None, stream=s0, train=train)
         if self.shared is not None:
-            self._shared_ffn(h, shared_w13, shared_w2, s0)
+            self._shared_ffn(h, shared_w13, shared_w2, s0, train, shared_adapters)
         mark(5)
         M.moelb_combine(self.y, self.pos, self.wts, self.out, shared=self.shared, stream=s0)
         mark(6)
         s0.wait_event(self.ev_side)
         mark(7)
         return self._out()
+
+    def backward(self, dout, h, w_cur, b_cur, w13, w2, shared_w13=None, shared_w2=None, stream=None) -> Gradients:
+        """Gradients of the last ``step(..., train=True)`` for ``dout`` [T, d],
+        the gradient of its ``out``; the other arguments are that step's.
+        The placement of pairs on ranks carries no gradient: a pair's row is
+        its expert's output wherever it is computed.  The combine's gradient
+        comes first, then the experts' (dx a row per pair), the router's and
+        the shared expert's; the hidden states' gradient is the sum of their
+        shares, each rounded to the layer's type once."""
+        b = self._train
+        if b is None:
+            raise RuntimeError("backward without a step(..., train=True)")
+        s0 = stream if stream is not None else torch.cuda.current_stream()
+        x = h if self.gather_rows else self.x_perm
+        M.moelb_combine_backward(dout, self.y, self.pos, self.wts, b["dy"], b["dwts"], stream=s0)
+        M.moelb_grouped_ffn_backward(b["dy"], x, self.P, self.group_off, self.E, w13, w2, b["z"], b["ws"], b["dx"],
+                                     b["dw13"], b["dw2"], G=self.G, stream=s0, **self._gather())
+        M.moelb_gate_backward(h, w_cur, b_cur, self.idx, b["dwts"], b["ws_gate"], b["dh_router"], b["dw"], b["db"],
+                              stream=s0)
+        M.moelb_combine(b["dx"], self.pos, b["ones"], b["dh"], shared=b["dh_router"], stream=s0)
+        if self.shared is None:
+            return Gradients(b["dh"], b["dw"], b["db"], b["dw13"], b["dw2"], None, None)
+        d13, d2 = b["dw13_shared"].view(shared_w13.shape), b["dw2_shared"].view(shared_w2.shape)
+        M.moelb_grouped_ffn_backward(dout, h, self.T, self.shared_off, 1, shared_w13, shared_w2, b["z_shared"],
+                                     b["ws_shared"], b["dx_shared"], d13, d2, stream=s0)
+        # dh += dx_shared: dh_router's buffer is free again
+        M.moelb_combine(b["dx_shared"], b["own_row"], b["one"], b["dh_router"], shared=b["dh"], stream=s0)
+        return Gradients(b["dh_router"], b["dw"], b["db"], b["dw13"], b["dw2"], d13, d2)
 
 
     def step_two_stage(self, h, w_cur, b_cur, w_next, b_next, home, replica_cur, w13, w2, shared_w13=None,

@@ -365,8 +365,8 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
 
 // fp32: the same sum on 64 x 64 tiles.
 template <bool GU>
-__global__ __launch_bounds__(mt::THREADS) void adapter_tile_f32_kernel(AdapterArgs p) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
+__global__ __launch_bounds__(mt::S_THREADS) void adapter_tile_f32_kernel(AdapterArgs p) {
+  __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   __shared__ int tok[64];
   int mi, ni;
   if (!tile_of(p, 64, mi, ni)) return;
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_f32_kernel(AdapterAr
   {
     auto pa = [&](int i, int k) { return t0 + i < p.Ttok ? x + (size_t)(t0 + i) * p.d_in + k : nullptr; };
     auto pb = [&](int i, int k) { return wrow(i) >= 0 ? w + (size_t)wrow(i) * p.d_in + k : nullptr; };
-    mt::k_loop_f32<false, false>(lds, pa, pb, p.d_in, acc);
+    mt::k_loop_f32<64, false, false>(lds, pa, pb, p.d_in, acc);
   }
   if (p.n > 0) {
     // every wave walks the tile's adapters (they load the rows together); a
@@ -391,28 +391,27 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_f32_kernel(AdapterAr
     if (threadIdx.x < 64) tok[threadIdx.x] = t0 + (int)threadIdx.x < p.Ttok ? id_of(p, t0 + threadIdx.x) : -1;
     __syncthreads();
     int left = tok[threadIdx.x & 63];
-    const int own = tok[(threadIdx.x >> 7) * 32 + (threadIdx.x & 31)];
-    const int ti = threadIdx.x >> 2;  // the row this thread fetches
+    const int own = tok[(threadIdx.x >> 6 & 1) * 32 + (threadIdx.x & 31)];  // the lane's token
     for (uint64_t some = __ballot(left >= 0); some; some = __ballot(left >= 0)) {
       const int id = __builtin_amdgcn_readlane(left, __builtin_ctzll(some));
       if (left == id) left = -1;
       const float* b = static_cast<const float*>(p.b) + (size_t)id * p.d_out * p.r;
-      auto pa = [&](int, int k) { return tok[ti] == id ? low + (size_t)(t0 + ti) * p.r + k : nullptr; };
+      auto pa = [&](int i, int k) { return tok[i] == id ? low + (size_t)(t0 + i) * p.r + k : nullptr; };
       auto pb = [&](int i, int k) { return wrow(i) >= 0 ? b + (size_t)wrow(i) * p.r + k : nullptr; };
       f32x16_t more;
       __syncthreads();
-      mt::k_loop_f32<false, false>(lds, pa, pb, p.r, more);
+      mt::k_loop_f32<64, false, false>(lds, pa, pb, p.r, more);
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[q] = own == id ? acc[q] + more[q] : acc[q];
     }
   }
   float* y = static_cast<float*>(p.y);
   if constexpr (GU) {
-    mt::drain_f32<true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
+    mt::drain_f32<64, true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
       if (t0 + r < p.Ttok && n0 + c < out) store_gated(y + (size_t)(t0 + r) * out + n0 + c, g, u);
     });
   } else {
-    mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) {
+    mt::drain_f32<64, false>(lds, acc, [&](int r, int c, const float* v) {
       if (t0 + r < p.Ttok && n0 + c < out) mt::store8(y + (size_t)(t0 + r) * out + n0 + c, v);
     });
   }
@@ -675,7 +674,7 @@ int launch_f32(AdapterArgs p, hipStream_t s) {
   p.ntn = (out + bn - 1) / bn;
   const size_t grid = ((size_t)((p.Ttok + 63) / 64) * p.ntn + 7) / 8 * 8;
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
-  hipLaunchKernelGGL((adapter_tile_f32_kernel<GU>), dim3((unsigned)grid), dim3(mt::THREADS), 0, s, p);
+  hipLaunchKernelGGL((adapter_tile_f32_kernel<GU>), dim3((unsigned)grid), dim3(mt::S_THREADS), 0, s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }

@@ -152,7 +152,7 @@ __device__ __forceinline__ void rows_tile(const TrainArgs<uint16_t>& p, int bloc
   }
 }
 
-template <int OP>
+template <int TN, int OP>
 __device__ __forceinline__ void rows_tile(const TrainArgs<float>& p, int block, float* lds) {
   const int n_mtiles = *p.s.n_mtiles;
   const int tile = xcd_tile(block, n_mtiles * p.ntn);
@@ -161,38 +161,42 @@ __device__ __forceinline__ void rows_tile(const TrainArgs<float>& p, int block, 
   const int e = p.s.mt_e[mti], v0 = p.s.mt_v0[mti], vend = p.s.eoff[e + 1];
   const int d = p.d, I = p.inter;
   constexpr bool GU = OP == OP_UP;
-  const int n0 = nt * (GU ? 32 : 64);
+  const int n0 = nt * (GU ? TN / 2 : TN);
   const int N = (OP == OP_UP || OP == OP_DA) ? I : d;
   const int K = OP == OP_DOWN ? I : OP == OP_DX ? 2 * I : d;
   const float* base = OP == OP_UP ? p.x : OP == OP_DOWN ? p.a : OP == OP_DA ? p.dy : p.dz;
   const int rows = OP == OP_UP ? p.rows_x : p.rows;
   const int32_t* map = OP == OP_UP ? p.s.asrc : OP == OP_DA ? p.s.rowmap : nullptr;
-  const int va = v0 + (threadIdx.x >> 2);  // the row this thread fetches
-  const int ra = va < vend ? (map ? clampi(map[va], rows) : va) : -1;
-  auto pa = [&](int, int k) { return ra < 0 ? nullptr : base + (size_t)ra * K + k; };
+  __shared__ int src[mt::S_BM];  // row of the left factor, -1 past the end
+  if (threadIdx.x < mt::S_BM) {
+    const int v = v0 + threadIdx.x;
+    src[threadIdx.x] = v < vend ? (map ? clampi(map[v], rows) : v) : -1;
+  }
+  __syncthreads();
+  auto pa = [&](int r, int k) { return src[r] < 0 ? nullptr : base + (size_t)src[r] * K + k; };
   f32x16_t acc;
   if constexpr (OP == OP_UP || OP == OP_DOWN) {
     const float* w = OP == OP_UP ? p.w13 + (size_t)e * 2 * I * d : p.w2 + (size_t)e * d * I;
     auto pb = [&](int r, int k) {
-      const int c = n0 + (GU ? r & 31 : r);
-      return c < N ? w + ((size_t)c + (GU && r >= 32 ? I : 0)) * K + k : nullptr;
+      const int c = n0 + (GU ? r % (TN / 2) : r);
+      return c < N ? w + ((size_t)c + (GU && r >= TN / 2 ? I : 0)) * K + k : nullptr;
     };
-    mt::k_loop_f32<false, false>(lds, pa, pb, K, acc);
+    mt::k_loop_f32<TN, false, false>(lds, pa, pb, K, acc);
   } else {
     const float* w = OP == OP_DA ? p.w2 + (size_t)e * d * I : p.w13 + (size_t)e * 2 * I * d;
     auto pb = [&](int r, int k) { return n0 + r < N ? w + (size_t)k * N + n0 + r : nullptr; };
-    mt::k_loop_f32<false, true>(lds, pa, pb, K, acc);
+    mt::k_loop_f32<TN, false, true>(lds, pa, pb, K, acc);
   }
   if constexpr (GU) {
-    mt::drain_f32<true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
+    mt::drain_f32<TN, true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
       if (v0 + r < vend && n0 + c < N) put_up(p, v0 + r, n0 + c, g, u);
     });
   } else if constexpr (OP == OP_DA) {
-    mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) {
+    mt::drain_f32<TN, false>(lds, acc, [&](int r, int c, const float* v) {
       if (v0 + r < vend && n0 + c < N) put_da(p, v0 + r, n0 + c, v);
     });
   } else {
-    mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) {
+    mt::drain_f32<TN, false>(lds, acc, [&](int r, int c, const float* v) {
       if (v0 + r < vend && n0 + c < N)
         mt::store8(p.out + (size_t)clampi(p.s.rowmap[v0 + r], p.rows) * d + n0 + c, v);
     });
@@ -243,12 +247,12 @@ __device__ __forceinline__ void put_w(const TrainArgs<T>& p, const WTile& w, int
     mt::store8(p.out + at, v);
 }
 
-// A tile of B x B zeros, for an expert (or a split) without rows.
-template <int B, typename T>
+// A tile of zeros, for an expert (or a split) without rows.
+template <int BM, int BN, typename T>
 __device__ __forceinline__ void zero_w(const TrainArgs<T>& p, const WTile& w, int M, int N) {
   const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int c = threadIdx.x; c < B * (B / 8); c += mt::THREADS)
-    put_w(p, w, M, N, w.mi * B + c / (B / 8), w.ni * B + (c % (B / 8)) * 8, v);
+  for (int c = threadIdx.x; c < BM * (BN / 8); c += blockDim.x)
+    put_w(p, w, M, N, w.mi * BM + c / (BN / 8), w.ni * BN + (c % (BN / 8)) * 8, v);
 }
 
 template <int F, int OP>
@@ -258,7 +262,7 @@ __device__ __forceinline__ void weights_tile(const TrainArgs<uint16_t>& p, int b
   const int d = p.d, I = p.inter;
   const int M = OP == OP_DW13 ? 2 * I : d, N = OP == OP_DW13 ? d : I;
   if (w.n == 0) {
-    zero_w<64 * F>(p, w, M, N);
+    zero_w<64 * F, 64 * F>(p, w, M, N);
     return;
   }
   const int m0 = w.mi * 64 * F, n0 = w.ni * 64 * F;
@@ -280,17 +284,17 @@ __device__ __forceinline__ void weights_tile(const TrainArgs<uint16_t>& p, int b
   mt::drain<F, false>(lds, acc, [&](int r, int c, const float* v) { put_w(p, w, M, N, m0 + r, n0 + c, v); });
 }
 
-template <int OP>
+template <int TN, int OP>
 __device__ __forceinline__ void weights_tile(const TrainArgs<float>& p, int block, float* lds) {
   WTile w;
   if (!w_tile(p, block, w)) return;
   const int d = p.d, I = p.inter;
   const int M = OP == OP_DW13 ? 2 * I : d, N = OP == OP_DW13 ? d : I;
   if (w.n == 0) {
-    zero_w<mt::S_BM>(p, w, M, N);
+    zero_w<mt::S_BM, TN>(p, w, M, N);
     return;
   }
-  const int m0 = w.mi * 64, n0 = w.ni * 64;
+  const int m0 = w.mi * 64, n0 = w.ni * TN;
   f32x16_t acc;
   auto pa = [&](int r, int k) -> const float* {
     if (m0 + r >= M) return nullptr;
@@ -302,8 +306,8 @@ __device__ __forceinline__ void weights_tile(const TrainArgs<float>& p, int bloc
     if (OP == OP_DW13) return p.x + (size_t)clampi(p.s.asrc[w.v0 + k], p.rows_x) * N + n0 + r;
     return p.a + (size_t)(w.v0 + k) * N + n0 + r;
   };
-  mt::k_loop_f32<true, true>(lds, pa, pb, w.n, acc);
-  mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) { put_w(p, w, M, N, m0 + r, n0 + c, v); });
+  mt::k_loop_f32<TN, true, true>(lds, pa, pb, w.n, acc);
+  mt::drain_f32<TN, false>(lds, acc, [&](int r, int c, const float* v) { put_w(p, w, M, N, m0 + r, n0 + c, v); });
 }
 
 // ---------------------------------------------------------------- kernels
@@ -313,10 +317,10 @@ __global__ __launch_bounds__(mt::THREADS) void train_rows_kernel(TrainArgs<uint1
   extern __shared__ __align__(16) char smem[];
   rows_tile<F, OP>(p, blockIdx.x, reinterpret_cast<uint16_t*>(smem));
 }
-template <int OP>
-__global__ __launch_bounds__(mt::THREADS) void train_rows_f32_kernel(TrainArgs<float> p) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
-  rows_tile<OP>(p, blockIdx.x, lds);
+template <int TN, int OP>
+__global__ __launch_bounds__(mt::S_THREADS) void train_rows_f32_kernel(TrainArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::STile<TN>::FLOATS];
+  rows_tile<TN, OP>(p, blockIdx.x, lds);
 }
 
 // dW13, dW2 and dx all follow from [dg, du], a and dy: one launch, so the last
@@ -325,29 +329,39 @@ __global__ __launch_bounds__(mt::THREADS) void train_rows_f32_kernel(TrainArgs<f
 template <typename T>
 struct GradArgs {
   TrainArgs<T> w13, w2, x;
-  int n13, n2;  // blocks of the first two
+  int n13, n2, nx;  // their blocks
+  bool x_first;     // dx's sums are the longest: its blocks come first
 };
 template <int F>
 __global__ __launch_bounds__(mt::THREADS) void train_grads_kernel(GradArgs<uint16_t> g) {
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
-  const int b = blockIdx.x;
+  int b = blockIdx.x;
+  const int x0 = g.x_first ? 0 : g.n13 + g.n2;
+  if (b >= x0 && b < x0 + g.nx) {
+    rows_tile<F, OP_DX>(g.x, b - x0, lds);
+    return;
+  }
+  if (g.x_first) b -= g.nx;
   if (b < g.n13)
     weights_tile<F, OP_DW13>(g.w13, b, lds);
-  else if (b < g.n13 + g.n2)
+  else
     weights_tile<F, OP_DW2>(g.w2, b - g.n13, lds);
-  else
-    rows_tile<F, OP_DX>(g.x, b - g.n13 - g.n2, lds);
 }
-__global__ __launch_bounds__(mt::THREADS) void train_grads_f32_kernel(GradArgs<float> g) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
-  const int b = blockIdx.x;
+template <int TN>
+__global__ __launch_bounds__(mt::S_THREADS) void train_grads_f32_kernel(GradArgs<float> g) {
+  __shared__ __align__(16) float lds[mt::STile<TN>::FLOATS];
+  int b = blockIdx.x;
+  const int x0 = g.x_first ? 0 : g.n13 + g.n2;
+  if (b >= x0 && b < x0 + g.nx) {
+    rows_tile<TN, OP_DX>(g.x, b - x0, lds);
+    return;
+  }
+  if (g.x_first) b -= g.nx;
   if (b < g.n13)
-    weights_tile<OP_DW13>(g.w13, b, lds);
-  else if (b < g.n13 + g.n2)
-    weights_tile<OP_DW2>(g.w2, b - g.n13, lds);
+    weights_tile<TN, OP_DW13>(g.w13, b, lds);
   else
-    rows_tile<OP_DX>(g.x, b - g.n13 - g.n2, lds);
+    weights_tile<TN, OP_DW2>(g.w2, b - g.n13, lds);
 }
 
 // out[i] = sum over splits, in order, of part[s][i]; 8 values per thread.
@@ -378,11 +392,20 @@ int tile_rows(int rows, int E, int d, int inter, int dtype) {
   return (size_t)rows >= (size_t)192 * E && tiles >= 192 ? 256 : 128;
 }
 
+// Column tile: as wide as the row tile, but for fp32 half of it where a call's
+// row-tiled products have fewer 64-wide tiles than compute units.
+int tile_cols(int rows, int E, int d, int inter, int dtype) {
+  const int b = tile_rows(rows, E, d, inter, dtype);
+  if (dtype == MOELB_BF16) return b;
+  const int least = d < inter ? d : inter;
+  return (size_t)(rows + 63) / 64 * ((least + 63) / 64) < 256 ? 32 : 64;
+}
+
 // Parts the rows of every expert are cut into for the weight gradients: enough
 // workgroups for the compute units, at least 512 rows each on average.
-int weight_splits(int rows, int E, int M, int N, int b) {
+int weight_splits(int rows, int E, int M, int N, int b, int bn) {
   const int slots = b == 256 ? 256 : 512;
-  const size_t tiles = (size_t)E * ((M + b - 1) / b) * ((N + b - 1) / b);
+  const size_t tiles = (size_t)E * ((M + b - 1) / b) * ((N + bn - 1) / bn);
   const size_t want = slots / tiles, most = (size_t)rows / E / 512;
   const size_t s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
@@ -394,11 +417,12 @@ struct BackLayout {
 BackLayout back_layout(int rows, int num_groups, int E, int d, int inter, int dtype) {
   BackLayout l;
   const size_t eb = moelb_elem_bytes(dtype);
-  const int tile = tile_rows(rows, E, d, inter, dtype);
+  const int tile = tile_rows(rows, E, d, inter, dtype), tn = tile_cols(rows, E, d, inter, dtype);
   l.order = sched_layout(rows, num_groups, E, inter, dtype, nullptr, nullptr);  // schedule tables and a
   l.dz = l.order + moelb_align256((size_t)E * 4);
   l.part13 = l.dz + moelb_align256((size_t)rows * 2 * inter * eb);
-  const size_t s13 = weight_splits(rows, E, 2 * inter, d, tile), s2 = weight_splits(rows, E, d, inter, tile);
+  const size_t s13 = weight_splits(rows, E, 2 * inter, d, tile, tn),
+               s2 = weight_splits(rows, E, d, inter, tile, tn);
   l.part2 = l.part13 + (s13 > 1 ? moelb_align256(s13 * E * 2 * inter * d * 4) : 0);
   l.total = l.part2 + (s2 > 1 ? moelb_align256(s2 * E * inter * d * 4) : 0);
   return l;
@@ -414,10 +438,10 @@ size_t rows_grid(TrainArgs<T>& p, int BM, int bn, int N) {
 // Blocks of a weight gradient; sets its tiles, splits and units: about 32
 // tiles a unit (the compute units of an XCD), at least 32 units in all.
 template <typename T>
-size_t weights_grid(TrainArgs<T>& p, int BM, int M, int N) {
-  p.splits = weight_splits(p.rows, p.E, M, N, BM);
+size_t weights_grid(TrainArgs<T>& p, int BM, int BN, int M, int N) {
+  p.splits = weight_splits(p.rows, p.E, M, N, BM, BN);
   p.ntm = (M + BM - 1) / BM;
-  p.ntn = (N + BM - 1) / BM;
+  p.ntn = (N + BN - 1) / BN;
   const int per = p.ntm * p.ntn * p.splits;
   const int c = per / 32, least = (32 + p.E - 1) / p.E;
   p.chunks = c > least ? c : least;
@@ -427,17 +451,21 @@ size_t weights_grid(TrainArgs<T>& p, int BM, int M, int N) {
 }
 
 template <typename T, int OP>
-int launch_rows(TrainArgs<T> p, int BM, hipStream_t s) {
-  const size_t grid = rows_grid(p, BM, OP == OP_UP ? BM / 2 : BM, (OP == OP_UP || OP == OP_DA) ? p.inter : p.d);
+int launch_rows(TrainArgs<T> p, int BM, int BN, hipStream_t s) {
+  const size_t grid = rows_grid(p, BM, OP == OP_UP ? BN / 2 : BN, (OP == OP_UP || OP == OP_DA) ? p.inter : p.d);
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
+  const dim3 g((unsigned)grid);
   if constexpr (sizeof(T) == 4) {
-    hipLaunchKernelGGL((train_rows_f32_kernel<OP>), dim3((unsigned)grid), dim3(mt::THREADS), 0, s, p);
+    if (BN == 64)
+      hipLaunchKernelGGL((train_rows_f32_kernel<64, OP>), g, dim3(mt::S_THREADS), 0, s, p);
+    else
+      hipLaunchKernelGGL((train_rows_f32_kernel<32, OP>), g, dim3(mt::S_THREADS), 0, s, p);
   } else if (BM == 256) {
     if (!moelb_allow_lds(train_rows_kernel<4, OP>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL((train_rows_kernel<4, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<4>(), s, p);
+    hipLaunchKernelGGL((train_rows_kernel<4, OP>), g, dim3(mt::THREADS), mt::lds_bytes<4>(), s, p);
   } else {
     if (!moelb_allow_lds(train_rows_kernel<2, OP>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL((train_rows_kernel<2, OP>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<2>(), s, p);
+    hipLaunchKernelGGL((train_rows_kernel<2, OP>), g, dim3(mt::THREADS), mt::lds_bytes<2>(), s, p);
   }
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
@@ -468,36 +496,40 @@ bool sizes_ok(int rows_x, int rows, int num_groups, int E, int G, int rank, cons
 }
 
 template <typename T>
-int run_forward(TrainArgs<T> p, int BM, hipStream_t s) {
-  int st = launch_rows<T, OP_UP>(p, BM, s);
-  return st != MOELB_OK ? st : launch_rows<T, OP_DOWN>(p, BM, s);
+int run_forward(TrainArgs<T> p, int BM, int BN, hipStream_t s) {
+  int st = launch_rows<T, OP_UP>(p, BM, BN, s);
+  return st != MOELB_OK ? st : launch_rows<T, OP_DOWN>(p, BM, BN, s);
 }
 
 template <typename T>
-int run_backward(TrainArgs<T> p, int BM, T* dx, T* dw13, T* dw2, float* part2, hipStream_t s) {
+int run_backward(TrainArgs<T> p, int BM, int BN, T* dx, T* dw13, T* dw2, float* part2, hipStream_t s) {
   if (p.rows > 0) {
-    const int st = launch_rows<T, OP_DA>(p, BM, s);
+    const int st = launch_rows<T, OP_DA>(p, BM, BN, s);
     if (st != MOELB_OK) return st;
   }
-  GradArgs<T> g = {p, p, p, 0, 0};
+  GradArgs<T> g = {p, p, p, 0, 0, 0, p.rows / p.E < 2 * p.inter};
   size_t n13 = 0, n2 = 0, nx = 0;
   g.w13.out = dw13, g.w2.out = dw2, g.x.out = dx;
   g.w2.part = part2;
-  if (dw13) n13 = weights_grid(g.w13, BM, 2 * p.inter, p.d);
-  if (dw2) n2 = weights_grid(g.w2, BM, p.d, p.inter);
-  if (dx && p.rows > 0) nx = rows_grid(g.x, BM, BM, p.d);
+  if (dw13) n13 = weights_grid(g.w13, BM, BN, 2 * p.inter, p.d);
+  if (dw2) n2 = weights_grid(g.w2, BM, BN, p.d, p.inter);
+  if (dx && p.rows > 0) nx = (rows_grid(g.x, BM, BN, p.d) + 7) / 8 * 8;
   const size_t grid = n13 + n2 + nx;
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
   if (grid == 0) return MOELB_OK;
-  g.n13 = (int)n13, g.n2 = (int)n2;
+  g.n13 = (int)n13, g.n2 = (int)n2, g.nx = (int)nx;
+  const dim3 gd((unsigned)grid);
   if constexpr (sizeof(T) == 4) {
-    hipLaunchKernelGGL(train_grads_f32_kernel, dim3((unsigned)grid), dim3(mt::THREADS), 0, s, g);
+    if (BN == 64)
+      hipLaunchKernelGGL((train_grads_f32_kernel<64>), gd, dim3(mt::S_THREADS), 0, s, g);
+    else
+      hipLaunchKernelGGL((train_grads_f32_kernel<32>), gd, dim3(mt::S_THREADS), 0, s, g);
   } else if (BM == 256) {
     if (!moelb_allow_lds(train_grads_kernel<4>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL((train_grads_kernel<4>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<4>(), s, g);
+    hipLaunchKernelGGL((train_grads_kernel<4>), gd, dim3(mt::THREADS), mt::lds_bytes<4>(), s, g);
   } else {
     if (!moelb_allow_lds(train_grads_kernel<2>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL((train_grads_kernel<2>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<2>(), s, g);
+    hipLaunchKernelGGL((train_grads_kernel<2>), gd, dim3(mt::THREADS), mt::lds_bytes<2>(), s, g);
   }
   MOELB_CHECK_LAUNCH();
   if (dw13 && g.w13.splits > 1) {
@@ -523,7 +555,7 @@ extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, cons
   sched_layout(rows, num_groups, E, inter, dtype, &sc, static_cast<char*>(ws));
   sc.wpacked = 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int BM = tile_rows(rows, E, d, inter, dtype);
+  const int BM = tile_rows(rows, E, d, inter, dtype), BN = tile_cols(rows, E, d, inter, dtype);
   const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, sc, s);
   if (st != MOELB_OK) return st;
   auto run = [&](auto* t) {
@@ -541,12 +573,12 @@ extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, cons
     // schedule and activations (it lets a tile's stores run beside the next
     // tile's loads: 634 -> 5xx us at 131072 rows, d = 2048, inter = 1024)
     if (BM == 256) {
-      const int up = launch_rows<T, OP_UP>(p, BM, s);
+      const int up = launch_rows<T, OP_UP>(p, BM, BN, s);
       if (up != MOELB_OK) return up;
       return moelb_grouped_ffn_stages(MOELB_FFN_DOWN, x, rows_x, rows, group_off, num_groups, E, G, rank, gather,
                                       gather_k, d, inter, dtype, w13, w2, ws, ws_bytes, y, stream);
     }
-    return run_forward<T>(p, BM, s);
+    return run_forward<T>(p, BM, BN, s);
   };
   return dtype == MOELB_BF16 ? run(static_cast<uint16_t*>(nullptr)) : run(static_cast<float*>(nullptr));
 }
@@ -576,7 +608,7 @@ extern "C" int moelb_grouped_ffn_backward(const void* dy, const void* x, int row
   sc.wpacked = 0;
   sc.order = reinterpret_cast<int32_t*>(base + l.order);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int BM = tile_rows(rows, E, d, inter, dtype);
+  const int BM = tile_rows(rows, E, d, inter, dtype), BN = tile_cols(rows, E, d, inter, dtype);
   const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, sc, s);
   if (st != MOELB_OK) return st;
   auto run = [&](auto* t) {
@@ -592,7 +624,7 @@ extern "C" int moelb_grouped_ffn_backward(const void* dy, const void* x, int row
     p.dz = reinterpret_cast<T*>(base + l.dz);
     p.part = reinterpret_cast<float*>(base + l.part13);
     p.rows = rows, p.d = d, p.inter = inter, p.E = E, p.s = sc;
-    return run_backward<T>(p, BM, static_cast<T*>(dx), static_cast<T*>(dw13), static_cast<T*>(dw2),
+    return run_backward<T>(p, BM, BN, static_cast<T*>(dx), static_cast<T*>(dw13), static_cast<T*>(dw2),
                            reinterpret_cast<float*>(base + l.part2), s);
   };
   return dtype == MOELB_BF16 ? run(static_cast<uint16_t*>(nullptr)) : run(static_cast<float*>(nullptr));

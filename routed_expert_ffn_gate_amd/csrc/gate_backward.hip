@@ -159,14 +159,14 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
   }
 }
 
-__global__ __launch_bounds__(mt::THREADS) void gate_logits_f32_kernel(GateArgs<float> p) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
+__global__ __launch_bounds__(mt::S_THREADS) void gate_logits_f32_kernel(GateArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
   f32x16_t acc;
   auto pa = [&](int r, int k) { return m0 + r < p.Ttok ? p.h + (size_t)(m0 + r) * p.d + k : nullptr; };
   auto pb = [&](int r, int k) { return n0 + r < p.E ? p.w + (size_t)(n0 + r) * p.d + k : nullptr; };
-  mt::k_loop_f32<false, false>(lds, pa, pb, p.d, acc);
-  mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) {
+  mt::k_loop_f32<64, false, false>(lds, pa, pb, p.d, acc);
+  mt::drain_f32<64, false>(lds, acc, [&](int r, int c, const float* v) {
     if (m0 + r < p.Ttok && n0 + c < p.Ep) mt::store8(p.z + (size_t)(m0 + r) * p.Ep + n0 + c, v);
   });
 }
@@ -388,16 +388,16 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dh_kernel(GateArgs<uint16_t>
   }
 }
 
-__global__ __launch_bounds__(mt::THREADS) void gate_grads_f32_kernel(GateArgs<float> p) {
-  __shared__ __align__(16) float lds[mt::S_FLOATS];
+__global__ __launch_bounds__(mt::S_THREADS) void gate_grads_f32_kernel(GateArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   f32x16_t acc;
   if ((int)blockIdx.x < p.nh) {
     const int ntn = (p.d + 63) / 64;
     const int m0 = blockIdx.x / ntn * 64, n0 = blockIdx.x % ntn * 64;
     auto pa = [&](int r, int k) { return m0 + r < p.Ttok ? p.dz + (size_t)(m0 + r) * p.Ep + k : nullptr; };
     auto pb = [&](int r, int k) { return n0 + r < p.d && k < p.E ? p.w + (size_t)k * p.d + n0 + r : nullptr; };
-    mt::k_loop_f32<false, true>(lds, pa, pb, p.Ep, acc);
-    mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) { put_dh(p, m0 + r, n0 + c, v); });
+    mt::k_loop_f32<64, false, true>(lds, pa, pb, p.Ep, acc);
+    mt::drain_f32<64, false>(lds, acc, [&](int r, int c, const float* v) { put_dh(p, m0 + r, n0 + c, v); });
     return;
   }
   int mi, ni, split, k0, n;
@@ -405,8 +405,8 @@ __global__ __launch_bounds__(mt::THREADS) void gate_grads_f32_kernel(GateArgs<fl
   const int m0 = mi * 64, n0 = ni * 64;
   auto pa = [&](int r, int k) { return m0 + r < p.Ep ? p.dz + (size_t)(k0 + k) * p.Ep + m0 + r : nullptr; };
   auto pb = [&](int r, int k) { return n0 + r < p.d ? p.h + (size_t)(k0 + k) * p.d + n0 + r : nullptr; };
-  mt::k_loop_f32<true, true>(lds, pa, pb, n, acc);
-  mt::drain_f32<false>(lds, acc, [&](int r, int c, const float* v) { put_dw(p, split, m0 + r, n0 + c, v); });
+  mt::k_loop_f32<64, true, true>(lds, pa, pb, n, acc);
+  mt::drain_f32<64, false>(lds, acc, [&](int r, int c, const float* v) { put_dw(p, split, m0 + r, n0 + c, v); });
 }
 
 // ---- 4: sums over the parts.  Blocks below nw: dW, 8 values a thread; the
@@ -536,7 +536,7 @@ int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
 
 int run(GateArgs<float> p, bool, hipStream_t s) {
   if (p.Ttok > 0) {
-    hipLaunchKernelGGL(gate_logits_f32_kernel, dim3((p.Ttok + 63) / 64, (p.E + 63) / 64), dim3(mt::THREADS), 0, s, p);
+    hipLaunchKernelGGL(gate_logits_f32_kernel, dim3((p.Ttok + 63) / 64, (p.E + 63) / 64), dim3(mt::S_THREADS), 0, s, p);
     MOELB_CHECK_LAUNCH();
   }
   const int st = launch_softmax(p, s);
@@ -547,7 +547,7 @@ int run(GateArgs<float> p, bool, hipStream_t s) {
   if (nh + nw > 0x7fffffffull) return MOELB_EINVAL;
   p.nh = (int)nh;
   if (nh + nw > 0) {
-    hipLaunchKernelGGL(gate_grads_f32_kernel, dim3((unsigned)(nh + nw)), dim3(mt::THREADS), 0, s, p);
+    hipLaunchKernelGGL(gate_grads_f32_kernel, dim3((unsigned)(nh + nw)), dim3(mt::S_THREADS), 0, s, p);
     MOELB_CHECK_LAUNCH();
   }
   return MOELB_OK;

@@ -433,91 +433,114 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
 
 // ---------------------------------------------------------------- fp32 tile
 //
-// The same products for fp32 storage: tile 64 x 64, 4 waves of one
-// v_mfma_f32_32x32x2_f32 block each.  K steps of 32 are loaded two ahead into
-// registers and written to one of two LDS buffers as [k][m] (stride 68
-// floats), so a step has one barrier.  a(r, k) / b(r, k) give the address of 4
-// consecutive floats (along k for a row operand, along r for a column operand)
-// or null for zeros.
-constexpr int S_BM = 64, S_BK = 32, S_LD = 68;
-constexpr int S_BUF = 2 * S_BK * S_LD;  // floats of one buffer: A, then B
-constexpr int S_FLOATS = 2 * S_BUF;     // 34 KiB; the epilogue stages 64 x 64 in it
+// The same products for fp32 storage: tile 64 x TN (TN = 64, or 32 where a call
+// has few tiles), 512 threads.  A 32 x 32 block of v_mfma_f32_32x32x2_f32 is
+// bound by its own 64 cycles per instruction, so the 8 waves share the tile's
+// 2 TN / 32 blocks by cutting k between them: with one wave a block a step
+// of one wave's chain was the time of the small calls (tiny training step 88 ->
+// 6x us).  K steps (64 or 128 wide) are loaded one ahead into registers and
+// written to LDS as [k][m]; partial blocks meet in LDS in a fixed order.
+// a(r, k) / b(r, k) give the address of 4 consecutive floats (along k for a
+// row operand, along r for a column operand) or null for zeros.
+constexpr int S_BM = 64, S_THREADS = 512;
 
-template <bool CA, bool CB, class PA, class PB>
+template <int TN>
+struct STile {
+  static constexpr int BLOCKS = 2 * TN / 32, GROUPS = 8 / BLOCKS;  // waves that share a block
+  static constexpr int BK = 32 * GROUPS;                           // 64 or 128
+  static constexpr int FLOATS_A = BK * (64 + 4), FLOATS_B = BK * (TN + 4);
+  static constexpr int STAGE = GROUPS * 64 * TN;  // partial blocks in the epilogue
+  static constexpr int FLOATS = FLOATS_A + FLOATS_B > STAGE ? FLOATS_A + FLOATS_B : STAGE;
+};
+
+template <int TN, bool CA, bool CB, class PA, class PB>
 __device__ __forceinline__ void k_loop_f32(float* lds, PA pa, PB pb, int K, f32x16_t& acc) {
+  using S = STile<TN>;
+  constexpr int BK = S::BK;
+  float* As = lds;
+  float* Bs = lds + S::FLOATS_A;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int blk = wave % S::BLOCKS, kg = wave / S::BLOCKS;  // block, k group
+  const int wm = blk & 1, wn = blk >> 1;
 #pragma unroll
   for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  // 256 threads x 4 floats = 64 x 16, twice a step: row operand thread -> (row
-  // tid / 4, k 4 (tid % 4)), column operand thread -> (k tid / 16, row 4 (tid % 16))
-  auto fetch = [&](auto p, bool col, int k0) {
-    const int r = col ? (tid & 15) * 4 : tid >> 2, k = k0 + (col ? tid >> 4 : (tid & 3) * 4);
-    const float* q = k < K ? p(r, k) : nullptr;
-    return q ? *reinterpret_cast<const float4*>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  auto put = [&](float* s, bool col, float4 v) {
-    if (col) {
-      *reinterpret_cast<float4*>(s + (tid >> 4) * S_LD + (tid & 15) * 4) = v;
-    } else {
-      float* q = s + (tid & 3) * 4 * S_LD + (tid >> 2);
-      q[0] = v.x, q[S_LD] = v.y, q[2 * S_LD] = v.z, q[3 * S_LD] = v.w;
+  // R rows x BK k in pieces of 4 floats, NV a thread.  Row operand: 4 k of a
+  // row; LDS stride R + 1 (scalar writes).  Column operand: 4 rows of a k; LDS
+  // stride R + 4.
+  auto fetch = [&](auto p, auto R_, auto col_, int k0, auto& v) {
+    constexpr int R = decltype(R_)::value, NV = R * BK / 4 / S_THREADS;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = tid + i * S_THREADS;
+      const int r = decltype(col_)::value ? c % (R / 4) * 4 : c / (BK / 4);
+      const int k = k0 + (decltype(col_)::value ? c / (R / 4) : c % (BK / 4) * 4);
+      const float* q = k < K ? p(r, k) : nullptr;
+      v[i] = q ? *reinterpret_cast<const float4*>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
-  float4 ra[2][2], rb[2][2];  // [step parity][half of the step]
+  auto put = [&](float* s, auto R_, auto col_, const auto& v) {
+    constexpr int R = decltype(R_)::value, NV = R * BK / 4 / S_THREADS;
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ra[s][h] = fetch(pa, CA, s * S_BK + h * 16);
-      rb[s][h] = fetch(pb, CB, s * S_BK + h * 16);
-    }
-  for (int k0 = 0; k0 < K; k0 += 2 * S_BK) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      // buffer s: the reads of two steps ago are behind the last barrier
-      float* As = lds + s * S_BUF;
-      float* Bs = As + S_BK * S_LD;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        put(As + h * 16 * S_LD, CA, ra[s][h]);
-        put(Bs + h * 16 * S_LD, CB, rb[s][h]);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ra[s][h] = fetch(pa, CA, k0 + (s + 2) * S_BK + h * 16);
-        rb[s][h] = fetch(pb, CB, k0 + (s + 2) * S_BK + h * 16);
-      }
-#pragma unroll
-      for (int k = 0; k < S_BK; k += 2) {
-        const float a = As[(k + (lane >> 5)) * S_LD + wm * 32 + (lane & 31)];
-        const float b = Bs[(k + (lane >> 5)) * S_LD + wn * 32 + (lane & 31)];
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a, acc, 0, 0, 0);
+    for (int i = 0; i < NV; ++i) {
+      const int c = tid + i * S_THREADS;
+      if constexpr (decltype(col_)::value) {
+        *reinterpret_cast<float4*>(s + c / (R / 4) * (R + 4) + c % (R / 4) * 4) = v[i];
+      } else {
+        float* q = s + c % (BK / 4) * 4 * (R + 1) + c / (BK / 4);
+        q[0] = v[i].x, q[R + 1] = v[i].y, q[2 * (R + 1)] = v[i].z, q[3 * (R + 1)] = v[i].w;
       }
     }
+  };
+  const std::integral_constant<int, 64> ra;
+  const std::integral_constant<int, TN> rb;
+  const std::integral_constant<bool, CA> ca;
+  const std::integral_constant<bool, CB> cb;
+  float4 va[64 * BK / 4 / S_THREADS], vb[TN * BK / 4 / S_THREADS];
+  fetch(pa, ra, ca, 0, va);
+  fetch(pb, rb, cb, 0, vb);
+  const float* ar = As + (kg * 32 + (lane >> 5)) * (CA ? 68 : 65) + wm * 32 + (lane & 31);
+  const float* br = Bs + (kg * 32 + (lane >> 5)) * (TN + (CB ? 4 : 1)) + wn * 32 + (lane & 31);
+  for (int k0 = 0; k0 < K; k0 += BK) {
+    __syncthreads();
+    put(As, ra, ca, va);
+    put(Bs, rb, cb, vb);
+    __syncthreads();
+    if (k0 + BK < K) {
+      fetch(pa, ra, ca, k0 + BK, va);
+      fetch(pb, rb, cb, k0 + BK, vb);
+    }
+#pragma unroll
+    for (int k = 0; k < 32; k += 2)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(br[k * (TN + (CB ? 4 : 1))], ar[k * (CA ? 68 : 65)], acc, 0, 0, 0);
   }
 }
 
-template <bool GU, class Store>
+// As drain: GU, the first half of the tile's columns are gate, the second up.
+template <int TN, bool GU, class Store>
 __device__ __forceinline__ void drain_f32(float* st, const f32x16_t& acc, Store store) {
+  using S = STile<TN>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int row = (wave >> 1) * 32 + (lane & 31);
+  const int blk = wave % S::BLOCKS, kg = wave / S::BLOCKS;
+  const int row = (blk & 1) * 32 + (lane & 31);
+  constexpr int X = TN / 4 - 1 < 15 ? TN / 4 - 1 : 15;
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int c4 = ((wave & 1) * 32 + q * 8 + (lane >> 5) * 4) / 4;
+    const int c4 = ((blk >> 1) * 32 + q * 8 + (lane >> 5) * 4) / 4;
     const f32x4_t v = {acc[q * 4], acc[q * 4 + 1], acc[q * 4 + 2], acc[q * 4 + 3]};
-    *reinterpret_cast<f32x4_t*>(st + row * 64 + ((c4 ^ (row & 15)) * 4)) = v;
+    *reinterpret_cast<f32x4_t*>(st + (kg * 64 + row) * TN + ((c4 ^ (row & X)) * 4)) = v;
   }
   __syncthreads();
-  constexpr int W = GU ? 32 : 64;
-  for (int c = tid; c < 64 * (W / 8); c += THREADS) {
+  constexpr int W = GU ? TN / 2 : TN;
+  for (int c = tid; c < 64 * (W / 8); c += S_THREADS) {
     const int r = c / (W / 8), col = (c % (W / 8)) * 8;
     auto get = [&](int col_, float* v) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + r * 64 + (((col_ / 4 + h) ^ (r & 15)) * 4));
+        f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < S::GROUPS; ++g)
+          x += *reinterpret_cast<const f32x4_t*>(st + (g * 64 + r) * TN + (((col_ / 4 + h) ^ (r & X)) * 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[h * 4 + i] = x[i];
       }
@@ -526,7 +549,7 @@ __device__ __forceinline__ void drain_f32(float* st, const f32x16_t& acc, Store 
     get(col, v);
     if constexpr (GU) {
       float u[8];
-      get(col + 32, u);
+      get(col + TN / 2, u);
       store(r, col, v, u);
     } else {
       store(r, col, v);

@@ -75,9 +75,81 @@ __device__ __forceinline__ float row_reduce(float v, Op op) {
   return op(v, ror(v, std::integral_constant<int, 1>{}));
 }
 
-// Steps 1 and 2 for Ep <= 128: 128 tokens a workgroup.  The logits go through
-// LDS (fp32, 16-byte chunks XORed with the row); then 16 lanes take a row, 8
-// experts a lane, 16 rows at a time.
+// Steps 1 and 2 in one: the logits of ROWS tokens from m0 lie in LDS, get(r, c,
+// v) reads NC of them; 16 lanes take a row, NC experts a lane, the workgroup
+// THREADS / 16 rows at a time.  db partials to row blockIdx.x of pdb.  The
+// caller has synchronised; `part` (THREADS NC floats) may be the logits' LDS.
+template <typename T, int NC, int ROWS, int THREADS, class Get>
+__device__ __forceinline__ void softmax_rows(const GateArgs<T>& p, int m0, float* part, Get get) {
+  const int tid = threadIdx.x, lane = tid & 63, s = tid & 15, c = s * NC;
+  auto add = [](float a, float b) { return a + b; };
+  float bias[NC], db[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    bias[i] = c + i < p.E ? p.b[c + i] : 0.f;
+    db[i] = 0.f;
+  }
+  for (int pass = 0; pass < ROWS / (THREADS / 16); ++pass) {
+    const int r = pass * (THREADS / 16) + (tid >> 4), t = m0 + r;
+    const bool on = t < p.Ttok;
+    const int id = on && s < p.k ? p.idx[(size_t)t * p.k + s] : -1;
+    const float g = on && s < p.k ? p.dwts[(size_t)t * p.k + s] : 0.f;
+    float z[NC], q[NC];
+    float m = -INFINITY, sum = 0.f, pq = 0.f;
+    get(r, c, z);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      z[i] = c + i < p.E ? z[i] + bias[i] : -INFINITY;
+      m = fmaxf(m, z[i]);
+      q[i] = 0.f;
+    }
+    m = row_reduce(m, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      z[i] = c + i < p.E ? (sizeof(T) == 2 ? __expf(z[i] - m) : expf(z[i] - m)) : 0.f;
+      sum += z[i];
+    }
+    sum = 1.0f / row_reduce(sum, add);
+    for (int j = 0; j < p.k; ++j) {
+      const int e = __shfl(id, (lane & 48) + j, 64) - c;
+      const float gj = __shfl(g, (lane & 48) + j, 64);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) q[i] += e == i ? gj : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      z[i] *= sum;
+      pq += z[i] * q[i];
+    }
+    pq = row_reduce(pq, add);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      z[i] = on && c + i < p.E ? z[i] * (q[i] - pq) : 0.f;
+      db[i] += z[i];
+    }
+    // dz is rounded to the storage type: the matrix products that read it take
+    // it beside h and w of that type
+    if (on && c < p.Ep) {
+      if constexpr (NC == 8)
+        mt::store8(p.dz + (size_t)t * p.Ep + c, z);
+      else
+        *reinterpret_cast<float4*>(p.dz + (size_t)t * p.Ep + c) = make_float4(z[0], z[1], z[2], z[3]);
+    }
+  }
+  // db: the lanes of an expert, added in order
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NC; ++i) part[(tid >> 4) * 16 * NC + c + i] = db[i];
+  __syncthreads();
+  if (tid < p.Ep) {
+    float v = 0.f;
+    for (int i = 0; i < THREADS / 16; ++i) v += part[i * 16 * NC + tid];
+    p.pdb[(size_t)blockIdx.x * p.Ep + tid] = v;
+  }
+}
+
+// E <= 128, bf16: 128 tokens a workgroup.
+template <int D>
 __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t> p) {
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
@@ -88,75 +160,36 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
     ob.init(p.w, bytes32((size_t)p.E * p.d * 2), p.d, p.d, [&](int r) { return min(r, p.E - 1); });
     const int KT = (p.d + mt::BK - 1) / mt::BK;
     f32x16_t acc[GF][GF];
-    mt::k_loop<GF, false>(lds, oa, ob, KT, acc, blockIdx.x % KT);
+    mt::k_loop<GF, false, D>(lds, oa, ob, KT, acc, blockIdx.x % KT);
     mt::stage<GF, false, 0>(lds, acc);
   }
-  const float* st = reinterpret_cast<const float*>(smem);
-  const int tid = threadIdx.x, lane = tid & 63, s = tid & 15, c = s * 8;
-  float bias[8], db[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = c + i < p.E ? p.b[c + i] : 0.f;
-    db[i] = 0.f;
-  }
   __syncthreads();
-  for (int pass = 0; pass < GB / 16; ++pass) {
-    const int r = pass * 16 + (tid >> 4), t = m0 + r;
-    const bool on = t < p.Ttok;
-    const int id = on && s < p.k ? p.idx[(size_t)t * p.k + s] : -1;
-    const float g = on && s < p.k ? p.dwts[(size_t)t * p.k + s] : 0.f;
-    float z[8], q[8];
-    float m = -INFINITY, sum = 0.f, pq = 0.f;
+  float* st = reinterpret_cast<float*>(smem);
+  softmax_rows<uint16_t, 8, GB, mt::THREADS>(p, m0, st, [&](int r, int c, float* z) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + r * GB + (((2 * s + h) ^ (r & 15)) * 4));
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + r * GB + ((c / 4 + h) ^ (r & 15)) * 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[h * 4 + i] = x[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      z[i] = c + i < p.E ? z[i] + bias[i] : -INFINITY;
-      m = fmaxf(m, z[i]);
-      q[i] = 0.f;
-    }
-    m = row_reduce(m, [](float a, float b) { return fmaxf(a, b); });
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      z[i] = c + i < p.E ? __expf(z[i] - m) : 0.f;
-      sum += z[i];
-    }
-    sum = 1.0f / row_reduce(sum, [](float a, float b) { return a + b; });
-    for (int j = 0; j < p.k; ++j) {
-      const int e = __shfl(id, (lane & 48) + j, 64) - c;
-      const float gj = __shfl(g, (lane & 48) + j, 64);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] += e == i ? gj : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      z[i] *= sum;
-      pq += z[i] * q[i];
-    }
-    pq = row_reduce(pq, [](float a, float b) { return a + b; });
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      z[i] = on && c + i < p.E ? z[i] * (q[i] - pq) : 0.f;
-      db[i] += z[i];
-    }
-    if (on && c < p.Ep) mt::store8(p.dz + (size_t)t * p.Ep + c, z);
-  }
-  // db: 16 rows' lanes per expert, added in order
+  });
+}
+
+// E <= 64, fp32: 64 tokens a workgroup.
+__global__ __launch_bounds__(mt::S_THREADS) void gate_dz_f32_kernel(GateArgs<float> p) {
+  __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
+  const int m0 = blockIdx.x * 64;
+  f32x16_t acc;
+  auto pa = [&](int r, int k) { return m0 + r < p.Ttok ? p.h + (size_t)(m0 + r) * p.d + k : nullptr; };
+  auto pb = [&](int r, int k) { return r < p.E ? p.w + (size_t)r * p.d + k : nullptr; };
+  mt::k_loop_f32<64, false, false>(lds, pa, pb, p.d, acc);
+  mt::stage_f32<64>(lds, acc);
   __syncthreads();
-  float* part = reinterpret_cast<float*>(smem);
+  softmax_rows<float, 4, 64, mt::S_THREADS>(p, m0, lds, [&](int r, int c, float* z) {
+    const f32x4_t x = mt::staged_f32<64>(lds, r, c / 4);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[(tid >> 4) * GB + c + i] = db[i];
-  __syncthreads();
-  if (tid < p.Ep) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v += part[i * GB + tid];
-    p.pdb[(size_t)blockIdx.x * p.Ep + tid] = v;
-  }
+    for (int i = 0; i < 4; ++i) z[i] = x[i];
+  });
 }
 
 __global__ __launch_bounds__(mt::S_THREADS) void gate_logits_f32_kernel(GateArgs<float> p) {
@@ -447,10 +480,11 @@ GateLayout gate_layout(int T, int d, int E, int dtype) {
   GateLayout l;
   const size_t eb = moelb_elem_bytes(dtype);
   l.Ep = (E + 63) & ~63;
-  // db partials: one a 128-token tile (bf16, E <= 128), else 16 tokens a
+  // db partials: one a tile (bf16: 128 tokens, E <= 128; fp32: 64, 64), else 16 tokens a
   // workgroup, at most 1024 of them
-  l.fused = dtype == MOELB_BF16 && l.Ep <= GB;
-  l.blocks = l.fused ? (T + GB - 1) / GB : (T + 15) / 16;
+  const int tok = dtype == MOELB_BF16 ? GB : 64;
+  l.fused = l.Ep <= tok;
+  l.blocks = l.fused ? (T + tok - 1) / tok : (T + 15) / 16;
   l.blocks = l.blocks < 1 ? 1 : !l.fused && l.blocks > 1024 ? 1024 : l.blocks;
   // dW: parts of at least 256 tokens, about a workgroup a compute unit (bf16:
   // they run beside nothing else, so two)
@@ -502,8 +536,15 @@ int launch_dh(const GateArgs<uint16_t>& p, hipStream_t s) {
 int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
   constexpr size_t lds = mt::lds_bytes<GF>();
   if (p.Ttok > 0 && fused) {
-    if (!moelb_allow_lds(gate_dz_kernel, lds)) return MOELB_ELAUNCH;
-    hipLaunchKernelGGL(gate_dz_kernel, dim3(p.blocks), dim3(mt::THREADS), lds, s, p);
+    // a deeper ring where a round of the compute units holds all tiles
+    const bool deep = p.blocks <= moelb_compute_units();
+    constexpr size_t lds4 = mt::lds_bytes<GF, 4>();
+    if (!(deep ? moelb_allow_lds(gate_dz_kernel<4>, lds4) : moelb_allow_lds(gate_dz_kernel<2>, lds)))
+      return MOELB_ELAUNCH;
+    if (deep)
+      hipLaunchKernelGGL(gate_dz_kernel<4>, dim3(p.blocks), dim3(mt::THREADS), lds4, s, p);
+    else
+      hipLaunchKernelGGL(gate_dz_kernel<2>, dim3(p.blocks), dim3(mt::THREADS), lds, s, p);
     MOELB_CHECK_LAUNCH();
   } else {
     if (p.Ttok > 0) {
@@ -534,13 +575,19 @@ int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
   }
 }
 
-int run(GateArgs<float> p, bool, hipStream_t s) {
-  if (p.Ttok > 0) {
-    hipLaunchKernelGGL(gate_logits_f32_kernel, dim3((p.Ttok + 63) / 64, (p.E + 63) / 64), dim3(mt::S_THREADS), 0, s, p);
+int run(GateArgs<float> p, bool fused, hipStream_t s) {
+  if (fused) {
+    hipLaunchKernelGGL(gate_dz_f32_kernel, dim3(p.blocks), dim3(mt::S_THREADS), 0, s, p);
     MOELB_CHECK_LAUNCH();
+  } else {
+    if (p.Ttok > 0) {
+      hipLaunchKernelGGL(gate_logits_f32_kernel, dim3((p.Ttok + 63) / 64, (p.E + 63) / 64), dim3(mt::S_THREADS), 0, s,
+                         p);
+      MOELB_CHECK_LAUNCH();
+    }
+    const int st = launch_softmax(p, s);
+    if (st != MOELB_OK) return st;
   }
-  const int st = launch_softmax(p, s);
-  if (st != MOELB_OK) return st;
   const size_t ntn = (p.d + 63) / 64;
   const size_t nh = p.dh && p.Ttok > 0 ? (size_t)((p.Ttok + 63) / 64) * ntn : 0;
   const size_t nw = p.dw ? (size_t)((p.E + 63) / 64) * ntn * p.splits : 0;

@@ -314,7 +314,7 @@ __device__ __forceinline__ bool tile_of(const AdapterArgs& p, int B, int& mi, in
   return true;
 }
 
-template <int F, int D, bool GU>
+template <int F, bool GU>
 __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p) {
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
                bytes32((size_t)p.d_out * p.r * 2), p.r, p.r, wrow);
   oa.first = ob.first = (p.d_in + mt::BK - 1) / mt::BK;
   f32x16_t acc[F][F];
-  mt::k_loop<F, GU, D>(lds, oa, ob, oa.first + (id >= 0 ? (p.r + mt::BK - 1) / mt::BK : 0), acc);
+  mt::k_loop<F, GU>(lds, oa, ob, oa.first + (id >= 0 ? (p.r + mt::BK - 1) / mt::BK : 0), acc);
   if (p.n > 0 && id < 0) {
     const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
     const uint16_t* low[F];
@@ -656,15 +656,14 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
 
 constexpr int FEW_TOKENS = 64;
 
-template <int F, int D, bool GU>
+template <int F, bool GU>
 int launch_tile(AdapterArgs p, hipStream_t s) {
   const int B = 64 * F, bn = GU ? B / 2 : B, out = GU ? p.d_out / 2 : p.d_out;
   p.ntn = (out + bn - 1) / bn;
   const size_t grid = ((size_t)((p.Ttok + B - 1) / B) * p.ntn + 7) / 8 * 8;
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
-  constexpr size_t lds = mt::lds_bytes<F, D>();
-  if (!moelb_allow_lds(adapter_tile_kernel<F, D, GU>, lds)) return MOELB_ELAUNCH;
-  hipLaunchKernelGGL((adapter_tile_kernel<F, D, GU>), dim3((unsigned)grid), dim3(mt::THREADS), lds, s, p);
+  if (!moelb_allow_lds(adapter_tile_kernel<F, GU>, mt::lds_bytes<F>())) return MOELB_ELAUNCH;
+  hipLaunchKernelGGL((adapter_tile_kernel<F, GU>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<F>(), s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
@@ -741,9 +740,7 @@ int launch_prompts(AdapterArgs p, hipStream_t s) {
     MOELB_CHECK_LAUNCH();
   }
   const size_t tiles = (size_t)((p.Ttok + 255) / 256) * ((p.d_out + 255) / 256);
-  if (tiles >= 192) return launch_tile<4, 2, GU>(p, s);
-  const size_t tiles2 = (size_t)((p.Ttok + 127) / 128) * ((p.d_out + 127) / 128);
-  return tiles2 <= (size_t)moelb_compute_units() ? launch_tile<2, 4, GU>(p, s) : launch_tile<2, 2, GU>(p, s);
+  return tiles >= 192 ? launch_tile<4, GU>(p, s) : launch_tile<2, GU>(p, s);
 }
 
 }  // namespace

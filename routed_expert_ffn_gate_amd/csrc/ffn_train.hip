@@ -94,7 +94,7 @@ __device__ __forceinline__ void put_da(const TrainArgs<T>& p, int v, int n, cons
 // ---------------------------------------------------------------- row-tiled products
 
 // Workgroup `block` of the product OP.
-template <int F, int D, int OP>
+template <int F, int OP>
 __device__ __forceinline__ void rows_tile(const TrainArgs<uint16_t>& p, int block, uint16_t* lds) {
   const int n_mtiles = *p.s.n_mtiles;
   const int tile = xcd_tile(block, n_mtiles * p.ntn);
@@ -129,12 +129,12 @@ __device__ __forceinline__ void rows_tile(const TrainArgs<uint16_t>& p, int bloc
       const int c = n0 + (GU ? r % HB : r);
       return (c < N ? c : 0) + (GU && r >= HB ? I : 0);
     });
-    mt::k_loop<F, GU, D>(lds, oa, ob, KT, acc);
+    mt::k_loop<F, GU>(lds, oa, ob, KT, acc);
   } else {
     mt::ColOp<F, false> ob;
     const uint16_t* w = OP == OP_DA ? p.w2 + (size_t)e * d * I : p.w13 + (size_t)e * 2 * I * d;
     ob.init(w, bytes_u32((size_t)K * N * 2), N, K, n0, N);
-    mt::k_loop<F, GU, D>(lds, oa, ob, KT, acc);
+    mt::k_loop<F, GU>(lds, oa, ob, KT, acc);
   }
   if constexpr (GU) {
     mt::drain<F, true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
@@ -312,10 +312,10 @@ __device__ __forceinline__ void weights_tile(const TrainArgs<float>& p, int bloc
 
 // ---------------------------------------------------------------- kernels
 
-template <int F, int D, int OP>
+template <int F, int OP>
 __global__ __launch_bounds__(mt::THREADS) void train_rows_kernel(TrainArgs<uint16_t> p) {
   extern __shared__ __align__(16) char smem[];
-  rows_tile<F, D, OP>(p, blockIdx.x, reinterpret_cast<uint16_t*>(smem));
+  rows_tile<F, OP>(p, blockIdx.x, reinterpret_cast<uint16_t*>(smem));
 }
 template <int TN, int OP>
 __global__ __launch_bounds__(mt::S_THREADS) void train_rows_f32_kernel(TrainArgs<float> p) {
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(mt::THREADS) void train_grads_kernel(GradArgs<uint1
   int b = blockIdx.x;
   const int x0 = g.x_first ? 0 : g.n13 + g.n2;
   if (b >= x0 && b < x0 + g.nx) {
-    rows_tile<F, 2, OP_DX>(g.x, b - x0, lds);
+    rows_tile<F, OP_DX>(g.x, b - x0, lds);
     return;
   }
   if (g.x_first) b -= g.nx;
@@ -460,21 +460,12 @@ int launch_rows(TrainArgs<T> p, int BM, int BN, hipStream_t s) {
       hipLaunchKernelGGL((train_rows_f32_kernel<64, OP>), g, dim3(mt::S_THREADS), 0, s, p);
     else
       hipLaunchKernelGGL((train_rows_f32_kernel<32, OP>), g, dim3(mt::S_THREADS), 0, s, p);
+  } else if (BM == 256) {
+    if (!moelb_allow_lds(train_rows_kernel<4, OP>, mt::lds_bytes<4>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_rows_kernel<4, OP>), g, dim3(mt::THREADS), mt::lds_bytes<4>(), s, p);
   } else {
-    // 128-row tiles that a round of the compute units holds: a deeper ring
-    // instead of a second workgroup a CU (1111 tokens on 3 experts, d = 1000,
-    // inter = 520: up 19 -> 1x us)
-    auto go = [&](auto kernel, size_t lds) {
-      if (!moelb_allow_lds(kernel, lds)) return MOELB_ELAUNCH;
-      hipLaunchKernelGGL(kernel, g, dim3(mt::THREADS), lds, s, p);
-      return MOELB_OK;
-    };
-    const size_t tiles = (size_t)(p.rows + BM - 1) / BM * p.ntn;
-    const int st = BM == 256 ? go(train_rows_kernel<4, 2, OP>, mt::lds_bytes<4>())
-                   : tiles <= (size_t)moelb_compute_units()
-                       ? go(train_rows_kernel<2, 4, OP>, mt::lds_bytes<2, 4>())
-                       : go(train_rows_kernel<2, 2, OP>, mt::lds_bytes<2>());
-    if (st != MOELB_OK) return st;
+    if (!moelb_allow_lds(train_rows_kernel<2, OP>, mt::lds_bytes<2>())) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL((train_rows_kernel<2, OP>), g, dim3(mt::THREADS), mt::lds_bytes<2>(), s, p);
   }
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;

@@ -149,7 +149,6 @@ __device__ __forceinline__ void softmax_rows(const GateArgs<T>& p, int m0, float
 }
 
 // E <= 128, bf16: 128 tokens a workgroup.
-template <int D>
 __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t> p) {
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
@@ -160,7 +159,7 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
     ob.init(p.w, bytes32((size_t)p.E * p.d * 2), p.d, p.d, [&](int r) { return min(r, p.E - 1); });
     const int KT = (p.d + mt::BK - 1) / mt::BK;
     f32x16_t acc[GF][GF];
-    mt::k_loop<GF, false, D>(lds, oa, ob, KT, acc, blockIdx.x % KT);
+    mt::k_loop<GF, false>(lds, oa, ob, KT, acc, blockIdx.x % KT);
     mt::stage<GF, false, 0>(lds, acc);
   }
   __syncthreads();
@@ -536,15 +535,8 @@ int launch_dh(const GateArgs<uint16_t>& p, hipStream_t s) {
 int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
   constexpr size_t lds = mt::lds_bytes<GF>();
   if (p.Ttok > 0 && fused) {
-    // a deeper ring where a round of the compute units holds all tiles
-    const bool deep = p.blocks <= moelb_compute_units();
-    constexpr size_t lds4 = mt::lds_bytes<GF, 4>();
-    if (!(deep ? moelb_allow_lds(gate_dz_kernel<4>, lds4) : moelb_allow_lds(gate_dz_kernel<2>, lds)))
-      return MOELB_ELAUNCH;
-    if (deep)
-      hipLaunchKernelGGL(gate_dz_kernel<4>, dim3(p.blocks), dim3(mt::THREADS), lds4, s, p);
-    else
-      hipLaunchKernelGGL(gate_dz_kernel<2>, dim3(p.blocks), dim3(mt::THREADS), lds, s, p);
+    if (!moelb_allow_lds(gate_dz_kernel, lds)) return MOELB_ELAUNCH;
+    hipLaunchKernelGGL(gate_dz_kernel, dim3(p.blocks), dim3(mt::THREADS), lds, s, p);
     MOELB_CHECK_LAUNCH();
   } else {
     if (p.Ttok > 0) {

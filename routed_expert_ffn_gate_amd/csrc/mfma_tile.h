@@ -9,12 +9,10 @@
 //  * Tile 64F x 64F, F = 4 (256) or F = 2 (128); 256 threads as 2 x 2 waves,
 //    wave tile 32F x 32F of v_mfma_f32_32x32x16_bf16, fp32 accumulators.
 //  * K steps of 64 stream memory -> LDS with buffer_load_dwordx4 ... lds into a
-//    ring of 2 D + 1 half-stages (A or B of one step; 32 KiB each at F = 4, 16
-//    KiB at F = 2): while step t computes, steps t+1 .. t+D-1 and half of t+D
-//    are in flight.  D = 2 fills the LDS at F = 4 and leaves room for two F = 2
-//    workgroups a CU; D = 4 at F = 2 is for calls with no more tiles than
-//    compute units, whose steps are shorter than a load's way.  The refills are
-//    spread over the step, one instruction per F MFMAs.
+//    ring of five half-stages (A or B of one step; 32 KiB each at F = 4, 16 KiB
+//    at F = 2, so two F = 2 workgroups share a CU): while step t computes,
+//    steps t+1 and half of t+2 are in flight.  The refills are spread over the
+//    step, one instruction per F MFMAs.
 //  * The loads go through a buffer descriptor: a lane whose k lies past the end
 //    asks for an offset outside the descriptor and gets zeros in LDS, which is
 //    how K tails and ragged token counts end inside a step without a branch.
@@ -36,6 +34,7 @@
 namespace mt {
 
 constexpr int BK = 64;
+constexpr int SLOTS = 5;
 constexpr int THREADS = 256;
 // outside every descriptor below (their byte counts stay under it)
 constexpr uint32_t OUTSIDE = 0xfffffff0u;
@@ -47,8 +46,8 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 template <int F>
 constexpr int half_elems() { return 64 * F * BK; }
 // the ring; the epilogue stages 128 rows x 64F fp32 in the same space
-template <int F, int D = 2>
-constexpr size_t lds_bytes() { return (size_t)(2 * D + 1) * half_elems<F>() * sizeof(uint16_t); }
+template <int F>
+constexpr size_t lds_bytes() { return (size_t)SLOTS * half_elems<F>() * sizeof(uint16_t); }
 
 __device__ __forceinline__ i32x4_t descriptor(const void* p, uint32_t bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(p);
@@ -224,19 +223,6 @@ __device__ __forceinline__ int block_col(int wn, int ni) {
   return GU ? wn * 16 * F + (ni % (F / 2)) * 32 + (ni / (F / 2)) * 32 * F : wn * 32 * F + ni * 32;
 }
 
-// Waits until at most n half-stages of NI loads each (n <= MAX) are in flight,
-// and for this wave's LDS reads.
-template <int NI, int MAX>
-__device__ __forceinline__ void wait_halves(int n) {
-  if constexpr (MAX > 0) {
-    if (n < MAX) {
-      wait_halves<NI, MAX - 1>(n);
-      return;
-    }
-  }
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(MAX * NI) : "memory");
-}
-
 // The K loop: acc[mi][ni] += A block mi x B block ni over KT >= 1 steps, from
 // step `turn` (< KT) on and around.  Rows a multiple of 4 KiB apart have the
 // same k on the same memory channel: workgroups that all read k = 0, then k =
@@ -245,9 +231,9 @@ __device__ __forceinline__ void wait_halves(int n) {
 // acc holds each 32x32 block transposed (the B fragment is the MFMA's first
 // operand): lane -> row lane % 32 of block mi, element j -> column (j / 4) * 8 +
 // (lane / 32) * 4 + j % 4 of block ni.
-template <int F, bool GU, int D = 2, class OA, class OB>
+template <int F, bool GU, class OA, class OB>
 __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f32x16_t (&acc)[F][F], int turn = 0) {
-  constexpr int HALF = half_elems<F>(), SLOTS = 2 * D + 1;
+  constexpr int HALF = half_elems<F>();
   constexpr int NI = 2 * F;  // DMA instructions per half-stage and wave
   const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -304,19 +290,25 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
 #pragma unroll
     for (int jj = 0; jj < NI; ++jj) MT_ISSUE(j, jj)
   }
-  // A_0 and B_0 landed: the later half-stages may be in flight
-  wait_halves<NI, 2 * D - 1>(min(SLOTS, nh) - 2);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  {
+    const int after = min(SLOTS, nh) - 2;  // half-stages that may still be in flight
+    if (after >= 3)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * NI) : "memory");
+    else if (after == 2)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NI) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
 #pragma unroll
   for (int i = 0; i < F; ++i) {
     xa[i] = MT_RA(lds, 0, i);
     xb[i] = MT_RB(lds + HALF, 0, i);
   }
-  // One K step kt.  B1: issue the second half of B_kt+D-1; A2: issue A_kt+D;
-  // MORE: a step follows; B2: issue the first half of B_kt+D.  AFTER: the
-  // half-stages issued behind step kt+1's.
-#define MT_STEP(KT_, B1, A2, MORE, B2, AFTER)                                                                 \
+  // One K step kt.  B1: issue the second half of B_kt+1; A2: issue A_kt+2;
+  // MORE: a step follows; B2: issue the first half of B_kt+2.
+#define MT_STEP(KT_, B1, A2, MORE, B2)                                                                        \
   {                                                                                                           \
     const int kt_ = (KT_);                                                                                    \
     int o0 = ((2 * kt_) % SLOTS) * HALF, o1 = ((2 * kt_ + 1) % SLOTS) * HALF;                                 \
@@ -325,33 +317,33 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
     asm volatile("" : "+s"(o0), "+s"(o1), "+s"(o2), "+s"(o3));                                                \
     const uint16_t* sa = lds + o0;                                                                            \
     const uint16_t* sb = lds + o1;                                                                            \
-    MT_SUB(xa, xb, ya, yb, sa, sb, 1, true, B1, 2 * kt_ + 2 * D - 1, F)                                       \
-    if (A2) oa.begin(kt_ + D);                                                                                \
-    MT_SUB(ya, yb, xa, xb, sa, sb, 2, true, A2, 2 * kt_ + 2 * D, 0)                                           \
-    MT_SUB(xa, xb, ya, yb, sa, sb, 3, true, A2, 2 * kt_ + 2 * D, F)                                           \
+    MT_SUB(xa, xb, ya, yb, sa, sb, 1, true, B1, 2 * kt_ + 3, F)                                               \
+    if (A2) oa.begin(kt_ + 2);                                                                                \
+    MT_SUB(ya, yb, xa, xb, sa, sb, 2, true, A2, 2 * kt_ + 4, 0)                                               \
+    MT_SUB(xa, xb, ya, yb, sa, sb, 3, true, A2, 2 * kt_ + 4, F)                                               \
     if (MORE) {                                                                                               \
-      /* lgkmcnt(0): this wave's reads of step kt are done before any wave                                    \
-         refills its slots */                                                                                 \
-      wait_halves<NI, 2 * D - 3>(AFTER);                                                                      \
+      /* A_kt+2 is the only half-stage issued after B_kt+1; lgkmcnt(0): this                                  \
+         wave's reads of step kt are done before any wave refills its slots */                                \
+      if (B2)                                                                                                 \
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(NI) : "memory");                                  \
+      else                                                                                                    \
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");                                           \
       __builtin_amdgcn_s_barrier();                                                                           \
       asm volatile("" ::: "memory");                                                                          \
     }                                                                                                         \
     const uint16_t* na = lds + o2;                                                                            \
     const uint16_t* nb = lds + o3;                                                                            \
-    if (B2) ob.begin(kt_ + D);                                                                                \
-    MT_SUB(ya, yb, xa, xb, na, nb, 0, MORE, B2, 2 * kt_ + 2 * D + 1, 0)                                       \
+    if (B2) ob.begin(kt_ + 2);                                                                                \
+    MT_SUB(ya, yb, xa, xb, na, nb, 0, MORE, B2, 2 * kt_ + 5, 0)                                               \
   }
-  if (KT >= D + 2) {
-    MT_STEP(0, false, false, true, true, 2 * D - 3)
-    for (int kt = 1; kt + D < KT; ++kt) MT_STEP(kt, true, true, true, true, 2 * D - 3)
-    MT_STEP(KT - D, true, false, true, false, 2 * (D - 2))
-    if constexpr (D > 2)
-      for (int kt = KT - D + 1; kt + 1 < KT; ++kt) MT_STEP(kt, false, false, true, false, 2 * (KT - 2 - kt))
-    MT_STEP(KT - 1, false, false, false, false, 0)
+  if (KT >= 4) {
+    MT_STEP(0, false, false, true, true)
+    for (int kt = 1; kt + 2 < KT; ++kt) MT_STEP(kt, true, true, true, true)
+    MT_STEP(KT - 2, true, false, true, false)
+    MT_STEP(KT - 1, false, false, false, false)
   } else {
     for (int kt = 0; kt < KT; ++kt)
-      MT_STEP(kt, kt >= 1 && kt + D - 1 < KT, kt >= 1 && kt + D < KT, kt + 1 < KT, kt + D < KT,
-              min(2 * D - 3, 2 * (KT - 2 - kt)))
+      MT_STEP(kt, kt >= 1 && kt + 1 < KT, kt >= 1 && kt + 2 < KT, kt + 1 < KT, kt + 2 < KT)
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #undef MT_STEP

@@ -480,8 +480,8 @@ int moelb_pack_weights(const void* w, int E, int rows, int K, int dtype, void* p
  *  ws         train: moelb_grouped_ffn_workspace_bytes(...) bytes; backward:
  *             moelb_grouped_ffn_backward_workspace_bytes(...) bytes; no state
  *             is kept in it between the calls.
- * Requires what moelb_grouped_ffn requires, and rows*d, rows_x*d,
- * rows*2*inter and 2*inter*d elements each below 2^32 - 65536 bytes.
+ * Requires what moelb_grouped_ffn requires, d and inter up to 2^19, and rows*d, rows_x*d,
+ * rows*2*inter and 2*inter*d elements each below 2^32 - 2^21 bytes.
  * All row data, weights, z and ws 16-byte aligned.  Outputs must not overlap
  * the inputs or each other.
  */
@@ -548,7 +548,7 @@ int moelb_combine_backward(const void* dout, const void* y, int rows_y, const in
  *       or NULL (T = 0: dw and db are zero)
  * Ids outside [0,E) are left out; an id listed twice counts twice.
  * Requires 1 <= k <= min(E, 16), E <= 256, d % 8 == 0, T >= 0, T*d elements
- * below 2^32 - 65536 bytes; h, w, ws, dh and dw 16-byte aligned.
+ * below 2^32 - 2^21 bytes; h, w, ws, dh and dw 16-byte aligned.
  */
 size_t moelb_gate_backward_workspace_bytes(int T, int d, int E, int dtype);
 int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, const void* w,
@@ -577,7 +577,7 @@ int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, co
  * ids, a, b and scale may be NULL where n = 0, ws where its size is 0.  Requires d_in % 8 == 0,
  * d_out % 8 == 0 (gated: % 16), n >= 0, r % 8 == 0 and 8 <= r <= 256
  * (n > 0), and T*d_in, d_out*d_in, n*d_out*r and T*r elements each below 2^32 -
- * 65536 bytes; x, w, a, b, ws and y 16-byte aligned.  y must not overlap the
+ * 2^21 bytes; x, w, a, b, ws and y 16-byte aligned.  y must not overlap the
  * inputs.
  */
 size_t moelb_adapter_projection_workspace_bytes(int T, int d_in, int d_out, int n, int r, int dtype);

@@ -45,7 +45,7 @@ struct AdapterArgs {
   int Ttok, d_in, d_out, n, r, ntn, splits, nbase;
 };
 
-__device__ __forceinline__ uint32_t bytes32(size_t n) { return n < mt::OUTSIDE ? (uint32_t)n : mt::OUTSIDE; }
+__device__ __forceinline__ uint32_t bytes32(size_t n) { return n < mt::MAX_BYTES ? (uint32_t)n : (uint32_t)mt::MAX_BYTES; }
 __device__ __forceinline__ int id_of(const AdapterArgs& p, int t) {
   const int id = p.n > 0 ? p.ids[t] : -1;
   return id >= 0 && id < p.n ? id : -1;
@@ -466,11 +466,11 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
     const int k = (s0 + i) * 64;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      mt::copy16(wck[j] + k < p.d_in ? woff[j] + (uint32_t)k * 2u : mt::OUTSIDE, ws,
+      mt::copy16(wck[j] + k < p.d_in ? woff[j] : mt::OUTSIDE, ws, (uint32_t)k * 2u,
                  st + (uint32_t)((wave * 2 + j) * 512) * 2u);
 #pragma unroll
     for (int j = 0; j < NX; ++j)
-      mt::copy16(xck[j] + k < p.d_in ? xoff[j] + (uint32_t)k * 2u : mt::OUTSIDE, xs,
+      mt::copy16(xck[j] + k < p.d_in ? xoff[j] : mt::OUTSIDE, xs, (uint32_t)k * 2u,
                  st + (uint32_t)(64 * 64 + xblk[j] * 512) * 2u);
   };
   f32x4_t acc[NB];
@@ -765,7 +765,7 @@ extern "C" int moelb_adapter_projection(const void* x, int T, int d_in, int d_ou
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(a) |
        reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(y)) & 15)
     return MOELB_EINVAL;
-  const size_t eb = moelb_elem_bytes(dtype), most = (1ull << 32) - 65536;
+  const size_t eb = moelb_elem_bytes(dtype), most = mt::MAX_BYTES;
   if ((size_t)T * d_in * eb >= most || (size_t)d_out * d_in * eb >= most ||
       (n > 0 && ((size_t)n * d_out * r * eb >= most || (size_t)T * r * eb >= most)))
     return MOELB_EINVAL;

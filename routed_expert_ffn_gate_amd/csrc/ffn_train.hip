@@ -53,7 +53,7 @@ struct TrainArgs {
 };
 
 __device__ __forceinline__ uint32_t bytes_u32(size_t n) {
-  return n < mt::OUTSIDE ? (uint32_t)n : mt::OUTSIDE;
+  return n < mt::MAX_BYTES ? (uint32_t)n : (uint32_t)mt::MAX_BYTES;
 }
 
 __device__ __forceinline__ int clampi(int v, int n) { return min(max(v, 0), n - 1); }
@@ -487,10 +487,12 @@ bool sizes_ok(int rows_x, int rows, int num_groups, int E, int G, int rank, cons
               int inter, int dtype) {
   if (rows < 0 || rows_x < 0 || num_groups < 1 || num_groups > 32768 || E < 1 || E > MOELB_MAX_E) return false;
   if (d <= 0 || d % 8 != 0 || inter <= 0 || inter % 8 != 0 || !moelb_dtype_ok(dtype)) return false;
+  // a gathered row past the end plus a column stays outside (mt::GONE)
+  if (d > 1 << 19 || inter > 1 << 19) return false;
   if (rank >= 0 && (G < 1 || rank >= G || num_groups % E != 0)) return false;
   if (gather && gather_k < 1) return false;
   if (rows > 0 && rows_x < 1) return false;
-  const size_t eb = moelb_elem_bytes(dtype), most = (1ull << 32) - 65536;
+  const size_t eb = moelb_elem_bytes(dtype), most = mt::MAX_BYTES;
   return (size_t)rows_x * d * eb < most && (size_t)rows * d * eb < most && (size_t)rows * 2 * inter * eb < most &&
          (size_t)2 * inter * d * eb < most;
 }

@@ -42,7 +42,7 @@ struct GateArgs {
   int Ttok, d, E, Ep, k, splits, blocks, nh;  // nh: workgroups of dh in step 3
 };
 
-__device__ __forceinline__ uint32_t bytes32(size_t n) { return n < mt::OUTSIDE ? (uint32_t)n : mt::OUTSIDE; }
+__device__ __forceinline__ uint32_t bytes32(size_t n) { return n < mt::MAX_BYTES ? (uint32_t)n : (uint32_t)mt::MAX_BYTES; }
 
 // ---- 1: logits
 
@@ -623,7 +623,7 @@ extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, in
        reinterpret_cast<uintptr_t>(dw)) & 15)
     return MOELB_EINVAL;
   const size_t eb = moelb_elem_bytes(dtype);
-  if ((size_t)T * d * eb >= (1ull << 32) - 65536) return MOELB_EINVAL;
+  if ((size_t)T * d * eb >= mt::MAX_BYTES) return MOELB_EINVAL;
   const GateLayout l = gate_layout(T, d, E, dtype);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < l.total) return MOELB_EWORKSPACE;
   if (!dh && !dw && !db) return MOELB_OK;

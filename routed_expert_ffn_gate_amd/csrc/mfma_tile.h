@@ -13,11 +13,15 @@
 //    at F = 2, so two F = 2 workgroups share a CU): while step t computes,
 //    steps t+1 and half of t+2 are in flight.  The refills are spread over the
 //    step, one instruction per F MFMAs.
-//  * The loads go through a buffer descriptor: a lane whose k lies past the end
-//    asks for an offset outside the descriptor and gets zeros in LDS, which is
-//    how K tails and ragged token counts end inside a step without a branch.
-//    Rows and columns of C past their end repeat a valid one and are not
-//    stored.
+//  * The loads go through a buffer descriptor: a lane that asks for an offset
+//    outside it gets zeros in LDS, which is how K tails and ragged token counts
+//    end inside a step without a branch.  A column operand's rows past the last
+//    are past the descriptor's end by themselves; a row operand's chunks past K
+//    ask for OUTSIDE.  The K step goes into the scalar offset (which the range
+//    check counts), so a lane's offsets stay in registers and a load costs at
+//    most one vector instruction beside it: the loop's other instructions have
+//    to fit between the MFMAs of the one wave a SIMD runs at F = 4.  Rows and
+//    columns of C past their end repeat a valid one and are not stored.
 //  * Row operand in LDS: 64F rows of 128 B, 16-byte chunks swizzled, fragments
 //    by ds_read_b128.  Column operand: 64 k rows of 128F B, 64-byte segments
 //    XORed with the k row, fragments by two ds_read_b64_tr_b16 (each 16 lanes
@@ -36,8 +40,11 @@ namespace mt {
 constexpr int BK = 64;
 constexpr int SLOTS = 5;
 constexpr int THREADS = 256;
-// outside every descriptor below (their byte counts stay under it)
-constexpr uint32_t OUTSIDE = 0xfffffff0u;
+// Outside every descriptor: operands are under MAX_BYTES.  GONE: the row offset
+// of a gathered k row past the end; a column offset (under 1 MiB) on top of it
+// stays outside.
+constexpr uint32_t OUTSIDE = 0xfffffff0u, GONE = 0xffe00000u;
+constexpr size_t MAX_BYTES = 0xffe00000u;
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -59,13 +66,14 @@ __device__ __forceinline__ i32x4_t descriptor(const void* p, uint32_t bytes) {
   return r;
 }
 
-// 16 bytes per lane, memory -> LDS: lane i lands at LDS byte address m0 + 16 i;
-// an offset outside the descriptor writes zeros.  M0 is a reserved register
-// (the build checks that no compiler code uses it).
+// 16 bytes per lane, memory (base + voff + soff) -> LDS: lane i lands at LDS
+// byte address m0 + 16 i; an offset outside the descriptor writes zeros.  M0 is
+// a reserved register (the build checks that no compiler code uses it).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void copy16(uint32_t voff, i32x4_t srd, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(srd), "s"(m0)
+__device__ __forceinline__ void copy16(uint32_t voff, i32x4_t srd, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(voff), "s"(srd),
+               "s"(m0), "s"(soff)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -78,46 +86,48 @@ struct RowOp {
   static constexpr bool COL = false;
   i32x4_t srd;
   uint32_t off[2 * F];
-  int ck[2];  // first k of this lane's chunk, even and odd instructions
-  int K;
+  int last;    // steps below it are whole
+  bool in[2];  // this lane's chunk lies below K in step `last` (even and odd instructions)
   // row(r): memory row of LDS row r, ld: elements per memory row
   template <class Row>
-  __device__ __forceinline__ void init(const void* base, uint32_t bytes, int ld, int K_, Row row) {
+  __device__ __forceinline__ void init(const void* base, uint32_t bytes, int ld, int K, Row row) {
     srd = descriptor(base, bytes);
-    K = K_;
+    last = K / BK;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < 2 * F; ++j) {
       const int r = (wave * 2 * F + j) * 8 + (lane >> 3);
       const int chunk = (lane & 7) ^ (((r >> 1) ^ (r << 2)) & 7);
-      if (j < 2) ck[j] = chunk * 8;
+      if (j < 2) in[j] = chunk * 8 < K - last * BK;
       off[j] = ((uint32_t)row(r) * (uint32_t)ld + (uint32_t)chunk * 8u) * 2u;
     }
   }
   __device__ __forceinline__ void begin(int) {}
   __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
-    const uint32_t v = ck[j & 1] < K - t * BK ? off[j] + (uint32_t)t * (BK * 2) : OUTSIDE;
-    copy16(v, srd, m0);
+    copy16(t < last || in[j & 1] ? off[j] : OUTSIDE, srd, (uint32_t)t * (BK * 2), m0);
   }
 };
 
 // Column operand: memory row = k, columns contiguous.  DMA instruction j of
 // wave w fills k rows 16 w + j R .. (R = 1024 / (128 F) rows of 128F bytes);
 // a lane's 16-byte slot s of its row holds chunk s with its 64-byte segment
-// (s / 4) XORed with the k row.  With GATHER, k row t reads memory row
-// idx[t] clamped to [0, rows).
+// (s / 4) XORed with the k row.  `bytes` are those of the K memory rows, so
+// that rows past them read zeros.  With GATHER, k row t reads memory row
+// idx[t] clamped to [0, rows), and `bytes` are the whole buffer's.
 template <int F, bool GATHER>
 struct ColOp {
   static constexpr bool COL = true;
   static constexpr int R = 8 / F;
+  // distinct column offsets: the XOR takes k % (2F) of k row 16 w + j R + lane
+  // part, which for F = 4 repeats every 4 instructions and for F = 2 always
+  static constexpr int NC = F == 4 ? 4 : 1;
   i32x4_t srd;
-  uint32_t off0;  // byte offset of the lane's column chunk (+ its first k row, if not gathered)
+  uint32_t off[GATHER ? NC : 2 * F];
   uint32_t ld2;
-  int kr;         // this lane's k row in a step, instruction 0
-  int K;
+  int K, sub;  // sub: which of an instruction's R rows this lane loads
   const int32_t* idx;
   int rows;
-  int gi[GATHER ? 8 : 1];
+  uint32_t gi[GATHER ? 8 : 1];
   // columns c0 .. of N; K memory rows from `base` (or from idx)
   __device__ __forceinline__ void init(const void* base, uint32_t bytes, int ld, int K_, int c0, int N,
                                        const int32_t* idx_ = nullptr, int rows_ = 0) {
@@ -127,22 +137,16 @@ struct ColOp {
     idx = idx_;
     rows = rows_;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int rr = lane / (64 / R), s = lane & (8 * F - 1);
-    kr = wave * 16 + rr;
-    // the k row of instruction j is kr + j R; its XOR bits: F = 4 (R = 2)
-    // needs k % 8, which changes with j, F = 2 (R = 4) k % 4, which does not
-    slot = s;
-    col0 = c0;
-    ncols = N;
-    off0 = GATHER ? 0u : (uint32_t)kr * ld2;
+    const int slot = lane & (8 * F - 1);
+    sub = lane / (64 / R);
+#pragma unroll
+    for (int j = 0; j < (GATHER ? NC : 2 * F); ++j) {
+      const int k = wave * 16 + j * R + sub;
+      const int c = c0 + ((((slot >> 2) ^ (k & (2 * F - 1))) << 2) | (slot & 3)) * 8;
+      off[j] = (uint32_t)(c < N ? c : 0) * 2u + (GATHER ? 0u : (uint32_t)k * ld2);
+    }
   }
-  int slot, col0, ncols;
-  __device__ __forceinline__ uint32_t col_off(int j) const {
-    const int k = kr + j * R;
-    const int c = col0 + ((((slot >> 2) ^ (k & (2 * F - 1))) << 2) | (slot & 3)) * 8;
-    return (uint32_t)(c < ncols ? c : 0) * 2u;
-  }
-  // before the first instruction of step t: indices for 32 steps at a time,
+  // before the first instruction of step t: row offsets for 32 steps at a time,
   // four steps a register (lane l: step l / 16, k row l % 16 of the wave)
   __device__ __forceinline__ void begin(int t) {
     if constexpr (GATHER) {
@@ -151,7 +155,7 @@ struct ColOp {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int k = (t + q * 4 + (lane >> 4)) * BK + wave * 16 + (lane & 15);
-          gi[q] = k < K ? min(max(idx[k], 0), rows - 1) : 0;
+          gi[q] = k < K ? (uint32_t)min(max(idx[k], 0), rows - 1) * ld2 : GONE;
         }
       } else if ((t & 3) == 0) {
 #pragma unroll
@@ -160,22 +164,18 @@ struct ColOp {
     }
   }
   __device__ __forceinline__ void issue(int t, int j, uint32_t m0) const {
-    const bool in = kr + j * R < K - t * BK;
-    uint32_t v;
     if constexpr (GATHER) {
       const int l0 = (t & 3) * 16 + j * R;
-      const int lane = threadIdx.x & 63;
-      uint32_t o = (uint32_t)__builtin_amdgcn_readlane(gi[0], l0) * ld2;
+      uint32_t o = __builtin_amdgcn_readlane(gi[0], l0);
 #pragma unroll
       for (int q = 1; q < R; ++q) {
-        const uint32_t oq = (uint32_t)__builtin_amdgcn_readlane(gi[0], l0 + q) * ld2;
-        o = lane / (64 / R) >= q ? oq : o;
+        const uint32_t oq = __builtin_amdgcn_readlane(gi[0], l0 + q);
+        o = sub >= q ? oq : o;
       }
-      v = o + col_off(j);
+      copy16(o + off[j & (NC - 1)], srd, 0, m0);
     } else {
-      v = off0 + (uint32_t)(t * BK + j * R) * ld2 + col_off(j);
+      copy16(off[j], srd, (uint32_t)t * (BK * ld2), m0);
     }
-    copy16(in ? v : OUTSIDE, srd, m0);
   }
 };
 
@@ -251,22 +251,23 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
   const int nh = 2 * KT;
   KT = __builtin_amdgcn_readfirstlane(KT);
   turn = __builtin_amdgcn_readfirstlane(turn);
-#define MT_DST(SLOT, JJ) (lds_u32 + (uint32_t)(((SLOT) * HALF + (wave * NI + (JJ)) * 512) * 2))
-#define MT_ISSUE(J, JJ)                                             \
+  const uint32_t dst0 = lds_u32 + (uint32_t)(wave * NI * 1024);
+  // DMA instruction JJ of step T's A (B: ISB) into the slot at element offset O
+#define MT_ISSUE(T, ISB, O, JJ)                                     \
   {                                                                 \
-    const int j_ = (J);                                             \
-    const int t_ = (j_ >> 1) + turn;                                \
-    if (j_ & 1)                                                     \
-      ob.issue(t_ < KT ? t_ : t_ - KT, (JJ), MT_DST(j_ % SLOTS, JJ)); \
+    const int t_ = (T) + turn, w_ = t_ < KT ? t_ : t_ - KT;         \
+    const uint32_t m_ = dst0 + (uint32_t)((O) * 2 + (JJ) * 1024);   \
+    if (ISB)                                                        \
+      ob.issue(w_, (JJ), m_);                                       \
     else                                                            \
-      oa.issue(t_ < KT ? t_ : t_ - KT, (JJ), MT_DST(j_ % SLOTS, JJ)); \
+      oa.issue(w_, (JJ), m_);                                       \
   }
 #define MT_RA(SA, KS, I) fa.read((SA), (KS), (I), (I) * 32)
 #define MT_RB(SB, KS, I) fb.read((SB), (KS), (I), block_col<F, GU>(0, I))
   bf16x8_t xa[F], xb[F], ya[F], yb[F];
   // one 16-wide k sub-step: per block row mi, read part of the next sub-step's
   // fragments (B first), run F MFMAs, issue one DMA instruction
-#define MT_SUB(FA, FB, NA, NB, SA, SB, KS, RD, DO, J, J0)                                                     \
+#define MT_SUB(FA, FB, NA, NB, SA, SB, KS, RD, DO, T, ISB, O, J0)                                             \
   _Pragma("unroll") for (int mi = 0; mi < F; ++mi) {                                                          \
     if (RD) {                                                                                                 \
       if (mi < F / 2) {                                                                                       \
@@ -279,7 +280,7 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
     }                                                                                                         \
     _Pragma("unroll") for (int ni = 0; ni < F; ++ni)                                                          \
       acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(FB[ni], FA[mi], acc[mi][ni], 0, 0, 0);            \
-    if (DO) MT_ISSUE(J, (J0) + mi)                                                                            \
+    if (DO) MT_ISSUE(T, ISB, O, (J0) + mi)                                                                    \
     __builtin_amdgcn_sched_barrier(0);                                                                        \
   }
   for (int j = 0; j < SLOTS && j < nh; ++j) {
@@ -288,7 +289,7 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
     else
       oa.begin(j >> 1);
 #pragma unroll
-    for (int jj = 0; jj < NI; ++jj) MT_ISSUE(j, jj)
+    for (int jj = 0; jj < NI; ++jj) MT_ISSUE(j >> 1, j & 1, j * HALF, jj)
   }
   {
     const int after = min(SLOTS, nh) - 2;  // half-stages that may still be in flight
@@ -311,16 +312,18 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
 #define MT_STEP(KT_, B1, A2, MORE, B2)                                                                        \
   {                                                                                                           \
     const int kt_ = (KT_);                                                                                    \
-    int o0 = ((2 * kt_) % SLOTS) * HALF, o1 = ((2 * kt_ + 1) % SLOTS) * HALF;                                 \
-    int o2 = ((2 * kt_ + 2) % SLOTS) * HALF, o3 = ((2 * kt_ + 3) % SLOTS) * HALF;                             \
-    /* opaque: the fragment addresses of every slot would otherwise be held */                                \
-    asm volatile("" : "+s"(o0), "+s"(o1), "+s"(o2), "+s"(o3));                                                \
+    /* slots of half-stages 2 kt .. 2 kt + 4; opaque: the fragment addresses of                               \
+       every slot would otherwise be held */                                                                  \
+    int o0 = slot;                                                                                            \
+    asm volatile("" : "+s"(o0));                                                                              \
+    const int o1 = next(o0), o2 = next(o1), o3 = next(o2), o4 = next(o3);                                     \
+    slot = o2;                                                                                                \
     const uint16_t* sa = lds + o0;                                                                            \
     const uint16_t* sb = lds + o1;                                                                            \
-    MT_SUB(xa, xb, ya, yb, sa, sb, 1, true, B1, 2 * kt_ + 3, F)                                               \
+    MT_SUB(xa, xb, ya, yb, sa, sb, 1, true, B1, kt_ + 1, true, o3, F)                                         \
     if (A2) oa.begin(kt_ + 2);                                                                                \
-    MT_SUB(ya, yb, xa, xb, sa, sb, 2, true, A2, 2 * kt_ + 4, 0)                                               \
-    MT_SUB(xa, xb, ya, yb, sa, sb, 3, true, A2, 2 * kt_ + 4, F)                                               \
+    MT_SUB(ya, yb, xa, xb, sa, sb, 2, true, A2, kt_ + 2, false, o4, 0)                                        \
+    MT_SUB(xa, xb, ya, yb, sa, sb, 3, true, A2, kt_ + 2, false, o4, F)                                        \
     if (MORE) {                                                                                               \
       /* A_kt+2 is the only half-stage issued after B_kt+1; lgkmcnt(0): this                                  \
          wave's reads of step kt are done before any wave refills its slots */                                \
@@ -334,8 +337,10 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
     const uint16_t* na = lds + o2;                                                                            \
     const uint16_t* nb = lds + o3;                                                                            \
     if (B2) ob.begin(kt_ + 2);                                                                                \
-    MT_SUB(ya, yb, xa, xb, na, nb, 0, MORE, B2, 2 * kt_ + 5, 0)                                               \
+    MT_SUB(ya, yb, xa, xb, na, nb, 0, MORE, B2, kt_ + 2, true, o0, 0)                                         \
   }
+  auto next = [](int o) { return o == (SLOTS - 1) * HALF ? 0 : o + HALF; };
+  int slot = 0;  // element offset of A_kt's slot
   if (KT >= 4) {
     MT_STEP(0, false, false, true, true)
     for (int kt = 1; kt + 2 < KT; ++kt) MT_STEP(kt, true, true, true, true)
@@ -351,7 +356,6 @@ __device__ __forceinline__ void k_loop(uint16_t* lds, OA& oa, OB& ob, int KT, f3
 #undef MT_RA
 #undef MT_RB
 #undef MT_ISSUE
-#undef MT_DST
 }
 
 // Row blocks 2 RD, 2 RD + 1 of every wave (128 rows) from the accumulators into

@@ -310,12 +310,10 @@ __device__ __forceinline__ void dw_part(const GateArgs<T>& p, int b, int B, int&
   n = min(p.Ttok, k0 + ps) - k0;
 }
 
-__global__ __launch_bounds__(mt::THREADS) void gate_dw_kernel(GateArgs<uint16_t> p) {
-  extern __shared__ __align__(16) char smem[];
-  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+__device__ __forceinline__ void dw_tile(const GateArgs<uint16_t>& p, int block, uint16_t* lds) {
   f32x16_t acc[GF][GF];
   int mi, ni, split, k0, n;
-  dw_part(p, blockIdx.x, GB, mi, ni, split, k0, n);
+  dw_part(p, block, GB, mi, ni, split, k0, n);
   mt::ColOp<GF, false> oa, ob;
   oa.init(p.dz + (size_t)k0 * p.Ep, bytes32((size_t)n * p.Ep * 2), p.Ep, n, mi * GB, p.Ep);
   ob.init(p.h + (size_t)k0 * p.d, bytes32((size_t)n * p.d * 2), p.d, n, ni * GB, p.d);
@@ -323,29 +321,30 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dw_kernel(GateArgs<uint16_t>
   mt::drain<GF, false>(lds, acc, [&](int r, int c, const float* v) { put_dw(p, split, mi * GB + r, ni * GB + c, v); });
 }
 
-// dh for 128 tokens and every gridDim.y-th 128-column tile.  Wave (wm, wn): 64
-// tokens, whose dz it keeps as fragments, x 64 columns.  A tile of W (Ep rows
-// x 128 columns, KB half-stages) is loaded NBUF - 1 tiles ahead.  The wait at
-// its use lets as many later operations be outstanding as one tile has loads:
-// later are at least those, so the tile itself has landed, however many stores
-// lie between.  The two lane halves trade 4-column runs, so that a lane stores
-// 8 adjacent columns of its token.
+// dh for 128 tokens and every parts-th 128-column tile from `part` on.  Wave
+// (wm, wn): 64 tokens, whose dz it keeps as fragments, x 64 columns.  A tile of
+// W (Ep rows x 128 columns, KB half-stages) is loaded NBUF - 1 tiles ahead.
+// With three buffers the wait at a tile's use lets as many later operations be
+// outstanding as one tile has loads: later are at least those, so the tile
+// itself has landed, however many stores lie between.  The two lane halves
+// trade 4-column runs, so that a lane stores 8 adjacent columns of its token.
 template <int KB>
-__global__ __launch_bounds__(mt::THREADS) void gate_dh_kernel(GateArgs<uint16_t> p) {
-  constexpr int NBUF = KB <= 3 ? 3 : 2;
+constexpr int dh_buffers() { return KB == 1 ? 3 : 2; }
+
+template <int KB>
+__device__ __forceinline__ void dh_tiles(const GateArgs<uint16_t>& p, int mi_, int part, int parts, uint16_t* lds) {
+  constexpr int NBUF = dh_buffers<KB>();
   constexpr int HALF = mt::half_elems<GF>(), TILE = KB * HALF, NI = 2 * GF;
-  extern __shared__ __align__(16) char smem[];
-  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
-  const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+  const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fh = lane >> 5;
-  const int m0 = blockIdx.x * GB + wm * 64;
-  const int ntn = (p.d + GB - 1) / GB, n = (ntn - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int m0 = mi_ * GB + wm * 64;
+  const int ntn = (p.d + GB - 1) / GB, n = (ntn - part + parts - 1) / parts;
   const uint32_t bytes = bytes32((size_t)p.E * p.d * 2);
   // the tiles in turn, each workgroup from another one on (the same columns of
   // rows 4 KiB apart lie on one memory channel)
-  auto col = [&](int i) { return ((int)blockIdx.y + (i + (int)blockIdx.x) % n * (int)gridDim.y) * GB; };
+  auto col = [&](int i) { return (part + (i + mi_) % n * parts) * GB; };
   auto issue = [&](int i) {
     mt::ColOp<GF, false> ob;
     ob.init(p.w, bytes, p.d, p.E, col(i), p.d);
@@ -420,6 +419,20 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dh_kernel(GateArgs<uint16_t>
   }
 }
 
+// dW and dh in one launch, their workgroups spread evenly over it: one reads h,
+// the other writes dh.
+template <int KB>
+__global__ __launch_bounds__(mt::THREADS) void gate_grads_kernel(GateArgs<uint16_t> p, int parts) {
+  extern __shared__ __align__(16) char smem[];
+  uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
+  const long long b = blockIdx.x, total = gridDim.x;
+  const int before = (int)(b * p.nh / total);  // dh workgroups before this one
+  if ((b + 1) * p.nh / total > before)
+    dh_tiles<KB>(p, before / parts, before % parts, parts, lds);
+  else
+    dw_tile(p, (int)b - before, lds);
+}
+
 __global__ __launch_bounds__(mt::S_THREADS) void gate_grads_f32_kernel(GateArgs<float> p) {
   __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   f32x16_t acc;
@@ -489,7 +502,7 @@ GateLayout gate_layout(int T, int d, int E, int dtype) {
   // they run beside nothing else, so two)
   const int B = dtype == MOELB_BF16 ? GB : 64;
   const int tiles = ((d + B - 1) / B) * ((E + B - 1) / B);
-  const int want = 512 / tiles, most = T / 256;
+  const int want = 256 / tiles, most = T / 256;
   l.splits = want < most ? want : most;
   l.splits = l.splits < 1 ? 1 : l.splits > 64 ? 64 : l.splits;
   l.z = 0;
@@ -521,13 +534,18 @@ int launch_softmax(const GateArgs<T>& p, hipStream_t s) {
 }
 
 template <int KB>
-int launch_dh(const GateArgs<uint16_t>& p, hipStream_t s) {
-  constexpr size_t lds = (size_t)(KB <= 3 ? 3 : 2) * KB * mt::half_elems<GF>() * sizeof(uint16_t);
-  if (!moelb_allow_lds(gate_dh_kernel<KB>, lds)) return MOELB_ELAUNCH;
+int launch_grads(GateArgs<uint16_t> p, hipStream_t s) {
+  constexpr size_t dh = (size_t)dh_buffers<KB>() * KB * mt::half_elems<GF>() * sizeof(uint16_t);
+  constexpr size_t lds = dh > mt::lds_bytes<GF>() ? dh : mt::lds_bytes<GF>();
+  if (!moelb_allow_lds(gate_grads_kernel<KB>, lds)) return MOELB_ELAUNCH;
   const int m = (p.Ttok + GB - 1) / GB, ntn = (p.d + GB - 1) / GB;
-  int parts = (512 + m - 1) / m;  // about two workgroups a compute unit where there are few tokens
-  if (m >= 256) parts = 1;
-  hipLaunchKernelGGL((gate_dh_kernel<KB>), dim3(m, parts < ntn ? parts : ntn), dim3(mt::THREADS), lds, s, p);
+  // dh: about a workgroup a compute unit where there are few tokens
+  int parts = m > 0 ? (256 + m - 1) / m : 1;
+  if (parts > ntn) parts = ntn;
+  p.nh = p.dh ? m * parts : 0;
+  const int nw = p.dw ? ((p.E + GB - 1) / GB) * ntn * p.splits : 0;
+  if (p.nh + nw == 0) return MOELB_OK;
+  hipLaunchKernelGGL((gate_grads_kernel<KB>), dim3(p.nh + nw), dim3(mt::THREADS), lds, s, p, parts);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
@@ -548,22 +566,15 @@ int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
     const int st = launch_softmax(p, s);
     if (st != MOELB_OK) return st;
   }
-  if (p.dw) {
-    if (!moelb_allow_lds(gate_dw_kernel, lds)) return MOELB_ELAUNCH;
-    const int tiles = ((p.E + GB - 1) / GB) * ((p.d + GB - 1) / GB);
-    hipLaunchKernelGGL(gate_dw_kernel, dim3(tiles * p.splits), dim3(mt::THREADS), lds, s, p);
-    MOELB_CHECK_LAUNCH();
-  }
-  if (!p.dh || p.Ttok == 0) return MOELB_OK;
   switch (p.Ep / 64) {
     case 1:
-      return launch_dh<1>(p, s);
+      return launch_grads<1>(p, s);
     case 2:
-      return launch_dh<2>(p, s);
+      return launch_grads<2>(p, s);
     case 3:
-      return launch_dh<3>(p, s);
+      return launch_grads<3>(p, s);
     default:
-      return launch_dh<4>(p, s);
+      return launch_grads<4>(p, s);
   }
 }
 

@@ -442,7 +442,7 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
 // bound by its own 64 cycles per instruction, so the 8 waves share the tile's
 // 2 TN / 32 blocks by cutting k between them: with one wave a block a step
 // of one wave's chain was the time of the small calls (tiny training step 88 ->
-// 6x us).  K steps (64 or 128 wide) are loaded one ahead into registers and
+// 64 us).  K steps (64 or 128 wide) are loaded one ahead into registers and
 // written to LDS as [k][m]; partial blocks meet in LDS in a fixed order.
 // a(r, k) / b(r, k) give the address of 4 consecutive floats (along k for a
 // row operand, along r for a column operand) or null for zeros.

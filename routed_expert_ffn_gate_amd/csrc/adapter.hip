@@ -121,7 +121,7 @@ __device__ __forceinline__ int same_id(const AdapterArgs& p, int t0, int rows) {
 // one part of k (blockIdx.y); its waves read the same rows of A_a together.
 // Tokens of one adapter: the tile of mfma_tile.h (half its columns unused up to
 // rank 64; fragments straight from memory, a row a lane, are served 16 bytes a
-// cycle: 30 us against 13 at 8192 tokens, d_in = 4096, r = 64).  Others: a wave
+// cycle: 30 us against 21 at 8192 tokens, d_in = 4096, r = 64).  Others: a wave
 // walks the adapters among its tokens, in token order, with such fragments, and
 // keeps of each product the rows of that adapter's tokens.  Partial sums go to
 // part[split][T][r].

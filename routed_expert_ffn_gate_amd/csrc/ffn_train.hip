@@ -572,9 +572,11 @@ extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, cons
     p.out = static_cast<T*>(y);
     p.rows = rows, p.d = d, p.inter = inter, p.E = E, p.s = sc;
     // 256-row tiles: the down product is moelb_grouped_ffn's, on the same
-    // schedule and activations (it lets a tile's stores run beside the next
-    // tile's loads: 634 -> 5xx us at 131072 rows, d = 2048, inter = 1024)
-    if (BM == 256) {
+    // schedule and activations, where it streams whole K steps: it lets a tile's
+    // stores run beside the next tile's loads (634 -> 520 us at 131072 rows, d =
+    // 2048, inter = 1024).  With a K tail (inter = 1032) its staged form is
+    // the slower one.
+    if (BM == 256 && inter % mt::BK == 0 && inter >= 3 * mt::BK) {
       const int up = launch_rows<T, OP_UP>(p, BM, BN, s);
       if (up != MOELB_OK) return up;
       return moelb_grouped_ffn_stages(MOELB_FFN_DOWN, x, rows_x, rows, group_off, num_groups, E, G, rank, gather,

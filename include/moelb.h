@@ -470,7 +470,7 @@ int moelb_pack_weights(const void* w, int E, int rows, int K, int dtype, void* p
  *  w13        [E,2*inter,d], w2 [E,d,inter]  dtype, row-major
  *  z          [rows,2*inter] fp32: the projections [g, u], kept from the
  *             forward for the backward, in the call's expert-major row order
- *             (group_off, gather, rank, E and rows of both calls the same)
+ *             (x, group_off, gather, rank, E and rows of both calls the same)
  *  y          [rows,d]  dtype out (train); dy [rows,d] dtype (backward): rows
  *             outside every computed group are neither written nor read
  *  dx         [rows,d]  dtype out or NULL: rows outside every computed group
@@ -479,7 +479,8 @@ int moelb_pack_weights(const void* w, int E, int rows, int K, int dtype, void* p
  *             rows
  *  ws         train: moelb_grouped_ffn_workspace_bytes(...) bytes; backward:
  *             moelb_grouped_ffn_backward_workspace_bytes(...) bytes; no state
- *             is kept in it between the calls.
+ *             is kept in it between the calls, and calls that may run at the
+ *             same time need one each.
  * Requires what moelb_grouped_ffn requires, d and inter up to 2^19, and rows*d, rows_x*d,
  * rows*2*inter and 2*inter*d elements each below 2^32 - 2^21 bytes.
  * All row data, weights, z and ws 16-byte aligned.  Outputs must not overlap
@@ -543,7 +544,8 @@ int moelb_combine_backward(const void* dout, const void* y, int rows_y, const in
  * the operand of their products; db is summed from the fp32 dz.  Results do
  * not depend on the order of execution.
  *  h [T,d], w [E,d] dtype; b [E] fp32; idx [T,k] int32; dwts [T,k] fp32
- *  ws   workspace of moelb_gate_backward_workspace_bytes(...) bytes
+ *  ws   workspace of moelb_gate_backward_workspace_bytes(...) bytes; calls that
+ *       may run at the same time need one each
  *  dh   [T,d] dtype out or NULL;  dw [E,d] dtype out or NULL;  db [E] fp32 out
  *       or NULL (T = 0: dw and db are zero)
  * Ids outside [0,E) are left out; an id listed twice counts twice.
@@ -572,7 +574,8 @@ int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, co
  *  a      [n,r,d_in], b [n,d_out,r]  dtype; an adapter of a smaller rank is
  *                          padded with zero rows of a
  *  scale  [n] fp32
- *  ws     workspace of moelb_adapter_projection_workspace_bytes(...) bytes
+ *  ws     workspace of moelb_adapter_projection_workspace_bytes(...) bytes; calls
+ *         that may run at the same time need one each
  *  y      [T,d_out]  (gated: [T,d_out/2])  dtype out
  * ids, a, b and scale may be NULL where n = 0, ws where its size is 0.  Requires d_in % 8 == 0,
  * d_out % 8 == 0 (gated: % 16), n >= 0, r % 8 == 0 and 8 <= r <= 256

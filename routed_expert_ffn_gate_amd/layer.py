@@ -225,6 +225,7 @@ class MoELayer:
             self.n_swaps_next = torch.empty((1,), **i32)
             self.home_base = None
         self._train = None      # buffers of the training form, made at its first step
+        self._kept = False      # the layer's buffers are those of a training step
         self._adapter_ws = None
         self.ws_shared = None
         if shared_inter > 0:
@@ -236,6 +237,7 @@ class MoELayer:
     def predict_plan(self, h_prev, w_cur, b_cur, home, replica_out, stream=None):
         """Prologue: the previous step's lookahead for this layer (gate of this
         layer on the previous hidden states), its histogram and plan."""
+        self._kept = False  # the gate writes the layer's wts
         M.moelb_gate_topk(h_prev, w_cur, b_cur, None, None, self.idx_next, self.wts, None, None, stream=stream)
         M.moelb_histogram(self.idx_next, self.G, self.counts_next, stream=stream)
         M.moelb_plan(self.counts_next, home, self.L, replica_out, None, stream=stream)
@@ -246,6 +248,7 @@ class MoELayer:
         previous hidden states), its histogram, and the swaps from the base
         placement ``home_base`` (kept as the next layer's starting placement)
         into ``home_out``."""
+        self._kept = False
         M.moelb_gate_topk(h_prev, w_cur, b_cur, None, None, self.idx_next, self.wts, None, None, stream=stream)
         M.moelb_histogram(self.idx_next, self.G, self.counts_next, stream=stream)
         self.home_base = home_base
@@ -381,6 +384,7 @@ class MoELayer:
             raise ValueError("train and shared_adapters take row-major weights")
         if shared_adapters is not None and (train or self.shared is None):
             raise ValueError("shared_adapters need a shared expert, and are not trained")
+        self._kept = train
         ev = events
         s0 = stream if stream is not None else torch.cuda.current_stream()
 
@@ -447,9 +451,9 @@ class MoELayer:
         comes first, then the experts' (dx a row per pair), the router's and
         the shared expert's; the hidden states' gradient is the sum of their
         shares, each rounded to the layer's type once."""
+        if not self._kept:
+            raise RuntimeError("backward needs the layer's last step to be step(..., train=True)")
         b = self._train
-        if b is None:
-            raise RuntimeError("backward without a step(..., train=True)")
         s0 = stream if stream is not None else torch.cuda.current_stream()
         x = h if self.gather_rows else self.x_perm
         M.moelb_combine_backward(dout, self.y, self.pos, self.wts, b["dy"], b["dwts"], stream=s0)
@@ -478,6 +482,7 @@ class MoELayer:
         Outputs are identical to ``step``'s.  Event marks (TWO_STAGE_MARKS):
         ev_base+0..8 on the step's stream, +9..11 on the split stream, +12..13
         on the lookahead stream."""
+        self._kept = False
         ev = events
         s0 = stream if stream is not None else torch.cuda.current_stream()
         GE = self.G * self.E

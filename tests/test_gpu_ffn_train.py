@@ -202,6 +202,42 @@ def test_rows_behind_the_last_group_and_zero_rows(moelb):
     assert not bool(got["dw13"].any()) and not bool(got["dw2"].any())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_many_groups(moelb, dtype):
+    """More groups than the one-launch schedule takes (4096): 1000 groups of each of 5 experts."""
+    gen = torch.Generator().manual_seed(12)
+    counts = (torch.randint(0, 12, (5000,), generator=gen) // 9).tolist()
+    c = make(counts[:5], 72, 40, dtype, seed=12)
+    P = sum(counts)
+    more = make([P], 72, 40, dtype, seed=13)
+    c.update(x=more["x"], dy=more["dy"], P=P,
+             off=torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int32, device="cuda"))
+    got = run(c)
+    torch.cuda.synchronize()
+    off, E = c["off"].tolist(), 5
+    rows = [[r for g in range(e, 5000, E) for r in range(off[g], off[g + 1])] for e in range(E)]
+    # an expert's rows gathered together are one group of it
+    order = torch.tensor(sum(rows, []), device="cuda")
+    d = dict(c, x=c["x"][order], dy=c["dy"][order],
+             off=torch.tensor([0] + list(torch.tensor([len(r) for r in rows]).cumsum(0)), device="cuda"))
+    for n in ("y", "dx"):
+        got[n] = got[n][order]
+    check(c, got, *formulas(d))
+
+
+def test_offsets_out_of_order_stay_inside(moelb):
+    """Offsets that are negative, past the rows or decreasing: every access stays in the buffers (the schedule clamps
+    them), and groups with sound offsets before them keep their rows."""
+    c = make([40, 30, 20], 64, 64, torch.bfloat16, seed=14)
+    good = run(c)
+    c["off"] = torch.tensor([0, 40, 35, 1 << 30], dtype=torch.int32, device="cuda")
+    run(c)
+    c["off"] = torch.tensor([-7, 40, -1, 3], dtype=torch.int32, device="cuda")
+    got = run(c)
+    torch.cuda.synchronize()
+    assert torch.equal(got["y"][3:40], good["y"][3:40])
+
+
 def test_only_what_is_asked(moelb):
     c = make([100, 60], 64, 64, torch.bfloat16, seed=6)
     full = run(c)

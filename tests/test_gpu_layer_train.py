@@ -159,6 +159,17 @@ def test_refusals(moelb):
     L, t = build("bf16", True)
     with pytest.raises(ValueError):
         step(L, t, shared_adapters=make_adapters(L, 2, 8, 8, BF), train=True)
+    # the layer's buffers are another step's by now
+    args = (t["dout"], t["h"], t["wc"], t["bc"], t["w13"], t["w2"], t["s13"], t["s2"])
+    step(L, t, train=True)
+    L.backward(*args)
+    step(L, t)
+    with pytest.raises(RuntimeError):
+        L.backward(*args)
+    step(L, t, train=True)
+    L.predict_plan(t["h_prev"], t["wc"], t["bc"], t["home"], t["replica"])
+    with pytest.raises(RuntimeError):
+        L.backward(*args)
     L, t = build("bf16", True, d=128, inter=64, packed=True)
     with pytest.raises(ValueError):
         step(L, t, train=True)

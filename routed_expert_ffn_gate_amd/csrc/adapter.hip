@@ -19,7 +19,7 @@
 //    Its low products come from a launch of their own, in the storage type (an
 //    operand of the second product, off by half a step of the adapter's small
 //    share of y).
-//  * Few tokens (up to 64): the bytes of W and of the adapters in use bound it,
+//  * Few tokens (up to 256): the bytes of W and of the adapters in use bound it,
 //    so the work is cut for many loads in flight: 64 rows of W x a part of k a
 //    workgroup, v_mfma_f32_16x16x32_bf16 straight from registers, with the low
 //    products' workgroups in the same launch; fp32 partial sums and low products
@@ -233,13 +233,13 @@ struct LongRowOp {
 // adapter of row block mi's lane % 32-th token, -1: none.  brow(ni): row of B
 // for this lane in column block ni.
 template <int F, class Row>
-__device__ __forceinline__ void add_adapters(const AdapterArgs& p, const uint16_t* const (&low)[F],
+__device__ __forceinline__ void add_adapters(const AdapterArgs& p, int split, const uint16_t* const (&low)[F],
                                              const int (&own)[F], Row brow, f32x16_t (&acc)[F][F]) {
   const int kc = ((threadIdx.x & 63) >> 5) * 8;
   int left[F];
 #pragma unroll
   for (int mi = 0; mi < F; ++mi) left[mi] = own[mi];
-  for (;;) {
+  for (int i = 0;; ++i) {  // the i-th adapter is part i % splits'
     int id = -1;
 #pragma unroll
     for (int mi = F - 1; mi >= 0; --mi) {
@@ -254,6 +254,7 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs& p, const uint16_
       mine[mi] = own[mi] == id;
       if (mine[mi]) left[mi] = -1;
     }
+    if (i % p.splits != split) continue;
     for (int k = 0; k < p.r; k += 64) {
       bf16x8_t fa[F][4];
 #pragma unroll
@@ -314,6 +315,8 @@ __device__ __forceinline__ bool tile_of(const AdapterArgs& p, int B, int& mi, in
   return true;
 }
 
+// splits > 1: blockIdx.y takes a part of k, and of the adapters of a tile that
+// has several; fp32 partial sums to part[split][T][d_out].
 template <int F, bool GU>
 __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p) {
   extern __shared__ __align__(16) char smem[];
@@ -321,6 +324,9 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
   constexpr int B = 64 * F;
   int mi, ni;
   if (!tile_of(p, B, mi, ni)) return;
+  const int split = blockIdx.y;
+  const int steps = (p.d_in + mt::BK - 1) / mt::BK, ps = (steps + p.splits - 1) / p.splits;
+  const int k0 = min(p.d_in, split * ps * mt::BK), k1 = min(p.d_in, k0 + ps * mt::BK);
   const int t0 = mi * B, n0 = ni * (GU ? B / 2 : B);
   const int out = GU ? p.d_out / 2 : p.d_out;
   auto trow = [&](int i) { return min(t0 + i, p.Ttok - 1); };
@@ -328,17 +334,20 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
     const int c = n0 + (GU ? i % (B / 2) : i);
     return (c < out ? c : 0) + (GU && i >= B / 2 ? out : 0);
   };
-  // a tile of one adapter takes its ranks as further K steps
+  // a tile of one adapter takes its ranks as further K steps (of the last part)
   const int id = same_id(p, t0, B);
   LongRowOp<F> oa, ob;
-  oa.own.init(p.x, bytes32((size_t)p.Ttok * p.d_in * 2), p.d_in, p.d_in, trow);
-  ob.own.init(p.w, bytes32((size_t)p.d_out * p.d_in * 2), p.d_in, p.d_in, wrow);
+  oa.own.init(static_cast<const uint16_t*>(p.x) + k0, bytes32(((size_t)p.Ttok * p.d_in - k0) * 2), p.d_in, k1 - k0,
+              trow);
+  ob.own.init(static_cast<const uint16_t*>(p.w) + k0, bytes32(((size_t)p.d_out * p.d_in - k0) * 2), p.d_in, k1 - k0,
+              wrow);
   oa.more.init(p.low, bytes32((size_t)p.Ttok * p.r * 2), p.r, p.r, trow);
   ob.more.init(static_cast<const uint16_t*>(p.b) + (size_t)max(id, 0) * p.d_out * p.r,
                bytes32((size_t)p.d_out * p.r * 2), p.r, p.r, wrow);
-  oa.first = ob.first = (p.d_in + mt::BK - 1) / mt::BK;
+  oa.first = ob.first = max(1, (k1 - k0 + mt::BK - 1) / mt::BK);  // an empty part: a step of zeros
   f32x16_t acc[F][F];
-  mt::k_loop<F, GU>(lds, oa, ob, oa.first + (id >= 0 ? (p.r + mt::BK - 1) / mt::BK : 0), acc);
+  const bool more = id >= 0 && split == p.splits - 1;
+  mt::k_loop<F, GU>(lds, oa, ob, oa.first + (more ? (p.r + mt::BK - 1) / mt::BK : 0), acc);
   if (p.n > 0 && id < 0) {
     const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
     const uint16_t* low[F];
@@ -349,16 +358,27 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
       own[mi] = t < p.Ttok ? id_of(p, t) : -1;
       low[mi] = static_cast<const uint16_t*>(p.low) + (size_t)min(t, p.Ttok - 1) * p.r + (lane >> 5) * 8;
     }
-    add_adapters<F>(p, low, own, [&](int ni) { return wrow(mt::block_col<F, GU>(wn, ni) + (lane & 31)); }, acc);
+    add_adapters<F>(p, split, low, own, [&](int ni) { return wrow(mt::block_col<F, GU>(wn, ni) + (lane & 31)); }, acc);
   }
   uint16_t* y = static_cast<uint16_t*>(p.y);
+  float* part = p.part + ((size_t)split * p.Ttok + t0) * p.d_out + n0;
   if constexpr (GU) {
     mt::drain<F, true>(lds, acc, [&](int r, int c, const float* g, const float* u) {
-      if (t0 + r < p.Ttok && n0 + c < out) store_gated(y + (size_t)(t0 + r) * out + n0 + c, g, u);
+      if (t0 + r >= p.Ttok || n0 + c >= out) return;
+      if (p.splits > 1) {
+        mt::store8(part + (size_t)r * p.d_out + c, g);
+        mt::store8(part + (size_t)r * p.d_out + out + c, u);
+      } else {
+        store_gated(y + (size_t)(t0 + r) * out + n0 + c, g, u);
+      }
     });
   } else {
     mt::drain<F, false>(lds, acc, [&](int r, int c, const float* v) {
-      if (t0 + r < p.Ttok && n0 + c < out) mt::store8(y + (size_t)(t0 + r) * out + n0 + c, v);
+      if (t0 + r >= p.Ttok || n0 + c >= out) return;
+      if (p.splits > 1)
+        mt::store8(part + (size_t)r * p.d_out + c, v);
+      else
+        mt::store8(y + (size_t)(t0 + r) * out + n0 + c, v);
     });
   }
 }
@@ -419,7 +439,7 @@ __global__ __launch_bounds__(mt::S_THREADS) void adapter_tile_f32_kernel(Adapter
 
 // ---------------------------------------------------------------- few tokens
 
-// Base part: 64 rows of W x all tokens (16 NB of them) x one part of k.  W and
+// Base part: 64 rows of W x 16 NB tokens x one part of k.  W and
 // x stream memory -> LDS in 64-wide K steps, three ahead (a row's 128 bytes by 8
 // neighbouring lanes: read as fragments, a row a lane, they come at a quarter of
 // the rate), the slots of a row XORed so that 16 rows' fragments lie on
@@ -439,7 +459,9 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
   const uint32_t lds_u32 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x % p.splits, n0 = blockIdx.x / p.splits * 64;
+  // a token block's workgroups of one W block are neighbours: they share its rows in L2
+  const int tb = (p.Ttok + TOK - 1) / TOK;
+  const int split = blockIdx.x / tb % p.splits, n0 = blockIdx.x / tb / p.splits * 64, t0 = blockIdx.x % tb * TOK;
   const int steps = (p.d_in + 63) / 64, per = (steps + p.splits - 1) / p.splits;
   const int s0 = min(steps, split * per), n = min(steps, s0 + per) - s0;
   const mt::i32x4_t ws = mt::descriptor(p.w, bytes32((size_t)p.d_out * p.d_in * 2));
@@ -459,7 +481,7 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
     xblk[j] = NB > 1 ? wave * NX + j : wave & 1;  // NB = 1: waves 2, 3 write what 0, 1 write
     const int r = xblk[j] * 8 + (lane >> 3);
     xck[j] = chunk(r) * 8;
-    xoff[j] = ((uint32_t)min(r, p.Ttok - 1) * (uint32_t)p.d_in + xck[j]) * 2u;
+    xoff[j] = ((uint32_t)min(t0 + r, p.Ttok - 1) * (uint32_t)p.d_in + xck[j]) * 2u;
   }
   auto issue = [&](int i) {
     const uint32_t st = lds_u32 + (uint32_t)((i % FEW_STAGES) * STAGE) * 2u;
@@ -507,7 +529,7 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
   const int c0 = n0 + wave * 16 + fc * 4;
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const int tok = j * 16 + fr;
+    const int tok = t0 + j * 16 + fr;
     if (tok < p.Ttok && c0 < p.d_out)
       *reinterpret_cast<f32x4_t*>(p.part + ((size_t)split * p.Ttok + tok) * p.d_out + c0) = acc[j];
   }
@@ -654,7 +676,9 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
 
 // ---------------------------------------------------------------- host
 
-constexpr int FEW_TOKENS = 64;
+// Few tokens' kernels up to here: 64-token blocks re-read W, from the caches
+// (d = 4096: 200 tokens 33 us against 47 on the tile, 400 tokens 54 against 52).
+constexpr int FEW_TOKENS = 256;
 
 template <int F, bool GU>
 int launch_tile(AdapterArgs p, hipStream_t s) {
@@ -663,7 +687,8 @@ int launch_tile(AdapterArgs p, hipStream_t s) {
   const size_t grid = ((size_t)((p.Ttok + B - 1) / B) * p.ntn + 7) / 8 * 8;
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
   if (!moelb_allow_lds(adapter_tile_kernel<F, GU>, mt::lds_bytes<F>())) return MOELB_ELAUNCH;
-  hipLaunchKernelGGL((adapter_tile_kernel<F, GU>), dim3((unsigned)grid), dim3(mt::THREADS), mt::lds_bytes<F>(), s, p);
+  hipLaunchKernelGGL((adapter_tile_kernel<F, GU>), dim3((unsigned)grid, p.splits), dim3(mt::THREADS), mt::lds_bytes<F>(),
+                     s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
@@ -681,10 +706,19 @@ int launch_f32(AdapterArgs p, hipStream_t s) {
 
 // Parts of k for few tokens: about a workgroup a compute unit, at least 256 wide
 // (twice as many cost more in partial sums than they gain).
-int few_splits(int d_in, int d_out) {
-  const int blocks = (d_out + 63) / 64, want = 256 / blocks, most = d_in / 256;
+int few_splits(int T, int d_in, int d_out) {
+  const int blocks = (d_out + 63) / 64 * ((T + 63) / 64), want = 256 / blocks, most = d_in / 256;
   const int s = want < most ? want : most;
   return s < 1 ? 1 : s > 16 ? 16 : s;
+}
+
+// Parts of k for the 128-row tiles of prompts: two workgroups a compute unit,
+// at least 512 wide.  1: whole sums, no partial ones.
+int tile_splits(int T, int d_in, int d_out) {
+  const size_t tiles = (size_t)((T + 127) / 128) * ((d_out + 127) / 128);
+  const size_t want = 512 / tiles, most = (size_t)d_in / 512;
+  const size_t s = want < most ? want : most;
+  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
 }
 
 // Likewise for the low products of prompts.
@@ -706,13 +740,21 @@ int launch_one(const AdapterArgs& p, hipStream_t s) {
 }
 
 template <bool GU>
+int launch_sum(const AdapterArgs& p, hipStream_t s) {
+  const long long threads = (long long)p.Ttok * (p.d_out / 2);
+  hipLaunchKernelGGL((adapter_few_sum_kernel<GU>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+  MOELB_CHECK_LAUNCH();
+  return MOELB_OK;
+}
+
+template <bool GU>
 int launch_few(AdapterArgs p, hipStream_t s) {
-  const int out = GU ? p.d_out / 2 : p.d_out;
   if (one_launch(p.Ttok, p.n, p.r)) {
     return p.Ttok == 1 ? launch_one<1, GU>(p, s) : p.Ttok == 2 ? launch_one<2, GU>(p, s) : launch_one<4, GU>(p, s);
   }
-  p.splits = few_splits(p.d_in, p.d_out);
-  p.nbase = (p.d_out + 63) / 64 * p.splits;
+  p.splits = few_splits(p.Ttok, p.d_in, p.d_out);
+  const int tok = p.Ttok <= 16 ? 16 : p.Ttok <= 32 ? 32 : 64;
+  p.nbase = (p.d_out + 63) / 64 * p.splits * ((p.Ttok + tok - 1) / tok);
   const dim3 grid(p.nbase + (p.n > 0 ? (p.Ttok * p.r + 3) / 4 : 0));
   if (p.Ttok <= 16)
     hipLaunchKernelGGL(adapter_few_kernel<1>, grid, dim3(256), 0, s, p);
@@ -721,10 +763,7 @@ int launch_few(AdapterArgs p, hipStream_t s) {
   else
     hipLaunchKernelGGL(adapter_few_kernel<4>, grid, dim3(256), 0, s, p);
   MOELB_CHECK_LAUNCH();
-  const long long threads = (long long)p.Ttok * (GU ? out : out / 2);
-  hipLaunchKernelGGL((adapter_few_sum_kernel<GU>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
-  MOELB_CHECK_LAUNCH();
-  return MOELB_OK;
+  return launch_sum<GU>(p, s);
 }
 
 template <bool GU>
@@ -740,7 +779,15 @@ int launch_prompts(AdapterArgs p, hipStream_t s) {
     MOELB_CHECK_LAUNCH();
   }
   const size_t tiles = (size_t)((p.Ttok + 255) / 256) * ((p.d_out + 255) / 256);
-  return tiles >= 192 ? launch_tile<4, GU>(p, s) : launch_tile<2, GU>(p, s);
+  if (tiles >= 192) {
+    p.splits = 1;
+    return launch_tile<4, GU>(p, s);
+  }
+  p.splits = tile_splits(p.Ttok, p.d_in, p.d_out);
+  const int st = launch_tile<2, GU>(p, s);
+  if (st != MOELB_OK || p.splits == 1) return st;
+  p.n = 0;  // the adapters are in the partial sums
+  return launch_sum<GU>(p, s);
 }
 
 }  // namespace
@@ -751,8 +798,12 @@ extern "C" size_t moelb_adapter_projection_workspace_bytes(int T, int d_in, int 
   if (few && one_launch(T, n, r)) return 0;
   // low, and behind it the partial sums of few tokens, or of low itself
   const size_t low = n > 0 ? moelb_align256((size_t)T * r * (few ? 4 : moelb_elem_bytes(dtype))) : 0;
-  if (few) return low + (size_t)few_splits(d_in, d_out) * T * d_out * 4;
-  return low + (dtype == MOELB_BF16 && n > 0 && T > 0 ? (size_t)low_splits(T, d_in) * T * r * 4 : 0);
+  if (few) return low + (size_t)few_splits(T, d_in, d_out) * T * d_out * 4;
+  if (dtype != MOELB_BF16 || T == 0) return low;
+  const size_t lows = n > 0 ? (size_t)low_splits(T, d_in) * T * r * 4 : 0;
+  const int ts = tile_splits(T, d_in, d_out);
+  const size_t sums = ts > 1 ? (size_t)ts * T * d_out * 4 : 0;  // after low's own are added
+  return low + (lows > sums ? lows : sums);
 }
 
 extern "C" int moelb_adapter_projection(const void* x, int T, int d_in, int d_out, int dtype, const void* w,

@@ -79,7 +79,7 @@ SHAPES = [
     (1, 8, 16, 1, 8), (1, 2048, 2048, 8, 16), (4, 264, 272, 3, 16), (3, 1000, 528, 2, 8), (1, 136, 48, 2, 64),
     (2, 520, 80, 5, 32), (1, 264, 272, 3, 72), (5, 4096, 144, 2, 16), (2, 72, 80, 3, 24), (16, 264, 48, 5, 16), (17, 200, 208, 40, 8),
     (33, 1000, 528, 64, 32), (64, 4096, 512, 64, 16), (65, 136, 144, 7, 64), (100, 512, 272, 9, 40),
-    (129, 328, 272, 3, 72), (300, 264, 1040, 50, 256), (700, 520, 1040, 5, 128), (513, 64, 64, 2048, 8),
+    (129, 328, 272, 3, 72), (255, 2056, 272, 9, 16), (257, 1544, 528, 9, 24), (300, 264, 1040, 50, 256), (400, 4096, 656, 12, 16), (700, 520, 1040, 5, 128), (513, 64, 64, 2048, 8),
 ]
 
 

@@ -778,8 +778,8 @@ int launch_prompts(AdapterArgs p, hipStream_t s) {
     hipLaunchKernelGGL(adapter_low_sum_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
     MOELB_CHECK_LAUNCH();
   }
-  const size_t tiles = (size_t)((p.Ttok + 255) / 256) * ((p.d_out + 255) / 256);
-  if (tiles >= 192) {
+  if (mt::large_tiles((size_t)((p.Ttok + 255) / 256) * ((p.d_out + 255) / 256),
+                      (size_t)((p.Ttok + 127) / 128) * ((p.d_out + 127) / 128))) {
     p.splits = 1;
     return launch_tile<4, GU>(p, s);
   }

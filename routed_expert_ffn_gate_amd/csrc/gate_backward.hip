@@ -79,8 +79,27 @@ __device__ __forceinline__ float row_reduce(float v, Op op) {
 // v) reads NC of them; 16 lanes take a row, NC experts a lane, the workgroup
 // THREADS / 16 rows at a time.  db partials to row blockIdx.x of pdb.  The
 // caller has synchronised; `part` (THREADS NC floats) may be the logits' LDS.
+// Picks: a lane's ids and gradients of all its rows, asked for before the logits
+// are formed.
+template <int N>
+struct Picks {
+  int id[N];
+  float g[N];
+};
+template <typename T, int ROWS, int THREADS>
+__device__ __forceinline__ void load_picks(const GateArgs<T>& p, int m0, Picks<ROWS * 16 / THREADS>& k) {
+  const int s = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < ROWS * 16 / THREADS; ++i) {
+    const int t = m0 + i * (THREADS / 16) + (threadIdx.x >> 4);
+    const bool on = t < p.Ttok && s < p.k;
+    k.id[i] = on ? p.idx[(size_t)t * p.k + s] : -1;
+    k.g[i] = on ? p.dwts[(size_t)t * p.k + s] : 0.f;
+  }
+}
 template <typename T, int NC, int ROWS, int THREADS, class Get>
-__device__ __forceinline__ void softmax_rows(const GateArgs<T>& p, int m0, float* part, Get get) {
+__device__ __forceinline__ void softmax_rows(const GateArgs<T>& p, int m0, const Picks<ROWS * 16 / THREADS>& picks,
+                                             float* part, Get get) {
   const int tid = threadIdx.x, lane = tid & 63, s = tid & 15, c = s * NC;
   auto add = [](float a, float b) { return a + b; };
   float bias[NC], db[NC];
@@ -89,11 +108,12 @@ __device__ __forceinline__ void softmax_rows(const GateArgs<T>& p, int m0, float
     bias[i] = c + i < p.E ? p.b[c + i] : 0.f;
     db[i] = 0.f;
   }
-  for (int pass = 0; pass < ROWS / (THREADS / 16); ++pass) {
+#pragma unroll
+  for (int pass = 0; pass < ROWS * 16 / THREADS; ++pass) {
     const int r = pass * (THREADS / 16) + (tid >> 4), t = m0 + r;
     const bool on = t < p.Ttok;
-    const int id = on && s < p.k ? p.idx[(size_t)t * p.k + s] : -1;
-    const float g = on && s < p.k ? p.dwts[(size_t)t * p.k + s] : 0.f;
+    const int id = picks.id[pass];
+    const float g = picks.g[pass];
     float z[NC], q[NC];
     float m = -INFINITY, sum = 0.f, pq = 0.f;
     get(r, c, z);
@@ -153,6 +173,8 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
   const int m0 = blockIdx.x * GB;
+  Picks<GB * 16 / mt::THREADS> picks;
+  load_picks<uint16_t, GB, mt::THREADS>(p, m0, picks);
   {
     mt::RowOp<GF> oa, ob;
     oa.init(p.h, bytes32((size_t)p.Ttok * p.d * 2), p.d, p.d, [&](int r) { return min(m0 + r, p.Ttok - 1); });
@@ -164,7 +186,7 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
   }
   __syncthreads();
   float* st = reinterpret_cast<float*>(smem);
-  softmax_rows<uint16_t, 8, GB, mt::THREADS>(p, m0, st, [&](int r, int c, float* z) {
+  softmax_rows<uint16_t, 8, GB, mt::THREADS>(p, m0, picks, st, [&](int r, int c, float* z) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const f32x4_t x = *reinterpret_cast<const f32x4_t*>(st + r * GB + ((c / 4 + h) ^ (r & 15)) * 4);
@@ -178,13 +200,15 @@ __global__ __launch_bounds__(mt::THREADS) void gate_dz_kernel(GateArgs<uint16_t>
 __global__ __launch_bounds__(mt::S_THREADS) void gate_dz_f32_kernel(GateArgs<float> p) {
   __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   const int m0 = blockIdx.x * 64;
+  Picks<64 * 16 / mt::S_THREADS> picks;
+  load_picks<float, 64, mt::S_THREADS>(p, m0, picks);
   f32x16_t acc;
   auto pa = [&](int r, int k) { return m0 + r < p.Ttok ? p.h + (size_t)(m0 + r) * p.d + k : nullptr; };
   auto pb = [&](int r, int k) { return r < p.E ? p.w + (size_t)r * p.d + k : nullptr; };
   mt::k_loop_f32<64, false, false>(lds, pa, pb, p.d, acc);
   mt::stage_f32<64>(lds, acc);
   __syncthreads();
-  softmax_rows<float, 4, 64, mt::S_THREADS>(p, m0, lds, [&](int r, int c, float* z) {
+  softmax_rows<float, 4, 64, mt::S_THREADS>(p, m0, picks, lds, [&](int r, int c, float* z) {
     const f32x4_t x = mt::staged_f32<64>(lds, r, c / 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] = x[i];
@@ -464,6 +488,7 @@ __global__ __launch_bounds__(256) void gate_sums_kernel(GateArgs<T> p, int nw) {
     if (i >= n8) return;
     float v[8];
     mt::load8(p.pdw + i * 8, v);
+#pragma unroll 8
     for (int s = 1; s < p.splits; ++s) {
       float u[8];
       mt::load8(p.pdw + ((size_t)s * n8 + i) * 8, u);
@@ -492,11 +517,11 @@ GateLayout gate_layout(int T, int d, int E, int dtype) {
   GateLayout l;
   const size_t eb = moelb_elem_bytes(dtype);
   l.Ep = (E + 63) & ~63;
-  // db partials: one a tile (bf16: 128 tokens, E <= 128; fp32: 64, 64), else 16 tokens a
-  // workgroup, at most 1024 of them
+  // db partials: one a tile (bf16: 128 tokens, E <= 128; fp32: 64, 64), else a token a
+  // wave, at most 1024 workgroups
   const int tok = dtype == MOELB_BF16 ? GB : 64;
   l.fused = l.Ep <= tok;
-  l.blocks = l.fused ? (T + tok - 1) / tok : (T + 15) / 16;
+  l.blocks = l.fused ? (T + tok - 1) / tok : (T + 3) / 4;
   l.blocks = l.blocks < 1 ? 1 : !l.fused && l.blocks > 1024 ? 1024 : l.blocks;
   // dW: parts of at least 256 tokens, about a workgroup a compute unit (twice as
   // many: 245 against 212 us at T = 32768, d = 4096, E = 128)
@@ -504,7 +529,7 @@ GateLayout gate_layout(int T, int d, int E, int dtype) {
   const int tiles = ((d + B - 1) / B) * ((E + B - 1) / B);
   const int want = 256 / tiles, most = T / 256;
   l.splits = want < most ? want : most;
-  l.splits = l.splits < 1 ? 1 : l.splits > 64 ? 64 : l.splits;
+  l.splits = l.splits < 1 ? 1 : l.splits > 16 ? 16 : l.splits;
   l.z = 0;
   l.dz = moelb_align256((size_t)T * l.Ep * 4);
   l.pdb = l.dz + moelb_align256((size_t)T * l.Ep * eb);

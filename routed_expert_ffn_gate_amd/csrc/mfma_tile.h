@@ -442,7 +442,7 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
 // bound by its own 64 cycles per instruction, so the 8 waves share the tile's
 // 2 TN / 32 blocks by cutting k between them: with one wave a block a step
 // of one wave's chain was the time of the small calls (tiny training step 88 ->
-// 64 us).  K steps (64 or 128 wide) are loaded one ahead into registers and
+// 64 us).  K steps (64 or 128 wide) are loaded two ahead into registers and
 // written to LDS as [k][m]; partial blocks meet in LDS in a fixed order.
 // a(r, k) / b(r, k) give the address of 4 consecutive floats (along k for a
 // row operand, along r for a column operand) or null for zeros.
@@ -500,23 +500,30 @@ __device__ __forceinline__ void k_loop_f32(float* lds, PA pa, PB pb, int K, f32x
   const std::integral_constant<int, TN> rb;
   const std::integral_constant<bool, CA> ca;
   const std::integral_constant<bool, CB> cb;
-  float4 va[64 * BK / 4 / S_THREADS], vb[TN * BK / 4 / S_THREADS];
-  fetch(pa, ra, ca, 0, va);
-  fetch(pb, rb, cb, 0, vb);
+  float4 va[2][64 * BK / 4 / S_THREADS], vb[2][TN * BK / 4 / S_THREADS];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    fetch(pa, ra, ca, s * BK, va[s]);
+    fetch(pb, rb, cb, s * BK, vb[s]);
+  }
   const float* ar = As + (kg * 32 + (lane >> 5)) * (CA ? 68 : 65) + wm * 32 + (lane & 31);
   const float* br = Bs + (kg * 32 + (lane >> 5)) * (TN + (CB ? 4 : 1)) + wn * 32 + (lane & 31);
-  for (int k0 = 0; k0 < K; k0 += BK) {
-    __syncthreads();
-    put(As, ra, ca, va);
-    put(Bs, rb, cb, vb);
-    __syncthreads();
-    if (k0 + BK < K) {
-      fetch(pa, ra, ca, k0 + BK, va);
-      fetch(pb, rb, cb, k0 + BK, vb);
-    }
+  for (int k0 = 0; k0 < K; k0 += 2 * BK) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(br[k * (TN + (CB ? 4 : 1))], ar[k * (CA ? 68 : 65)], acc, 0, 0, 0);
+    for (int s = 0; s < 2; ++s) {
+      if (k0 + s * BK >= K) break;
+      __syncthreads();
+      put(As, ra, ca, va[s]);
+      put(Bs, rb, cb, vb[s]);
+      __syncthreads();
+      if (k0 + (s + 2) * BK < K) {
+        fetch(pa, ra, ca, k0 + (s + 2) * BK, va[s]);
+        fetch(pb, rb, cb, k0 + (s + 2) * BK, vb[s]);
+      }
+#pragma unroll
+      for (int k = 0; k < 32; k += 2)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(br[k * (TN + (CB ? 4 : 1))], ar[k * (CA ? 68 : 65)], acc, 0, 0, 0);
+    }
   }
 }
 

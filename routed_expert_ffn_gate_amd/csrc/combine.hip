@@ -119,7 +119,8 @@ int launch(const void* y, int rows_y, const int32_t* pos, const float* wts, int 
 // of dout per thread, and for it reads the k rows of y, adds to the k dot
 // products (fp32) and writes the k rows of dy.  The products meet by lane
 // shuffles and once in LDS, in a fixed order.  y and dy pass non-temporally:
-// both are far larger than the caches and used once here.
+// both are far larger than the caches and used once here.  Bound by HBM: T =
+// 32768, k = 8, d = 4096, bf16: 851 us, 5.4 TB/s of y, dy and dout.
 template <typename T, int KMAX>
 __global__ __launch_bounds__(CMB_THREADS) void combine_backward_kernel(const T* __restrict__ dout,
                                                                        const T* __restrict__ y, int rows_y,

@@ -19,6 +19,11 @@
 //      tiles of W (read as columns) past them, storing as it goes; the bytes of
 //      dh bound it
 //   5. the parts of dW and db, added in order
+//
+// What bounds it: reading h twice (for z and for dW) and writing dh.  T = 32768,
+// d = 4096, E = 128, bf16: step 1 and 2 in 77 us (3.5 TB/s of h), 3 and 4 in one
+// launch of 135 us, 5 in 6 us.  Small calls: three launches (T = 256, d = 256,
+// E = 16, fp32: 10, 8 and 2 us).
 #include "mfma_tile.h"
 
 namespace {

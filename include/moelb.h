@@ -579,8 +579,8 @@ int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, co
  *  y      [T,d_out]  (gated: [T,d_out/2])  dtype out
  * ids, a, b and scale may be NULL where n = 0, ws where its size is 0.  Requires d_in % 8 == 0,
  * d_out % 8 == 0 (gated: % 16), n >= 0, r % 8 == 0 and 8 <= r <= 256
- * (n > 0), and T*d_in, d_out*d_in, n*d_out*r and T*r elements each below 2^32 -
- * 2^21 bytes; x, w, a, b, ws and y 16-byte aligned.  y must not overlap the
+ * (n > 0), and T*d_in, d_out*d_in, r*d_in, n*d_out*r and T*r elements each below
+ * 2^32 - 2^21 bytes; x, w, a, b, ws and y 16-byte aligned.  y must not overlap the
  * inputs.
  */
 size_t moelb_adapter_projection_workspace_bytes(int T, int d_in, int d_out, int n, int r, int dtype);

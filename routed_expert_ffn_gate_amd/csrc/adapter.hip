@@ -824,7 +824,7 @@ extern "C" int moelb_adapter_projection(const void* x, int T, int d_in, int d_ou
     return MOELB_EINVAL;
   const size_t eb = moelb_elem_bytes(dtype), most = mt::MAX_BYTES;
   if ((size_t)T * d_in * eb >= most || (size_t)d_out * d_in * eb >= most ||
-      (n > 0 && ((size_t)n * d_out * r * eb >= most || (size_t)T * r * eb >= most)))
+      (n > 0 && ((size_t)n * d_out * r * eb >= most || (size_t)T * r * eb >= most || (size_t)r * d_in * eb >= most)))
     return MOELB_EINVAL;
   const size_t need = moelb_adapter_projection_workspace_bytes(T, d_in, d_out, n, r, dtype);
   if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < need)) return MOELB_EWORKSPACE;

@@ -102,6 +102,14 @@ def test_adapter_refuses(lib):
     assert lib.moelb_adapter_projection_workspace_bytes(1, 8, 16, 2, 8, 1) == 0
 
 
+def test_adapter_refuses_an_adapter_past_the_descriptor(lib):
+    """r * d_in of 8 GiB: one adapter's A is addressed with 32-bit byte offsets.  T = 0: nothing is launched."""
+    def call(di, r):
+        return lib.moelb_adapter_projection(P, 0, di, 8, 1, P, P, P, P, P, 1, r, 0, P, 1 << 30, P, N)
+    assert call(1 << 24, 256) == EINVAL
+    assert call(1 << 24, 64) == OK
+
+
 def test_binding_refuses():
     """Shapes, types and devices are the binding's to check: the library sees pointers."""
     from routed_expert_ffn_gate_amd import moelb as M

@@ -384,7 +384,7 @@ class MoELayer:
             raise ValueError("train and shared_adapters take row-major weights")
         if shared_adapters is not None and (train or self.shared is None):
             raise ValueError("shared_adapters need a shared expert, and are not trained")
-        self._kept = train
+        self._kept = False  # until the whole step is queued
         ev = events
         s0 = stream if stream is not None else torch.cuda.current_stream()
 
@@ -441,6 +441,7 @@ class MoELayer:
         mark(6)
         s0.wait_event(self.ev_side)
         mark(7)
+        self._kept = train
         return self._out()
 
     def backward(self, dout, h, w_cur, b_cur, w13, w2, shared_w13=None, shared_w2=None, stream=None) -> Gradients:
@@ -450,7 +451,9 @@ class MoELayer:
         its expert's output wherever it is computed.  The combine's gradient
         comes first, then the experts' (dx a row per pair), the router's and
         the shared expert's; the hidden states' gradient is the sum of their
-        shares, each rounded to the layer's type once."""
+        shares, each rounded to the layer's type once.  A step replayed from a
+        captured graph writes the layer's buffers unseen: its backward belongs
+        into the same graph."""
         if not self._kept:
             raise RuntimeError("backward needs the layer's last step to be step(..., train=True)")
         b = self._train

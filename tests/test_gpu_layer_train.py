@@ -175,6 +175,19 @@ def test_refusals(moelb):
         step(L, t, train=True)
 
 
+def test_a_step_that_fails_keeps_nothing(moelb):
+    L, t = build("bf16", True)
+    args = (t["dout"], t["h"], t["wc"], t["bc"], t["w13"], t["w2"], t["s13"], t["s2"])
+    step(L, t, train=True)
+    L.backward(*args)
+    with pytest.raises(moelb.MoelbError):  # after the gate wrote this step's picks
+        step(L, dict(t, w13=t["w13"][:, 1:]), train=True)
+    with pytest.raises(RuntimeError):
+        L.backward(*args)
+    step(L, t, train=True)
+    L.backward(*args)
+
+
 def test_full_shape_step(moelb):
     """Qwen3-30B's decode shape (T = 512, d = 2048, E = 128, k = 8, inter = 768) as one training step: random
     routing, every gradient finite and the router's bias gradient summing to zero (a softmax has no gradient along

@@ -226,7 +226,8 @@ class MoELayer:
             self.home_base = None
         self._train = None      # buffers of the training form, made at its first step
         self._kept = False      # the layer's buffers are those of a training step
-        self._adapter_ws = None
+        self._adapter_ws = []   # the last one in use; a captured graph may hold an earlier one
+        self._adapter_mid = None
         self.ws_shared = None
         if shared_inter > 0:
             self.ws_shared = torch.empty((M.moelb_grouped_ffn_workspace_bytes(T, 1, 1, d, shared_inter, code),),
@@ -353,10 +354,11 @@ class MoELayer:
         n, r13, r2 = ad.a13.shape[0], ad.a13.shape[1], ad.a2.shape[1]
         need = max(M.moelb_adapter_projection_workspace_bytes(T, d, 2 * si, n, r13, code),
                    M.moelb_adapter_projection_workspace_bytes(T, si, d, n, r2, code))
-        if self._adapter_ws is None or self._adapter_ws[0].numel() < need:
-            self._adapter_ws = (torch.empty((max(1, need),), dtype=torch.uint8, device=self.dev),
-                                torch.empty((T, si), dtype=self.tdtype, device=self.dev))
-        ws, mid = self._adapter_ws
+        if not self._adapter_ws or self._adapter_ws[-1].numel() < need:
+            self._adapter_ws.append(torch.empty((max(1, need),), dtype=torch.uint8, device=self.dev))
+        if self._adapter_mid is None:
+            self._adapter_mid = torch.empty((T, si), dtype=self.tdtype, device=self.dev)
+        ws, mid = self._adapter_ws[-1], self._adapter_mid
         M.moelb_adapter_projection(h, shared_w13.reshape(2 * si, d), ad.ids, ad.a13, ad.b13, ad.scale13, ws, mid,
                                    gated=True, stream=stream)
         M.moelb_adapter_projection(mid, shared_w2.reshape(d, si), ad.ids, ad.a2, ad.b2, ad.scale2, ws, self.shared,

@@ -188,6 +188,26 @@ def test_a_step_that_fails_keeps_nothing(moelb):
     L.backward(*args)
 
 
+def test_captured_adapters_keep_their_workspace(moelb):
+    """A larger rank makes a larger workspace; the one a captured graph writes to stays the layer's."""
+    L, t = build("bf16", True)
+    small, large = make_adapters(L, 3, 8, 8, BF), make_adapters(L, 3, 256, 256, BF)
+    want = step(L, t, shared_adapters=small).out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(L, t, shared_adapters=small)
+    held = L._adapter_ws[-1].numel()
+    large_out = step(L, t, shared_adapters=large).out.clone()
+    assert L._adapter_ws[-1].numel() > held
+    canaries = [torch.full((held,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(L.out, want)
+        assert all(bool((c == 7).all()) for c in canaries)
+        assert torch.equal(step(L, t, shared_adapters=large).out, large_out)
+
+
 def test_full_shape_step(moelb):
     """Qwen3-30B's decode shape (T = 512, d = 2048, E = 128, k = 8, inter = 768) as one training step: random
     routing, every gradient finite and the router's bias gradient summing to zero (a softmax has no gradient along

@@ -279,10 +279,22 @@ class MoELayer:
         self.sched_cur, self.sched_next = self.sched_next, self.sched_cur
         return self.replica_spare
 
+    def _may_make(self, what):
+        """Buffers made by a step are made outside of a capture: their constants
+        are written once, not at every replay."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"{what}: run one such step before capturing one, it makes its buffers")
+
+    def _ready(self):
+        """New buffers (memory of the current stream, constants written on it)
+        may be used on any stream from here on."""
+        torch.cuda.current_stream().synchronize()
+
     def _train_buffers(self):
         """What the training form keeps between step and backward, and the
         gradients."""
         if self._train is None:
+            self._may_make("train")
             T, P, d, E, i, si = self.T, self.P, self.d, self.E, self.inter, self.shared_inter
             code = M.MOELB_BF16 if self.dtype == "bf16" else M.MOELB_F32
             t = dict(dtype=self.tdtype, device=self.dev)
@@ -303,6 +315,7 @@ class MoELayer:
                          ws_shared=bytes_(M.moelb_grouped_ffn_backward_workspace_bytes(T, 1, 1, d, si, code)),
                          own_row=torch.arange(T, dtype=torch.int32, device=self.dev), one=torch.ones((T, 1), **f))
             self._train = b
+            self._ready()
         return self._train
 
     def _gather(self):
@@ -350,19 +363,25 @@ class MoELayer:
         """The shared expert as two projections with each token's adapters
         beside them: gate and up gated into the activations, then down."""
         T, d, si = self.T, self.d, self.shared_inter
-        code = M.dtype_code(h)
-        n, r13, r2 = ad.a13.shape[0], ad.a13.shape[1], ad.a2.shape[1]
-        need = max(M.moelb_adapter_projection_workspace_bytes(T, d, 2 * si, n, r13, code),
-                   M.moelb_adapter_projection_workspace_bytes(T, si, d, n, r2, code))
-        if not self._adapter_ws or self._adapter_ws[-1].numel() < need:
-            self._adapter_ws.append(torch.empty((max(1, need),), dtype=torch.uint8, device=self.dev))
-        if self._adapter_mid is None:
-            self._adapter_mid = torch.empty((T, si), dtype=self.tdtype, device=self.dev)
-        ws, mid = self._adapter_ws[-1], self._adapter_mid
+        ws, mid = self._adapter_buffers(ad, M.dtype_code(h))
         M.moelb_adapter_projection(h, shared_w13.reshape(2 * si, d), ad.ids, ad.a13, ad.b13, ad.scale13, ws, mid,
                                    gated=True, stream=stream)
         M.moelb_adapter_projection(mid, shared_w2.reshape(d, si), ad.ids, ad.a2, ad.b2, ad.scale2, ws, self.shared,
                                    stream=stream)
+
+    def _adapter_buffers(self, ad: SharedAdapters, code):
+        """(workspace, activations) of a step with these adapters."""
+        T, d, si = self.T, self.d, self.shared_inter
+        n, r13, r2 = ad.a13.shape[0], ad.a13.shape[1], ad.a2.shape[1]
+        need = max(M.moelb_adapter_projection_workspace_bytes(T, d, 2 * si, n, r13, code),
+                   M.moelb_adapter_projection_workspace_bytes(T, si, d, n, r2, code))
+        if not self._adapter_ws or self._adapter_ws[-1].numel() < need:
+            self._may_make("shared_adapters")
+            self._adapter_ws.append(torch.empty((max(1, need),), dtype=torch.uint8, device=self.dev))
+            if self._adapter_mid is None:
+                self._adapter_mid = torch.empty((T, si), dtype=self.tdtype, device=self.dev)
+            self._ready()
+        return self._adapter_ws[-1], self._adapter_mid
 
     def _out(self):
         return StepOut(self.idx, self.wts, self.gap, self.idx_next, self.counts, self.counts_next, self.replica_next,
@@ -375,17 +394,23 @@ class MoELayer:
              shared_adapters: Optional[SharedAdapters] = None) -> StepOut:
         """One layer step.  ``train``: keep what ``backward`` needs (row-major
         weights only).  ``shared_adapters``: the shared expert with each
-        token's low-rank adapters (row-major weights only; not with
-        ``train``).  With ``events``, marks ev_base+0..7 bracket the
-        stages of STAGES on the step's stream, ev_base+8..11 bracket the
-        grouped FFN's three stages (schedule, gate/up GEMM, down GEMM, each
-        launched on its own), ev_base+12..13 bracket the side stream's work.
-        ``sched``: the split's round schedule for ``replica_cur`` (default: the
-        one ``predict_plan`` or ``advance`` left in force)."""
+        token's low-rank adapters (row-major weights only; not with ``train``).
+        The first step of either kind, and one with adapters of more rank than
+        before, makes buffers: not under graph capture. With ``events``, marks
+        ev_base+0..7 bracket the stages of STAGES on the step's stream,
+        ev_base+8..11 bracket the grouped FFN's three stages (schedule, gate/up
+        GEMM, down GEMM, each launched on its own), ev_base+12..13 bracket the
+        side stream's work. ``sched``: the split's round schedule for
+        ``replica_cur`` (default: the one ``predict_plan`` or ``advance`` left
+        in force)."""
         if self.ffn_opt and (train or shared_adapters is not None):
             raise ValueError("train and shared_adapters take row-major weights")
         if shared_adapters is not None and (train or self.shared is None):
             raise ValueError("shared_adapters need a shared expert, and are not trained")
+        if train:
+            self._train_buffers()
+        if shared_adapters is not None:
+            self._adapter_buffers(shared_adapters, M.dtype_code(h))
         self._kept = False  # until the whole step is queued
         ev = events
         s0 = stream if stream is not None else torch.cuda.current_stream()

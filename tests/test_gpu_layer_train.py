@@ -182,6 +182,7 @@ def test_a_step_that_fails_keeps_nothing(moelb):
     L.backward(*args)
     with pytest.raises(moelb.MoelbError):  # after the gate wrote this step's picks
         step(L, dict(t, w13=t["w13"][:, 1:]), train=True)
+    torch.cuda.synchronize()
     with pytest.raises(RuntimeError):
         L.backward(*args)
     step(L, t, train=True)
@@ -206,6 +207,56 @@ def test_captured_adapters_keep_their_workspace(moelb):
         assert torch.equal(L.out, want)
         assert all(bool((c == 7).all()) for c in canaries)
         assert torch.equal(step(L, t, shared_adapters=large).out, large_out)
+
+
+def test_first_steps_buffers(moelb):
+    """The buffers that the first step of a kind makes: refused under capture (nothing is queued), and usable at once
+    on a stream that does not wait for the one they were made on."""
+    L, t = build("bf16", True)
+    ad = make_adapters(L, 3, 8, 8, BF)
+    args = (t["dout"], t["h"], t["wc"], t["bc"], t["w13"], t["w2"], t["s13"], t["s2"])
+    torch.cuda.synchronize()
+    for kw in (dict(train=True), dict(shared_adapters=ad)):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            with pytest.raises(RuntimeError, match="before capturing"):
+                step(L, t, **kw)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device="cuda")
+    for _ in range(4):
+        busy = busy @ busy * 1e-2  # the current stream has work queued
+    step(L, t, train=True, stream=st)
+    got = L.backward(*args, stream=st)
+    st.synchronize()
+    first = [getattr(got, n).clone() for n in ("h", "w_cur", "b_cur", "w13", "w2", "shared_w13", "shared_w2")]
+    torch.cuda.synchronize()
+    step(L, t, train=True)
+    again = L.backward(*args)
+    torch.cuda.synchronize()
+    for a, n in zip(first, ("h", "w_cur", "b_cur", "w13", "w2", "shared_w13", "shared_w2")):
+        assert torch.equal(a, getattr(again, n)), n
+
+
+def test_captured_training_step(moelb):
+    """step and backward in one graph, replayed between eager steps of other inputs."""
+    L, t = build("bf16", True)
+    names = ("h", "w_cur", "b_cur", "w13", "w2", "shared_w13", "shared_w2")
+    args = (t["dout"], t["h"], t["wc"], t["bc"], t["w13"], t["w2"], t["s13"], t["s2"])
+    step(L, t, train=True)
+    want = {n: getattr(L.backward(*args), n).clone() for n in names}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(L, t, train=True)
+        got = L.backward(*args)
+    other = dict(t, h=-t["h"], dout=t["dout"] * 2)
+    for _ in range(3):
+        step(L, other, train=True)
+        L.backward(other["dout"], other["h"], *args[2:])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(getattr(got, n), want[n]), n
 
 
 def test_full_shape_step(moelb):

@@ -664,7 +664,9 @@ extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, in
        reinterpret_cast<uintptr_t>(dw)) & 15)
     return MOELB_EINVAL;
   const size_t eb = moelb_elem_bytes(dtype);
-  if ((size_t)T * d * eb >= mt::MAX_BYTES) return MOELB_EINVAL;
+  // h, w and dz are operands of the tile
+  const size_t Ep = ((size_t)E + 63) / 64 * 64, most = mt::MAX_BYTES;
+  if ((size_t)T * d * eb >= most || (size_t)E * d * eb >= most || (size_t)T * Ep * eb >= most) return MOELB_EINVAL;
   const GateLayout l = gate_layout(T, d, E, dtype);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < l.total) return MOELB_EWORKSPACE;
   if (!dh && !dw && !db) return MOELB_OK;

@@ -102,6 +102,15 @@ def test_adapter_refuses(lib):
     assert lib.moelb_adapter_projection_workspace_bytes(1, 8, 16, 2, 8, 1) == 0
 
 
+def test_gate_backward_refuses_operands_past_the_descriptor(lib):
+    """w and dz (E padded to 64) are addressed with 32-bit byte offsets too.  No workspace: nothing is launched."""
+    def call(T, d, E, dt):
+        return lib.moelb_gate_backward(P, T, d, E, 1, dt, P, P, P, P, N, 0, P, P, P, N)
+    assert call(1 << 26, 8, 64, 1) == EINVAL and call(1 << 25, 8, 8, 0) == EINVAL   # dz of 8 GiB
+    assert call(4, 1 << 23, 256, 1) == EINVAL                                       # w of 4 GiB
+    assert call(1 << 24, 8, 64, 1) == EWORKSPACE and call(4, 1 << 22, 256, 1) == EWORKSPACE
+
+
 def test_adapter_refuses_an_adapter_past_the_descriptor(lib):
     """r * d_in of 8 GiB: one adapter's A is addressed with 32-bit byte offsets.  T = 0: nothing is launched."""
     def call(di, r):

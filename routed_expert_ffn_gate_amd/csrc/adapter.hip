@@ -28,6 +28,10 @@
 //  * One to four tokens with few ranks: one launch.  Every workgroup takes 16
 //    rows of W and forms the low products itself (A_a of a token is as small as
 //    its rows of W, and comes from L2).
+// fp32 has the same forms on the fp32 tile: one to four tokens in one launch,
+// few tokens with the adapters in the sum's kernel, else a walk over the tile's
+// adapters; k is cut into parts wherever a call has fewer tiles than the card
+// has compute units.
 //
 // Measured, bf16: one token, 2048 x 2048, r = 16: 5.8 us; 64 requests with an
 // adapter each, 4096 x 4096 gated, r = 16: 11.3 us (4.4 TB/s of W and adapters)
@@ -78,38 +82,45 @@ __device__ __forceinline__ bf16x8_t frag_at(const uint16_t* row, int k, int kc, 
 
 // ---------------------------------------------------------------- low = scale x A^T
 
-// A wave per (token, rank): a dot product over d_in, 8 values a lane and step.
-// `L`: the type low is kept in.
-template <typename T, typename L>
+// low in fp32: a wave per token and R ranks, dot products over d_in, 8 values a
+// lane and step.
+template <typename T, int WAVES, int R>
 __device__ __forceinline__ void low_rows(const AdapterArgs& p, int block) {
-  const long long wv = (long long)block * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  const int t = (int)(wv / p.r), rr = (int)(wv % p.r);
+  const long long wv = (long long)block * WAVES + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, per = p.r / R;
+  const int t = (int)(wv / per), rr = (int)(wv % per) * R;
   if (t >= p.Ttok) return;
   const int id = id_of(p, t);
   if (id < 0) return;
   const T* x = static_cast<const T*>(p.x) + (size_t)t * p.d_in;
   const T* a = static_cast<const T*>(p.a) + ((size_t)id * p.r + rr) * p.d_in;
-  float s0 = 0.f, s1 = 0.f;
-#pragma unroll 8
+  float s[R][2];
+#pragma unroll
+  for (int j = 0; j < R; ++j) s[j][0] = s[j][1] = 0.f;
+#pragma unroll 8 / R
   for (int k = lane * 8; k < p.d_in; k += MOELB_WAVE * 8) {
-    float u[8], v[8];
+    float u[8], w[R][8];
     load_vec(x + k, u);
-    load_vec(a + k, v);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      s0 = fmaf(u[i], v[i], s0);
-      s1 = fmaf(u[i + 1], v[i + 1], s1);
-    }
+    for (int j = 0; j < R; ++j) load_vec(a + (size_t)j * p.d_in + k, w[j]);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i & 1] = fmaf(u[i], w[j][i], s[j][i & 1]);
   }
-  s0 += s1;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s0 += __shfl_xor(s0, o, MOELB_WAVE);
-  if (lane == 0) Elem<L>::store(static_cast<L*>(p.low), (size_t)t * p.r + rr, s0 * p.scale[id]);
+  for (int j = 0; j < R; ++j) {
+    float v = s[j][0] + s[j][1];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, MOELB_WAVE);
+    if (lane == 0) static_cast<float*>(p.low)[(size_t)t * p.r + rr + j] = v * p.scale[id];
+  }
 }
 
+// fp32 prompts.
+template <int R>
 __global__ __launch_bounds__(256) void adapter_low_rows_f32_kernel(AdapterArgs p) {
-  low_rows<float, float>(p, blockIdx.x);
+  low_rows<float, 4, R>(p, blockIdx.x);
 }
 
 // The adapter of all tokens t0 .. t0 + rows - 1 (up to T), -1 if they differ or
@@ -310,11 +321,11 @@ __device__ __forceinline__ void store_gated(float* y, const float* g, const floa
 
 // Tile order: as the grouped FFN's, 8 token tiles x every column tile, dealt in
 // contiguous ranges to the 8 XCDs.
-__device__ __forceinline__ bool tile_of(const AdapterArgs& p, int B, int& mi, int& ni) {
+__device__ __forceinline__ bool tile_of(const AdapterArgs& p, int B, int bid, int& mi, int& ni) {
   const int ntm = (p.Ttok + B - 1) / B, total = ntm * p.ntn;
   const int per = (total + 7) / 8;
-  const int t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || t >= total) return false;
+  const int t = (bid & 7) * per + (bid >> 3);
+  if (bid >> 3 >= per || t >= total) return false;
   const int group = t / (8 * p.ntn), gm = min(8, ntm - group * 8), local = t - group * 8 * p.ntn;
   ni = local / gm;
   mi = group * 8 + local % gm;
@@ -329,7 +340,7 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
   constexpr int B = 64 * F;
   int mi, ni;
-  if (!tile_of(p, B, mi, ni)) return;
+  if (!tile_of(p, B, blockIdx.x, mi, ni)) return;
   const int split = blockIdx.y;
   const int steps = (p.d_in + mt::BK - 1) / mt::BK, ps = (steps + p.splits - 1) / p.splits;
   const int k0 = min(p.d_in, split * ps * mt::BK), k1 = min(p.d_in, k0 + ps * mt::BK);
@@ -389,17 +400,26 @@ __global__ __launch_bounds__(mt::THREADS) void adapter_tile_kernel(AdapterArgs p
   }
 }
 
-// fp32: the same sum on 64 x 64 tiles.
-template <bool GU>
+// fp32: the same sum on 64 x 64 tiles.  FEW (few tokens): blocks from nbase on
+// form the low products and the adapters are left to the sum's kernel.  Parts of
+// k as above.
+template <bool GU, bool FEW>
 __global__ __launch_bounds__(mt::S_THREADS) void adapter_tile_f32_kernel(AdapterArgs p) {
   __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   __shared__ int tok[64];
+  if (FEW && (int)blockIdx.x >= p.nbase) {
+    low_rows<float, mt::S_THREADS / MOELB_WAVE, 1>(p, blockIdx.x - p.nbase);
+    return;
+  }
+  const int tiles = p.nbase / p.splits, split = blockIdx.x / tiles;  // tiles: a multiple of 8
   int mi, ni;
-  if (!tile_of(p, 64, mi, ni)) return;
+  if (!tile_of(p, 64, blockIdx.x - split * tiles, mi, ni)) return;
   const int t0 = mi * 64, n0 = ni * (GU ? 32 : 64);
   const int out = GU ? p.d_out / 2 : p.d_out;
-  const float* x = static_cast<const float*>(p.x);
-  const float* w = static_cast<const float*>(p.w);
+  const int per = ((p.d_in + 63) / 64 + p.splits - 1) / p.splits * 64;
+  const int k0 = min(p.d_in, split * per), k1 = min(p.d_in, k0 + per);
+  const float* x = static_cast<const float*>(p.x) + k0;
+  const float* w = static_cast<const float*>(p.w) + k0;
   const float* low = static_cast<const float*>(p.low);
   auto wrow = [&](int i) {
     const int c = n0 + (GU ? i & 31 : i);
@@ -409,18 +429,20 @@ __global__ __launch_bounds__(mt::S_THREADS) void adapter_tile_f32_kernel(Adapter
   {
     auto pa = [&](int i, int k) { return t0 + i < p.Ttok ? x + (size_t)(t0 + i) * p.d_in + k : nullptr; };
     auto pb = [&](int i, int k) { return wrow(i) >= 0 ? w + (size_t)wrow(i) * p.d_in + k : nullptr; };
-    mt::k_loop_f32<64, false, false>(lds, pa, pb, p.d_in, acc);
+    mt::k_loop_f32<64, false, false>(lds, pa, pb, k1 - k0, acc);
   }
-  if (p.n > 0) {
+  if (!FEW && p.n > 0) {
     // every wave walks the tile's adapters (they load the rows together); a
     // lane whose token has another one keeps its value
     if (threadIdx.x < 64) tok[threadIdx.x] = t0 + (int)threadIdx.x < p.Ttok ? id_of(p, t0 + threadIdx.x) : -1;
     __syncthreads();
     int left = tok[threadIdx.x & 63];
     const int own = tok[(threadIdx.x >> 6 & 1) * 32 + (threadIdx.x & 31)];  // the lane's token
+    int turn = 0;  // the parts take the adapters in turn
     for (uint64_t some = __ballot(left >= 0); some; some = __ballot(left >= 0)) {
       const int id = __builtin_amdgcn_readlane(left, __builtin_ctzll(some));
       if (left == id) left = -1;
+      if (turn++ % p.splits != split) continue;
       const float* b = static_cast<const float*>(p.b) + (size_t)id * p.d_out * p.r;
       auto pa = [&](int i, int k) { return tok[i] == id ? low + (size_t)(t0 + i) * p.r + k : nullptr; };
       auto pb = [&](int i, int k) { return wrow(i) >= 0 ? b + (size_t)wrow(i) * p.r + k : nullptr; };
@@ -430,6 +452,13 @@ __global__ __launch_bounds__(mt::S_THREADS) void adapter_tile_f32_kernel(Adapter
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[q] = own == id ? acc[q] + more[q] : acc[q];
     }
+  }
+  if (FEW || p.splits > 1) {
+    float* part = p.part + (size_t)split * p.Ttok * p.d_out;
+    mt::drain_f32<64, false>(lds, acc, [&](int r, int c, const float* v) {
+      if (t0 + r < p.Ttok && wrow(c) >= 0) mt::store8(part + (size_t)(t0 + r) * p.d_out + wrow(c), v);
+    });
+    return;
   }
   float* y = static_cast<float*>(p.y);
   if constexpr (GU) {
@@ -456,7 +485,7 @@ constexpr int FEW_STAGES = 4;
 template <int NB>
 __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
   if ((int)blockIdx.x >= p.nbase) {
-    low_rows<uint16_t, float>(p, blockIdx.x - p.nbase);
+    low_rows<uint16_t, 4, 1>(p, blockIdx.x - p.nbase);
     return;
   }
   constexpr int TOK = 16 * NB, STAGE = (64 + TOK) * 64;  // elements
@@ -543,7 +572,7 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
 
 // Two rows of W a thread (a gate and its up row, or two neighbours): their
 // partial sums in order, and low . B rows.
-template <bool GU>
+template <typename T, bool GU>
 __global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
   const int out = GU ? p.d_out / 2 : p.d_out, per = GU ? out : out / 2;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -561,7 +590,7 @@ __global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
   }
   if (id >= 0) {
     const float* low = static_cast<const float*>(p.low) + (size_t)t * p.r;
-    const uint16_t* b = static_cast<const uint16_t*>(p.b) + (size_t)id * p.d_out * p.r;
+    const T* b = static_cast<const T*>(p.b) + (size_t)id * p.d_out * p.r;
 #pragma unroll 2
     for (int k = 0; k < p.r; k += 8) {
       float l[8], u[8], w[8];
@@ -575,9 +604,11 @@ __global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
       }
     }
   }
-  uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)t * out;
-  if (GU)
-    y[c] = f32_to_bf16(silu_f32(v0) * v1);
+  T* y = static_cast<T*>(p.y) + (size_t)t * out;
+  if constexpr (GU)
+    Elem<T>::store(y, c, silu_f32(v0) * v1);
+  else if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float2*>(y + 2 * c) = make_float2(v0, v1);
   else
     *reinterpret_cast<uint32_t*>(y + 2 * c) = bf16x2_pack(v0, v1);
 }
@@ -589,7 +620,7 @@ __global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
 // loads of a wave at once.
 constexpr int ONE_TOKENS = 4, ONE_LOW = 64, ONE_WAVES = 16;
 
-template <int NT, bool GU>
+template <typename T, int NT, bool GU>
 __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(AdapterArgs p) {
   __shared__ float base[16][NT];
   __shared__ float low[ONE_LOW];
@@ -601,8 +632,8 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
     const int c = n0 + (GU ? i & 7 : i);
     return (c < out ? c : 0) + (GU && i >= 8 ? out : 0);
   };
-  const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  const uint16_t* w = static_cast<const uint16_t*>(p.w) + (size_t)wrow(wave) * p.d_in;
+  const T* x = static_cast<const T*>(p.x);
+  const T* w = static_cast<const T*>(p.w) + (size_t)wrow(wave) * p.d_in;
   // the output of this thread: token, row (GU: gate row and its up row)
   const int rows = GU ? 8 : 16;
   const int tt = threadIdx.x / rows, tj = threadIdx.x % rows;
@@ -627,7 +658,7 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
   for (int i = wave; i < nlow; i += ONE_WAVES) {
     const int t = i / p.r, id = __builtin_amdgcn_readfirstlane(id_of(p, t));
     if (id < 0) continue;
-    const uint16_t* a = static_cast<const uint16_t*>(p.a) + ((size_t)id * p.r + i % p.r) * p.d_in;
+    const T* a = static_cast<const T*>(p.a) + ((size_t)id * p.r + i % p.r) * p.d_in;
     float v = 0.f;
 #pragma unroll 4
     for (int k = lane * 8; k < p.d_in; k += MOELB_WAVE * 8) {
@@ -648,8 +679,8 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
     if (lane == 0) base[wave][t] = acc[t];
   }
   // the first 16 ranks of this thread's B rows, on their way while the sums meet
-  const uint16_t* b0 = static_cast<const uint16_t*>(p.b) + ((size_t)max(own, 0) * p.d_out + wrow(tj)) * p.r;
-  const uint16_t* b1 = static_cast<const uint16_t*>(p.b) + ((size_t)max(own, 0) * p.d_out + wrow(tj + 8)) * p.r;
+  const T* b0 = static_cast<const T*>(p.b) + ((size_t)max(own, 0) * p.d_out + wrow(tj)) * p.r;
+  const T* b1 = static_cast<const T*>(p.b) + ((size_t)max(own, 0) * p.d_out + wrow(tj + 8)) * p.r;
   float u0[2][8], u1[2][8];
   if (own >= 0) {
 #pragma unroll
@@ -677,7 +708,7 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
     }
   }
   if (GU) v0 = silu_f32(v0) * v1;
-  static_cast<uint16_t*>(p.y)[(size_t)tt * out + n0 + tj] = f32_to_bf16(v0);
+  Elem<T>::store(static_cast<T*>(p.y), (size_t)tt * out + n0 + tj, v0);
 }
 
 // ---------------------------------------------------------------- host
@@ -695,17 +726,6 @@ int launch_tile(AdapterArgs p, hipStream_t s) {
   if (!moelb_allow_lds(adapter_tile_kernel<F, GU>, mt::lds_bytes<F>())) return MOELB_ELAUNCH;
   hipLaunchKernelGGL((adapter_tile_kernel<F, GU>), dim3((unsigned)grid, p.splits), dim3(mt::THREADS), mt::lds_bytes<F>(),
                      s, p);
-  MOELB_CHECK_LAUNCH();
-  return MOELB_OK;
-}
-
-template <bool GU>
-int launch_f32(AdapterArgs p, hipStream_t s) {
-  const int bn = GU ? 32 : 64, out = GU ? p.d_out / 2 : p.d_out;
-  p.ntn = (out + bn - 1) / bn;
-  const size_t grid = ((size_t)((p.Ttok + 63) / 64) * p.ntn + 7) / 8 * 8;
-  if (grid > 0x7fffffffull) return MOELB_EINVAL;
-  hipLaunchKernelGGL((adapter_tile_f32_kernel<GU>), dim3((unsigned)grid), dim3(mt::S_THREADS), 0, s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
@@ -736,28 +756,33 @@ int low_splits(int T, int d_in) {
 
 bool one_launch(int T, int n, int r) { return T <= ONE_TOKENS && (n == 0 || T * r <= ONE_LOW); }
 
-template <int NT, bool GU>
+template <typename T, int NT, bool GU>
 int launch_one(const AdapterArgs& p, hipStream_t s) {
   const int out = GU ? p.d_out / 2 : p.d_out, rows = GU ? 8 : 16;
-  hipLaunchKernelGGL((adapter_one_kernel<NT, GU>), dim3((out + rows - 1) / rows), dim3(MOELB_WAVE * ONE_WAVES), 0, s,
+  hipLaunchKernelGGL((adapter_one_kernel<T, NT, GU>), dim3((out + rows - 1) / rows), dim3(MOELB_WAVE * ONE_WAVES), 0, s,
                      p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
 
-template <bool GU>
+template <typename T, bool GU>
 int launch_sum(const AdapterArgs& p, hipStream_t s) {
   const long long threads = (long long)p.Ttok * (p.d_out / 2);
-  hipLaunchKernelGGL((adapter_few_sum_kernel<GU>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((adapter_few_sum_kernel<T, GU>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
 
+template <typename T, bool GU>
+int launch_ones(const AdapterArgs& p, hipStream_t s) {
+  return p.Ttok == 1   ? launch_one<T, 1, GU>(p, s)
+         : p.Ttok == 2 ? launch_one<T, 2, GU>(p, s)
+                       : launch_one<T, 4, GU>(p, s);
+}
+
 template <bool GU>
 int launch_few(AdapterArgs p, hipStream_t s) {
-  if (one_launch(p.Ttok, p.n, p.r)) {
-    return p.Ttok == 1 ? launch_one<1, GU>(p, s) : p.Ttok == 2 ? launch_one<2, GU>(p, s) : launch_one<4, GU>(p, s);
-  }
+  if (one_launch(p.Ttok, p.n, p.r)) return launch_ones<uint16_t, GU>(p, s);
   p.splits = few_splits(p.Ttok, p.d_in, p.d_out);
   const int tok = p.Ttok <= 16 ? 16 : p.Ttok <= 32 ? 32 : 64;
   p.nbase = (p.d_out + 63) / 64 * p.splits * ((p.Ttok + tok - 1) / tok);
@@ -769,7 +794,7 @@ int launch_few(AdapterArgs p, hipStream_t s) {
   else
     hipLaunchKernelGGL(adapter_few_kernel<4>, grid, dim3(256), 0, s, p);
   MOELB_CHECK_LAUNCH();
-  return launch_sum<GU>(p, s);
+  return launch_sum<uint16_t, GU>(p, s);
 }
 
 template <bool GU>
@@ -793,21 +818,79 @@ int launch_prompts(AdapterArgs p, hipStream_t s) {
   const int st = launch_tile<2, GU>(p, s);
   if (st != MOELB_OK || p.splits == 1) return st;
   p.n = 0;  // the adapters are in the partial sums
-  return launch_sum<GU>(p, s);
+  return launch_sum<uint16_t, GU>(p, s);
+}
+
+// fp32: parts of k of the 64 x 64 tiles, about a workgroup a compute unit, at
+// least 256 wide (64 tokens, 3088 x 1248, no adapters: 16 us against 70 whole).
+int f32_splits(int T, int d_in, int d_out) {
+  const size_t tiles = (size_t)((T + 63) / 64) * ((d_out + 63) / 64);
+  const size_t want = 256 / tiles, most = (size_t)d_in / 256;
+  const size_t s = want < most ? want : most;
+  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+// Few tokens: the adapters are the sum's kernel's, where a thread reads its own
+// rows of B (T x d_out x r values in all).  Else the tile walks the adapters
+// among its tokens, dealt over the parts of k.  3088 x 1248, r = 64, 25 adapters
+// in any order: 64 tokens 25 us against 34, 128 (gated) 38 against 41, but with
+// 8 runs of one adapter 37 against 33.  64 tokens, 1024 x 8192, r = 256 (134 M
+// values): 119 against 106, in runs 96 against 57.
+constexpr int F32_FEW_TOKENS = 128;
+constexpr size_t F32_FEW_VALUES = (size_t)16 << 20;
+bool f32_few(int T, int d_out, int n, int r) {
+  return n > 0 && T <= F32_FEW_TOKENS && (size_t)T * d_out * r <= F32_FEW_VALUES;
+}
+
+// Prompts' low products: four ranks a wave, which share the token's x, from here
+// on (r = 64: 2687 tokens, d_in = 312, 50 us a call against 70 with one rank;
+// 436 tokens, d_in = 4088, 136 against 147; 2768 tokens, d_in = 1832, 190
+// against 179); below, a rank a wave fills the compute units.
+constexpr size_t F32_FOUR_RANKS = 16384;
+
+template <bool GU>
+int launch_f32(AdapterArgs p, hipStream_t s) {
+  if (one_launch(p.Ttok, p.n, p.r)) return launch_ones<float, GU>(p, s);
+  const bool few = f32_few(p.Ttok, p.d_out, p.n, p.r);
+  if (!few && p.n > 0) {
+    const size_t waves = (size_t)p.Ttok * p.r;
+    const bool four = waves >= F32_FOUR_RANKS;
+    const size_t blocks = four ? (waves / 4 + 3) / 4 : (waves + 3) / 4;
+    if (blocks > 0x7fffffffull) return MOELB_EINVAL;
+    if (four)
+      hipLaunchKernelGGL(adapter_low_rows_f32_kernel<4>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL(adapter_low_rows_f32_kernel<1>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+    MOELB_CHECK_LAUNCH();
+  }
+  const int bn = GU ? 32 : 64, out = GU ? p.d_out / 2 : p.d_out;
+  p.ntn = (out + bn - 1) / bn;
+  p.splits = f32_splits(p.Ttok, p.d_in, p.d_out);
+  const size_t base = ((size_t)((p.Ttok + 63) / 64) * p.ntn + 7) / 8 * 8 * p.splits;
+  constexpr int waves = mt::S_THREADS / MOELB_WAVE;
+  const size_t grid = base + (few && p.n > 0 ? (p.Ttok * p.r + waves - 1) / waves : 0);
+  if (grid > 0x7fffffffull) return MOELB_EINVAL;
+  p.nbase = (int)base;
+  if (few)
+    hipLaunchKernelGGL((adapter_tile_f32_kernel<GU, true>), dim3((unsigned)grid), dim3(mt::S_THREADS), 0, s, p);
+  else
+    hipLaunchKernelGGL((adapter_tile_f32_kernel<GU, false>), dim3((unsigned)grid), dim3(mt::S_THREADS), 0, s, p);
+  MOELB_CHECK_LAUNCH();
+  if (!few && p.splits == 1) return MOELB_OK;
+  if (!few) p.n = 0;  // the adapters are in the partial sums
+  return launch_sum<float, GU>(p, s);
 }
 
 }  // namespace
 
 extern "C" size_t moelb_adapter_projection_workspace_bytes(int T, int d_in, int d_out, int n, int r, int dtype) {
   if (T < 0 || d_in < 1 || d_out < 1 || n < 0 || r < 0 || !moelb_dtype_ok(dtype)) return 0;
-  const bool few = dtype == MOELB_BF16 && T <= FEW_TOKENS;
-  if (few && one_launch(T, n, r)) return 0;
+  const bool bf = dtype == MOELB_BF16, few = bf ? T <= FEW_TOKENS : f32_few(T, d_out, n, r);
+  if (T == 0 || one_launch(T, n, r)) return 0;
   // low, and behind it the partial sums of few tokens, or of low itself
   const size_t low = n > 0 ? moelb_align256((size_t)T * r * (few ? 4 : moelb_elem_bytes(dtype))) : 0;
-  if (few) return low + (size_t)few_splits(T, d_in, d_out) * T * d_out * 4;
-  if (dtype != MOELB_BF16 || T == 0) return low;
-  const size_t lows = n > 0 ? (size_t)low_splits(T, d_in) * T * r * 4 : 0;
-  const int ts = tile_splits(T, d_in, d_out);
+  if (few) return low + (size_t)(bf ? few_splits(T, d_in, d_out) : f32_splits(T, d_in, d_out)) * T * d_out * 4;
+  const size_t lows = bf && n > 0 ? (size_t)low_splits(T, d_in) * T * r * 4 : 0;
+  const int ts = bf ? tile_splits(T, d_in, d_out) : f32_splits(T, d_in, d_out);
   const size_t sums = ts > 1 ? (size_t)ts * T * d_out * 4 : 0;  // after low's own are added
   return low + (lows > sums ? lows : sums);
 }
@@ -840,12 +923,6 @@ extern "C" int moelb_adapter_projection(const void* x, int T, int d_in, int d_ou
   if (bf) {
     if (T <= FEW_TOKENS) return gated ? launch_few<true>(p, s) : launch_few<false>(p, s);
     return gated ? launch_prompts<true>(p, s) : launch_prompts<false>(p, s);
-  }
-  if (n > 0) {
-    const long long blocks = ((long long)T * r + 3) / 4;
-    if (blocks > 0x7fffffffll) return MOELB_EINVAL;
-    hipLaunchKernelGGL(adapter_low_rows_f32_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p);
-    MOELB_CHECK_LAUNCH();
   }
   return gated ? launch_f32<true>(p, s) : launch_f32<false>(p, s);
 }

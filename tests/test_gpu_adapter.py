@@ -142,3 +142,46 @@ def test_same_bits_twice_and_captured(moelb):
             graph.replay()
             assert torch.equal(run(x, w, ids, a, b, scale, True), eager)
             assert torch.equal(y, eager)
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("order", ["requests", "mixed"])
+@pytest.mark.parametrize("shape", [(40, 2064, 2064, 9, 256), (128, 1288, 144, 5, 16), (129, 1288, 144, 5, 16),
+                                   (1100, 4104, 80, 7, 16), (3, 4104, 48, 4, 16)], ids=lambda s: "x".join(map(str, s)))
+def test_f32_parts_of_k(moelb, shape, order, gated):
+    """fp32 calls with few tiles: k and a tile's adapters in parts, whole and with a short last part; few tokens whose
+    rows of B are many; four ranks a wave."""
+    t = make(*shape, F32, seed=21, ids="requests" if order == "requests" else None)
+    check(*t, gated, run(*t, gated))
+
+
+def test_f32_parts_keep_tokens_apart(moelb):
+    """As test_other_tokens_do_not_matter, with k and the adapters in parts."""
+    for T in (3, 40, 300):
+        x, w, ids, a, b, scale = make(T, 2056, 144, 3, 16, F32, seed=22)
+        ids = torch.arange(T, device="cuda").remainder(3).to(torch.int32)
+        good = run(x, w, ids, a, b, scale, False)
+        a2, b2, x2 = a.clone(), b.clone(), x.clone()
+        a2[1], b2[1], x2[2::3] = float("nan"), float("inf"), float("nan")
+        got = run(x2, w, ids, a2, b2, scale, False)
+        assert torch.equal(got[0::3], good[0::3]), T
+        assert bool(torch.isnan(got[1::3]).all()) and bool(torch.isnan(got[2::3]).all())
+
+
+def test_f32_same_bits_twice_and_captured(moelb):
+    from routed_expert_ffn_gate_amd import moelb as M
+    for T in (2, 50, 400):
+        x, w, ids, a, b, scale = make(T, 1544, 272, 6, 16, F32, seed=23)
+        eager = run(x, w, ids, a, b, scale, True)
+        y = torch.empty_like(eager)
+        ws = torch.empty((max(1, M.moelb_adapter_projection_workspace_bytes(T, 1544, 272, 6, 16, M.dtype_code(x))),),
+                         dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            M.moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=True)
+        for _ in range(3):
+            y.fill_(9.0)
+            graph.replay()
+            assert torch.equal(run(x, w, ids, a, b, scale, True), eager)
+            assert torch.equal(y, eager)

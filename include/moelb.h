@@ -480,7 +480,8 @@ int moelb_pack_weights(const void* w, int E, int rows, int K, int dtype, void* p
  *  ws         train: moelb_grouped_ffn_workspace_bytes(...) bytes; backward:
  *             moelb_grouped_ffn_backward_workspace_bytes(...) bytes; no state
  *             is kept in it between the calls, and calls that may run at the
- *             same time need one each.
+ *             same time need one each.  The backward's size is 0 for counts and
+ *             widths that the call refuses.
  * Requires what moelb_grouped_ffn requires, d and inter up to 2^19, and rows*d, rows_x*d,
  * rows*2*inter and 2*inter*d elements each below 2^32 - 2^21 bytes.
  * All row data, weights, z and ws 16-byte aligned.  Outputs must not overlap

@@ -490,13 +490,16 @@ int launch_sum(const TrainArgs<T>& p, int M, int N, hipStream_t s) {
 
 bool misaligned(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15; }
 
+// Widths of the calls: a gathered row past the end plus a column stays outside
+// (mt::GONE), and no tile count overflows.
+constexpr int MAX_WIDTH = 1 << 19;
+
 // What both calls require of their sizes; operands of 32-bit byte offsets.
 bool sizes_ok(int rows_x, int rows, int num_groups, int E, int G, int rank, const void* gather, int gather_k, int d,
               int inter, int dtype) {
   if (rows < 0 || rows_x < 0 || num_groups < 1 || num_groups > 32768 || E < 1 || E > MOELB_MAX_E) return false;
   if (d <= 0 || d % 8 != 0 || inter <= 0 || inter % 8 != 0 || !moelb_dtype_ok(dtype)) return false;
-  // a gathered row past the end plus a column stays outside (mt::GONE)
-  if (d > 1 << 19 || inter > 1 << 19) return false;
+  if (d > MAX_WIDTH || inter > MAX_WIDTH) return false;
   if (rank >= 0 && (G < 1 || rank >= G || num_groups % E != 0)) return false;
   if (gather && gather_k < 1) return false;
   if (rows > 0 && rows_x < 1) return false;
@@ -597,7 +600,9 @@ extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, cons
 
 extern "C" size_t moelb_grouped_ffn_backward_workspace_bytes(int rows, int num_groups, int E, int d, int inter,
                                                              int dtype) {
-  if (rows < 0 || num_groups < 1 || E < 1 || d < 1 || inter < 1 || !moelb_dtype_ok(dtype)) return 0;
+  if (rows < 0 || num_groups < 1 || num_groups > 32768 || E < 1 || E > MOELB_MAX_E || d < 1 || d > MAX_WIDTH ||
+      inter < 1 || inter > MAX_WIDTH || !moelb_dtype_ok(dtype))
+    return 0;
   return back_layout(rows, num_groups, E, d, inter, dtype).total;
 }
 

@@ -664,6 +664,9 @@ extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, in
        reinterpret_cast<uintptr_t>(dw)) & 15)
     return MOELB_EINVAL;
   const size_t eb = moelb_elem_bytes(dtype);
+  // a column operand's 64 rows of a step, those past the last included, have
+  // 32-bit offsets
+  if (dtype == MOELB_BF16 && d > 1 << 25) return MOELB_EINVAL;
   // h, w and dz are operands of the tile
   const size_t Ep = ((size_t)E + 63) / 64 * 64, most = mt::MAX_BYTES;
   if ((size_t)T * d * eb >= most || (size_t)E * d * eb >= most || (size_t)T * Ep * eb >= most) return MOELB_EINVAL;

@@ -36,3 +36,16 @@ assert f(8, 1, 1, 1 << 19, 8, 1) > 0 and f(8, 1, 1, 8, 1 << 19, 1) > 0 and f(8, 
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+def test_gate_backward_refuses_rows_whose_offsets_wrap(lib):
+    """bf16: w and h are read 64 memory rows at a time by 32-bit byte offsets, the rows past the last one included
+    (they have to lie past the operand's end to read as zeros): 64 rows of 2 d bytes are 2^32 at d = 2^25.  No
+    workspace: nothing is launched."""
+    def call(d, dt):
+        return lib.moelb_gate_backward(P, 4, d, 4, 1, dt, P, P, P, P, None, 0, P, P, P, None)
+    row = lambda d, k: k * 2 * d + 2 * (d - 8) + 15  # noqa: E731  last byte of a 16-byte load of row k
+    assert row(1 << 25, 63) < 1 << 32 <= row((1 << 25) + 8, 63)
+    assert call(1 << 25, 1) == EWORKSPACE
+    assert call((1 << 25) + 8, 1) == EINVAL and call(1 << 28, 1) == EINVAL
+    assert call((1 << 25) + 8, 0) == EWORKSPACE  # fp32 rows are addressed with 64 bits

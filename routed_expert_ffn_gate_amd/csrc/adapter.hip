@@ -53,7 +53,9 @@ struct AdapterArgs {
   float* part;  // few tokens: [splits][T][d_out]; prompts: [splits][T][r]
   void* y;
   int Ttok, d_in, d_out, n, r, ntn, splits, nbase;
+  int first;  // number of this launch's first workgroup (launch_blocks)
 };
+__device__ __forceinline__ unsigned block_of(const AdapterArgs& p) { return (unsigned)p.first + blockIdx.x; }
 
 __device__ __forceinline__ uint32_t bytes32(size_t n) { return n < mt::MAX_BYTES ? (uint32_t)n : (uint32_t)mt::MAX_BYTES; }
 __device__ __forceinline__ int id_of(const AdapterArgs& p, int t) {
@@ -120,7 +122,7 @@ __device__ __forceinline__ void low_rows(const AdapterArgs& p, int block) {
 // fp32 prompts.
 template <int R>
 __global__ __launch_bounds__(256) void adapter_low_rows_f32_kernel(AdapterArgs p) {
-  low_rows<float, 4, R>(p, blockIdx.x);
+  low_rows<float, 4, R>(p, (int)block_of(p));
 }
 
 // The adapter of all tokens t0 .. t0 + rows - 1 (up to T), -1 if they differ or
@@ -407,13 +409,14 @@ template <bool GU, bool FEW>
 __global__ __launch_bounds__(mt::S_THREADS) void adapter_tile_f32_kernel(AdapterArgs p) {
   __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
   __shared__ int tok[64];
-  if (FEW && (int)blockIdx.x >= p.nbase) {
-    low_rows<float, mt::S_THREADS / MOELB_WAVE, 1>(p, blockIdx.x - p.nbase);
+  const unsigned bid = block_of(p);
+  if (FEW && (int)bid >= p.nbase) {
+    low_rows<float, mt::S_THREADS / MOELB_WAVE, 1>(p, bid - p.nbase);
     return;
   }
-  const int tiles = p.nbase / p.splits, split = blockIdx.x / tiles;  // tiles: a multiple of 8
+  const int tiles = p.nbase / p.splits, split = bid / tiles;  // tiles: a multiple of 8
   int mi, ni;
-  if (!tile_of(p, 64, blockIdx.x - split * tiles, mi, ni)) return;
+  if (!tile_of(p, 64, bid - split * tiles, mi, ni)) return;
   const int t0 = mi * 64, n0 = ni * (GU ? 32 : 64);
   const int out = GU ? p.d_out / 2 : p.d_out;
   const int per = ((p.d_in + 63) / 64 + p.splits - 1) / p.splits * 64;
@@ -484,8 +487,9 @@ constexpr int FEW_STAGES = 4;
 
 template <int NB>
 __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
-  if ((int)blockIdx.x >= p.nbase) {
-    low_rows<uint16_t, 4, 1>(p, blockIdx.x - p.nbase);
+  const unsigned bid = block_of(p);
+  if ((int)bid >= p.nbase) {
+    low_rows<uint16_t, 4, 1>(p, bid - p.nbase);
     return;
   }
   constexpr int TOK = 16 * NB, STAGE = (64 + TOK) * 64;  // elements
@@ -496,7 +500,7 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // a token block's workgroups of one W block are neighbours: they share its rows in L2
   const int tb = (p.Ttok + TOK - 1) / TOK;
-  const int split = blockIdx.x / tb % p.splits, n0 = blockIdx.x / tb / p.splits * 64, t0 = blockIdx.x % tb * TOK;
+  const int split = bid / tb % p.splits, n0 = bid / tb / p.splits * 64, t0 = bid % tb * TOK;
   const int steps = (p.d_in + 63) / 64, per = (steps + p.splits - 1) / p.splits;
   const int s0 = min(steps, split * per), n = min(steps, s0 + per) - s0;
   const mt::i32x4_t ws = mt::descriptor(p.w, bytes32((size_t)p.d_out * p.d_in * 2));
@@ -575,7 +579,7 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs p) {
 template <typename T, bool GU>
 __global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
   const int out = GU ? p.d_out / 2 : p.d_out, per = GU ? out : out / 2;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = (long long)block_of(p) * 256 + threadIdx.x;
   const int t = (int)(i / per), c = (int)(i % per);
   if (t >= p.Ttok) return;
   const int c0 = GU ? c : 2 * c, c1 = GU ? out + c : 2 * c + 1;
@@ -627,7 +631,7 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int out = GU ? p.d_out / 2 : p.d_out;
-  const int n0 = blockIdx.x * (GU ? 8 : 16);
+  const int n0 = block_of(p) * (GU ? 8 : 16);
   auto wrow = [&](int i) {  // row of W for row i of the workgroup
     const int c = n0 + (GU ? i & 7 : i);
     return (c < out ? c : 0) + (GU && i >= 8 ? out : 0);
@@ -717,12 +721,25 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
 // (d = 4096: 200 tokens 33 us against 47 on the tile, 400 tokens 54 against 52).
 constexpr int FEW_TOKENS = 256;
 
+// `blocks` workgroups in launches of less than 2^32 threads, each told the
+// number of its first.
+int launch_blocks(void (*kernel)(AdapterArgs), size_t blocks, unsigned threads, AdapterArgs p, hipStream_t s) {
+  if (blocks > 0x7fffffffull) return MOELB_EINVAL;
+  const size_t most = moelb_most_blocks(threads) & ~(size_t)7;
+  for (size_t b = 0; b < blocks; b += most) {
+    p.first = (int)b;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(threads), 0, s, p);
+    MOELB_CHECK_LAUNCH();
+  }
+  return MOELB_OK;
+}
+
 template <int F, bool GU>
 int launch_tile(AdapterArgs p, hipStream_t s) {
   const int B = 64 * F, bn = GU ? B / 2 : B, out = GU ? p.d_out / 2 : p.d_out;
   p.ntn = (out + bn - 1) / bn;
   const size_t grid = ((size_t)((p.Ttok + B - 1) / B) * p.ntn + 7) / 8 * 8;
-  if (grid > 0x7fffffffull) return MOELB_EINVAL;
+  if (grid > moelb_most_blocks(mt::THREADS)) return MOELB_EINVAL;
   if (!moelb_allow_lds(adapter_tile_kernel<F, GU>, mt::lds_bytes<F>())) return MOELB_ELAUNCH;
   hipLaunchKernelGGL((adapter_tile_kernel<F, GU>), dim3((unsigned)grid, p.splits), dim3(mt::THREADS), mt::lds_bytes<F>(),
                      s, p);
@@ -759,18 +776,12 @@ bool one_launch(int T, int n, int r) { return T <= ONE_TOKENS && (n == 0 || T * 
 template <typename T, int NT, bool GU>
 int launch_one(const AdapterArgs& p, hipStream_t s) {
   const int out = GU ? p.d_out / 2 : p.d_out, rows = GU ? 8 : 16;
-  hipLaunchKernelGGL((adapter_one_kernel<T, NT, GU>), dim3((out + rows - 1) / rows), dim3(MOELB_WAVE * ONE_WAVES), 0, s,
-                     p);
-  MOELB_CHECK_LAUNCH();
-  return MOELB_OK;
+  return launch_blocks(adapter_one_kernel<T, NT, GU>, (out + rows - 1) / rows, MOELB_WAVE * ONE_WAVES, p, s);
 }
 
 template <typename T, bool GU>
 int launch_sum(const AdapterArgs& p, hipStream_t s) {
-  const long long threads = (long long)p.Ttok * (p.d_out / 2);
-  hipLaunchKernelGGL((adapter_few_sum_kernel<T, GU>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
-  MOELB_CHECK_LAUNCH();
-  return MOELB_OK;
+  return launch_blocks(adapter_few_sum_kernel<T, GU>, ((size_t)p.Ttok * (p.d_out / 2) + 255) / 256, 256, p, s);
 }
 
 template <typename T, bool GU>
@@ -786,14 +797,12 @@ int launch_few(AdapterArgs p, hipStream_t s) {
   p.splits = few_splits(p.Ttok, p.d_in, p.d_out);
   const int tok = p.Ttok <= 16 ? 16 : p.Ttok <= 32 ? 32 : 64;
   p.nbase = (p.d_out + 63) / 64 * p.splits * ((p.Ttok + tok - 1) / tok);
-  const dim3 grid(p.nbase + (p.n > 0 ? (p.Ttok * p.r + 3) / 4 : 0));
-  if (p.Ttok <= 16)
-    hipLaunchKernelGGL(adapter_few_kernel<1>, grid, dim3(256), 0, s, p);
-  else if (p.Ttok <= 32)
-    hipLaunchKernelGGL(adapter_few_kernel<2>, grid, dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL(adapter_few_kernel<4>, grid, dim3(256), 0, s, p);
-  MOELB_CHECK_LAUNCH();
+  const size_t grid = (size_t)p.nbase + (p.n > 0 ? (p.Ttok * p.r + 3) / 4 : 0);
+  const int st = launch_blocks(p.Ttok <= 16   ? adapter_few_kernel<1>
+                               : p.Ttok <= 32 ? adapter_few_kernel<2>
+                                              : adapter_few_kernel<4>,
+                               grid, 256, p, s);
+  if (st != MOELB_OK) return st;
   return launch_sum<uint16_t, GU>(p, s);
 }
 
@@ -855,12 +864,9 @@ int launch_f32(AdapterArgs p, hipStream_t s) {
     const size_t waves = (size_t)p.Ttok * p.r;
     const bool four = waves >= F32_FOUR_RANKS;
     const size_t blocks = four ? (waves / 4 + 3) / 4 : (waves + 3) / 4;
-    if (blocks > 0x7fffffffull) return MOELB_EINVAL;
-    if (four)
-      hipLaunchKernelGGL(adapter_low_rows_f32_kernel<4>, dim3((unsigned)blocks), dim3(256), 0, s, p);
-    else
-      hipLaunchKernelGGL(adapter_low_rows_f32_kernel<1>, dim3((unsigned)blocks), dim3(256), 0, s, p);
-    MOELB_CHECK_LAUNCH();
+    const int st =
+        launch_blocks(four ? adapter_low_rows_f32_kernel<4> : adapter_low_rows_f32_kernel<1>, blocks, 256, p, s);
+    if (st != MOELB_OK) return st;
   }
   const int bn = GU ? 32 : 64, out = GU ? p.d_out / 2 : p.d_out;
   p.ntn = (out + bn - 1) / bn;
@@ -870,11 +876,9 @@ int launch_f32(AdapterArgs p, hipStream_t s) {
   const size_t grid = base + (few && p.n > 0 ? (p.Ttok * p.r + waves - 1) / waves : 0);
   if (grid > 0x7fffffffull) return MOELB_EINVAL;
   p.nbase = (int)base;
-  if (few)
-    hipLaunchKernelGGL((adapter_tile_f32_kernel<GU, true>), dim3((unsigned)grid), dim3(mt::S_THREADS), 0, s, p);
-  else
-    hipLaunchKernelGGL((adapter_tile_f32_kernel<GU, false>), dim3((unsigned)grid), dim3(mt::S_THREADS), 0, s, p);
-  MOELB_CHECK_LAUNCH();
+  const int st = launch_blocks(few ? adapter_tile_f32_kernel<GU, true> : adapter_tile_f32_kernel<GU, false>, grid,
+                               mt::S_THREADS, p, s);
+  if (st != MOELB_OK) return st;
   if (!few && p.splits == 1) return MOELB_OK;
   if (!few) p.n = 0;  // the adapters are in the partial sums
   return launch_sum<float, GU>(p, s);

@@ -89,6 +89,10 @@ __device__ __forceinline__ int wave_sum_i32(int v) {
     if (hipGetLastError() != hipSuccess) return MOELB_ELAUNCH; \
   } while (0)
 
+// Threads of a one-dimensional launch stay below 2^32: the runtime counts them
+// in 32 bits and runs what the lower bits say, without an error.
+static inline size_t moelb_most_blocks(unsigned threads) { return 0xffffffffull / threads; }
+
 static inline size_t moelb_align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 static inline bool moelb_dtype_ok(int dtype) { return dtype == MOELB_F32 || dtype == MOELB_BF16; }
 static inline size_t moelb_elem_bytes(int dtype) { return dtype == MOELB_F32 ? 4 : 2; }

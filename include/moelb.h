@@ -483,7 +483,9 @@ int moelb_pack_weights(const void* w, int E, int rows, int K, int dtype, void* p
  *             same time need one each.  The backward's size is 0 for counts and
  *             widths that the call refuses.
  * Requires what moelb_grouped_ffn requires, d and inter up to 2^19, and rows*d, rows_x*d,
- * rows*2*inter and 2*inter*d elements each below 2^32 - 2^21 bytes.
+ * rows*2*inter and 2*inter*d elements each below 2^32 - 2^21 bytes.  A call whose
+ * tiles would take 2^32 threads or more in one launch (hundreds of fp32 experts of
+ * the widest layers) is refused.
  * All row data, weights, z and ws 16-byte aligned.  Outputs must not overlap
  * the inputs or each other.
  */

@@ -461,7 +461,6 @@ size_t weights_grid(TrainArgs<T>& p, int BM, int BN, int M, int N) {
 template <typename T, int OP>
 int launch_rows(TrainArgs<T> p, int BM, int BN, hipStream_t s) {
   const size_t grid = rows_grid(p, BM, OP == OP_UP ? BN / 2 : BN, (OP == OP_UP || OP == OP_DA) ? p.inter : p.d);
-  if (grid > 0x7fffffffull) return MOELB_EINVAL;
   const dim3 g((unsigned)grid);
   if constexpr (sizeof(T) == 4) {
     if (BN == 64)
@@ -508,6 +507,19 @@ bool sizes_ok(int rows_x, int rows, int num_groups, int E, int G, int rank, cons
          (size_t)2 * inter * d * eb < most;
 }
 
+// Whether every launch of a forward (of a backward, with the gradients that are
+// asked for) stays under 2^32 threads.
+bool launches_ok(int rows, int E, int d, int inter, int dtype, bool backward, bool dx, bool dw13, bool dw2) {
+  TrainArgs<float> p = {};  // sizes only
+  p.rows = rows, p.d = d, p.inter = inter, p.E = E;
+  const int BM = tile_rows(rows, E, d, inter, dtype), BN = tile_cols(rows, E, d, inter, dtype);
+  const size_t most = moelb_most_blocks(dtype == MOELB_BF16 ? mt::THREADS : mt::S_THREADS);
+  if (!backward) return rows_grid(p, BM, BN / 2, inter) <= most && rows_grid(p, BM, BN, d) <= most;
+  const size_t grads = (dw13 ? weights_grid(p, BM, BN, 2 * inter, d) : 0) + (dw2 ? weights_grid(p, BM, BN, d, inter) : 0) +
+                       (dx ? rows_grid(p, BM, BN, d) + 7 : 0);
+  return rows_grid(p, BM, BN, inter) <= most && grads <= most;
+}
+
 template <typename T>
 int run_forward(TrainArgs<T> p, int BM, int BN, hipStream_t s) {
   int st = launch_rows<T, OP_UP>(p, BM, BN, s);
@@ -528,7 +540,6 @@ int run_backward(TrainArgs<T> p, int BM, int BN, T* dx, T* dw13, T* dw2, float* 
   if (dw2) n2 = weights_grid(g.w2, BM, BN, p.d, p.inter);
   if (dx && p.rows > 0) nx = (rows_grid(g.x, BM, BN, p.d) + 7) / 8 * 8;
   const size_t grid = n13 + n2 + nx;
-  if (grid > 0x7fffffffull) return MOELB_EINVAL;
   if (grid == 0) return MOELB_OK;
   g.n13 = (int)n13, g.n2 = (int)n2, g.nx = (int)nx;
   const dim3 gd((unsigned)grid);
@@ -564,6 +575,7 @@ extern "C" int moelb_grouped_ffn_train(const void* x, int rows_x, int rows, cons
   const size_t need = sched_layout(rows, num_groups, E, inter, dtype, nullptr, nullptr);
   if (!ws || misaligned(ws) || ws_bytes < need) return MOELB_EWORKSPACE;
   if (rows == 0) return MOELB_OK;
+  if (!launches_ok(rows, E, d, inter, dtype, false, false, false, false)) return MOELB_EINVAL;
   FfnSched sc;
   sched_layout(rows, num_groups, E, inter, dtype, &sc, static_cast<char*>(ws));
   sc.wpacked = 0;
@@ -619,6 +631,7 @@ extern "C" int moelb_grouped_ffn_backward(const void* dy, const void* x, int row
   const BackLayout l = back_layout(rows, num_groups, E, d, inter, dtype);
   if (!ws || misaligned(ws) || ws_bytes < l.total) return MOELB_EWORKSPACE;
   if (!dx && !dw13 && !dw2) return MOELB_OK;
+  if (!launches_ok(rows, E, d, inter, dtype, true, dx, dw13, dw2)) return MOELB_EINVAL;
   char* base = static_cast<char*>(ws);
   FfnSched sc;
   sched_layout(rows, num_groups, E, inter, dtype, &sc, base);

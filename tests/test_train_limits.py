@@ -49,3 +49,22 @@ def test_gate_backward_refuses_rows_whose_offsets_wrap(lib):
     assert call(1 << 25, 1) == EWORKSPACE
     assert call((1 << 25) + 8, 1) == EINVAL and call(1 << 28, 1) == EINVAL
     assert call((1 << 25) + 8, 0) == EWORKSPACE  # fp32 rows are addressed with 64 bits
+
+
+def ffn(lib, back, rows, E, d, inter, dt, dx=P, d13=P, d2=P, ws=P):
+    """The call with `rows` rows in one group an expert."""
+    if back:
+        return lib.moelb_grouped_ffn_backward(P, P, max(rows, 1), rows, P, E, E, 1, -1, None, 1, d, inter, dt, P, P, P, ws,
+                                              1 << 62, dx, d13, d2, None)
+    return lib.moelb_grouped_ffn_train(P, max(rows, 1), rows, P, E, E, 1, -1, None, 1, d, inter, dt, P, P, ws, 1 << 62, P,
+                                       P, None)
+
+
+def test_ffn_refuses_launches_of_2_32_threads(lib):
+    """fp32, 256 experts, the widest layers: 64 x 16 tiles of the gate and up columns, or 64 x 32 tiles of the three
+    gradients together, pass 2^32 threads of 512 a tile; the runtime would run what the lower bits say."""
+    wide = 1 << 19
+    assert (8 // 64 + 1 + 256) * (wide // 16) * 512 >= 1 << 32
+    assert ffn(lib, False, 8, 256, 8, wide, 0) == EINVAL
+    # dw13 (16 rows) and dx 2^31 each, dw2 2^30
+    assert ffn(lib, True, 8, 256, wide, 8, 0) == EINVAL

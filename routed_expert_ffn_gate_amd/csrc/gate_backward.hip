@@ -608,6 +608,21 @@ int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
   }
 }
 
+// Workgroups of dh and of dW in fp32.
+void grads_grid(const GateArgs<float>& p, size_t& nh, size_t& nw) {
+  const size_t ntn = (p.d + 63) / 64;
+  nh = p.dh ? (size_t)((p.Ttok + 63) / 64) * ntn : 0;
+  nw = p.dw ? (size_t)((p.E + 63) / 64) * ntn * p.splits : 0;
+}
+bool launches_ok(const GateArgs<float>& p) {
+  size_t nh, nw;
+  grads_grid(p, nh, nw);
+  return nh + nw <= moelb_most_blocks(mt::S_THREADS);
+}
+// bf16 rows are at most 2^25 elements, T d and E d below 2^31 of them: T / 128 x
+// d / 128 workgroups of 256 threads and less
+bool launches_ok(const GateArgs<uint16_t>&) { return true; }
+
 int run(GateArgs<float> p, bool fused, hipStream_t s) {
   if (fused) {
     hipLaunchKernelGGL(gate_dz_f32_kernel, dim3(p.blocks), dim3(mt::S_THREADS), 0, s, p);
@@ -621,10 +636,8 @@ int run(GateArgs<float> p, bool fused, hipStream_t s) {
     const int st = launch_softmax(p, s);
     if (st != MOELB_OK) return st;
   }
-  const size_t ntn = (p.d + 63) / 64;
-  const size_t nh = p.dh && p.Ttok > 0 ? (size_t)((p.Ttok + 63) / 64) * ntn : 0;
-  const size_t nw = p.dw ? (size_t)((p.E + 63) / 64) * ntn * p.splits : 0;
-  if (nh + nw > 0x7fffffffull) return MOELB_EINVAL;
+  size_t nh, nw;
+  grads_grid(p, nh, nw);
   p.nh = (int)nh;
   if (nh + nw > 0) {
     hipLaunchKernelGGL(gate_grads_f32_kernel, dim3((unsigned)(nh + nw)), dim3(mt::S_THREADS), 0, s, p);
@@ -688,6 +701,7 @@ extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, in
     p.dw = static_cast<U*>(dw);
     p.db = db;
     p.Ttok = T, p.d = d, p.E = E, p.Ep = l.Ep, p.k = k, p.splits = l.splits, p.blocks = l.blocks;
+    if (!launches_ok(p)) return (int)MOELB_EINVAL;
     return run_all<U>(p, l.fused && T > 0, static_cast<hipStream_t>(stream));
   };
   return dtype == MOELB_BF16 ? go(static_cast<uint16_t*>(nullptr)) : go(static_cast<float*>(nullptr));

@@ -68,3 +68,12 @@ def test_ffn_refuses_launches_of_2_32_threads(lib):
     assert ffn(lib, False, 8, 256, 8, wide, 0) == EINVAL
     # dw13 (16 rows) and dx 2^31 each, dw2 2^30
     assert ffn(lib, True, 8, 256, wide, 8, 0) == EINVAL
+
+
+def test_gate_backward_refuses_launches_of_2_32_threads(lib):
+    """fp32: 64-column tiles of dh and of dw, 512 threads each, in one launch.  T = 1, d = 2^29 is 2^32 of them for dh
+    alone, d = 2^28 for both."""
+    def call(d, dh=P, dw=P):
+        return lib.moelb_gate_backward(P, 1, d, 1, 1, 0, P, P, P, P, P, 1 << 62, dh, dw, P, None)
+    assert call(1 << 29) == EINVAL and call((1 << 28) + 64) == EINVAL and call(1 << 28) == EINVAL
+    assert call(1 << 29, dw=None) == EINVAL and call(1 << 29, dh=None) == EINVAL

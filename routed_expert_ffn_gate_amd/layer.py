@@ -362,12 +362,16 @@ class MoELayer:
     def _shared_with_adapters(self, h, shared_w13, shared_w2, ad: SharedAdapters, stream):
         """The shared expert as two projections with each token's adapters
         beside them: gate and up gated into the activations, then down."""
-        T, d, si = self.T, self.d, self.shared_inter
+        d, si = self.d, self.shared_inter
+
+        def one(what, w, shape):  # one expert's weights, with or without the leading dimension
+            if tuple(w.shape) not in (shape, (1, *shape)):
+                raise M.MoelbError(f"shared_adapters: {what} is {tuple(w.shape)}, not {shape}")
+            return w[0] if w.dim() == 3 else w
+        w13, w2 = one("shared_w13", shared_w13, (2 * si, d)), one("shared_w2", shared_w2, (d, si))
         ws, mid = self._adapter_buffers(ad, M.dtype_code(h))
-        M.moelb_adapter_projection(h, shared_w13.reshape(2 * si, d), ad.ids, ad.a13, ad.b13, ad.scale13, ws, mid,
-                                   gated=True, stream=stream)
-        M.moelb_adapter_projection(mid, shared_w2.reshape(d, si), ad.ids, ad.a2, ad.b2, ad.scale2, ws, self.shared,
-                                   stream=stream)
+        M.moelb_adapter_projection(h, w13, ad.ids, ad.a13, ad.b13, ad.scale13, ws, mid, gated=True, stream=stream)
+        M.moelb_adapter_projection(mid, w2, ad.ids, ad.a2, ad.b2, ad.scale2, ws, self.shared, stream=stream)
 
     def _adapter_buffers(self, ad: SharedAdapters, code):
         """(workspace, activations) of a step with these adapters."""

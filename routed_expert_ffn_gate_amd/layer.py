@@ -226,6 +226,7 @@ class MoELayer:
             self.home_base = None
         self._train = None      # buffers of the training form, made at its first step
         self._kept = False      # the layer's buffers are those of a training step
+        self._captured = False  # which was captured, not run
         self._adapter_ws = []   # the last one in use; a captured graph may hold an earlier one
         self._adapter_mid = None
         self.ws_shared = None
@@ -473,6 +474,7 @@ class MoELayer:
         s0.wait_event(self.ev_side)
         mark(7)
         self._kept = train
+        self._captured = torch.cuda.is_current_stream_capturing()
         return self._out()
 
     def backward(self, dout, h, w_cur, b_cur, w13, w2, shared_w13=None, shared_w2=None, stream=None) -> Gradients:
@@ -484,9 +486,12 @@ class MoELayer:
         the shared expert's; the hidden states' gradient is the sum of their
         shares, each rounded to the layer's type once.  A step replayed from a
         captured graph writes the layer's buffers unseen: its backward belongs
-        into the same graph."""
+        into the same graph, and after a captured step is refused outside of a
+        capture."""
         if not self._kept:
             raise RuntimeError("backward needs the layer's last step to be step(..., train=True)")
+        if self._captured and not torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("backward: the layer's last step was captured, not run: capture backward with it")
         b = self._train
         s0 = stream if stream is not None else torch.cuda.current_stream()
         x = h if self.gather_rows else self.x_perm

@@ -25,3 +25,30 @@ def test_adapters_refuse_weights_of_another_shape(moelb):
             step(L, dict(t, **bad), shared_adapters=ad)
     torch.cuda.synchronize()
     assert torch.equal(step(L, t, shared_adapters=ad).out, want)
+
+
+def test_backward_outside_of_the_steps_capture(moelb):
+    """A captured step has not run when its capture ends: backward called eagerly after it would read what an earlier
+    step left."""
+    L, t = build("bf16", True)
+    args = (t["dout"], t["h"], t["wc"], t["bc"], t["w13"], t["w2"], t["s13"], t["s2"])
+    step(L, t, train=True)
+    want = L.backward(*args).h.clone()
+    step(L, dict(t, h=-t["h"]), train=True)  # what the buffers hold from here on
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(L, t, train=True)
+    with pytest.raises(RuntimeError, match="captured"):
+        L.backward(*args)
+    # in the same graph, or a step that has run, it is answered
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(L, t, train=True)
+        got = L.backward(*args)
+    for _ in range(3):
+        got.h.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got.h, want)
+    step(L, t, train=True)
+    assert torch.equal(L.backward(*args).h, want)

@@ -308,16 +308,11 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs& p, int split, co
   }
 }
 
-__device__ __forceinline__ void store_gated(uint16_t* y, const float* g, const float* u) {
+template <typename T>
+__device__ __forceinline__ void store_gated(T* y, const float* g, const float* u) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = silu_f32(g[i]) * u[i];
-  mt::store8(y, v);
-}
-__device__ __forceinline__ void store_gated(float* y, const float* g, const float* u) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = silu_f32(g[i]) * u[i];
+  for (int i = 0; i < 8; ++i) v[i] = mt::silu_as<T>(g[i]) * u[i];
   mt::store8(y, v);
 }
 
@@ -610,7 +605,7 @@ __global__ __launch_bounds__(256) void adapter_few_sum_kernel(AdapterArgs p) {
   }
   T* y = static_cast<T*>(p.y) + (size_t)t * out;
   if constexpr (GU)
-    Elem<T>::store(y, c, silu_f32(v0) * v1);
+    Elem<T>::store(y, c, mt::silu_as<T>(v0) * v1);
   else if constexpr (sizeof(T) == 4)
     *reinterpret_cast<float2*>(y + 2 * c) = make_float2(v0, v1);
   else
@@ -711,7 +706,7 @@ __global__ __launch_bounds__(MOELB_WAVE * ONE_WAVES) void adapter_one_kernel(Ada
       }
     }
   }
-  if (GU) v0 = silu_f32(v0) * v1;
+  if (GU) v0 = mt::silu_as<T>(v0) * v1;
   Elem<T>::store(static_cast<T*>(p.y), (size_t)tt * out + n0 + tj, v0);
 }
 

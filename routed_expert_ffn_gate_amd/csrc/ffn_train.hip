@@ -75,7 +75,7 @@ __device__ __forceinline__ void put_up(const TrainArgs<T>& p, int v, int n, cons
   mt::store8(z + p.inter, u);
   float a[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = silu_f32(g[i]) * u[i];
+  for (int i = 0; i < 8; ++i) a[i] = mt::silu_as<T>(g[i]) * u[i];
   mt::store8(p.a + (size_t)v * p.inter + n, a);
 }
 
@@ -87,11 +87,12 @@ __device__ __forceinline__ void put_da(const TrainArgs<T>& p, int v, int n, cons
   mt::load8(z + p.inter, u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[i]));
+    float s, c;
+    mt::sigmoid_as<T>(g[i], s, c);
     const float gs = g[i] * s;
     a[i] = gs * u[i];
     du[i] = da[i] * gs;
-    dg[i] = da[i] * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+    dg[i] = da[i] * u[i] * (s * (1.0f + g[i] * c));
   }
   T* dz = p.dz + (size_t)v * 2 * p.inter + n;
   mt::store8(dz, dg);

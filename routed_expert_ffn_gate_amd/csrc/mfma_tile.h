@@ -435,6 +435,27 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
+// The gate's s = 1 / (1 + e^-g) and 1 - s.  bf16: the hardware exponential and
+// reciprocal, whose error (about |g| 2^-24 relative, from the exponent's
+// rounding) is far under the type's half step.  fp32: the library's exponential
+// and a true quotient; for g > 0, 1 - s = e^-g s, since s itself is near 1.
+template <typename T>
+__device__ __forceinline__ void sigmoid_as(float g, float& s, float& c) {
+  if constexpr (sizeof(T) == 4) {
+    const float e = expf(-g);
+    s = 1.0f / (1.0f + e);
+    c = g > 0.f ? e * s : 1.0f - s;
+  } else {
+    s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+    c = 1.0f - s;
+  }
+}
+template <typename T>
+__device__ __forceinline__ float silu_as(float g) {
+  if constexpr (sizeof(T) == 4) return g / (1.0f + expf(-g));
+  return silu_f32(g);
+}
+
 // ---------------------------------------------------------------- fp32 tile
 //
 // The same products for fp32 storage: tile 64 x TN (TN = 64, or 32 where a call

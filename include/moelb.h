@@ -528,8 +528,9 @@ int moelb_combine(const void* y, int rows_y, const int32_t* pos, const float* wt
  *  dy     [rows_y,d] dtype out: rows that no pair names are not written
  *  dwts   [T*k] fp32 out
  * Pairs with pos < 0 or pos >= rows_y are left out.  The named rows must be
- * distinct, as moelb_permute's are: of several pairs naming one row, its dy
- * holds one's share (all memory safe).  dy must not overlap the inputs.
+ * distinct, as moelb_permute's are: of several pairs naming one row, each 16
+ * bytes of its dy hold one's share (all memory safe).  dy must not overlap the
+ * inputs.
  * Same requirements as moelb_combine.
  */
 int moelb_combine_backward(const void* dout, const void* y, int rows_y, const int32_t* pos,
@@ -565,8 +566,9 @@ int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, co
 /*
  * A shared projection with the low-rank adapters of many requests beside it:
  *   y[t] = x[t] w^T + scale[i] (x[t] a[i]^T) b[i]^T,  i = ids[t]
- * with fp32 accumulation, y rounded to dtype once (and the r values x[t]
- * a[i]^T once, as the operand of their second product).  gated: w and every
+ * with fp32 accumulation, y rounded to dtype once (and, above 256 tokens in
+ * bf16, the r values x[t] a[i]^T once, as the operand of their second product).
+ * gated: w and every
  * b[i] hold d_out / 2 gate rows and then d_out / 2 up rows, and y[t] =
  * SiLU(gate) * up.  Two calls, gated with w13 and plain with w2, are the
  * layer's shared expert with adapters; n = 0 is the bare projection.
@@ -575,7 +577,9 @@ int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, co
  *  ids    [T] int32        adapter of each token; outside [0,n): none.  Tokens
  *                          may come in any order; those of one adapter next to
  *                          each other run fastest.  A token's y depends on its
- *                          own x and adapter only
+ *                          own x and adapter only; the order of its sums and
+ *                          the rounding above, so its last bit, also on T and
+ *                          on whether its neighbours share the adapter
  *  a      [n,r,d_in], b [n,d_out,r]  dtype; an adapter of a smaller rank is
  *                          padded with zero rows of a
  *  scale  [n] fp32

@@ -18,7 +18,8 @@
 //    tokens (as a shared K step with zeros for the other tokens would let it).
 //    Its low products come from a launch of their own, in the storage type (an
 //    operand of the second product, off by half a step of the adapter's small
-//    share of y).
+//    share of y; few tokens keep them in fp32, so a token's last bit can follow
+//    from the size of its batch).
 //  * Few tokens (up to 256): the bytes of W and of the adapters in use bound it,
 //    so the work is cut for many loads in flight: 64 rows of W x a part of k a
 //    workgroup, v_mfma_f32_16x16x32_bf16 straight from registers, with the low
@@ -37,7 +38,11 @@
 // adapter each, 4096 x 4096 gated, r = 16: 11.3 us (4.4 TB/s of W and adapters)
 // and 4.2 us for the second launch; 8192 tokens of 16 requests, 4096 x 4096, r =
 // 64: low products 22 + 6 us, y 253 us (matrix units busy 0.59; 217 us is a
-// library product of W alone).
+// library product of W alone).  Tokens in no order cost a walk over a tile's
+// adapters: 512 tokens of 8 requests, r = 64, 50 us, each with an adapter of its
+// own 359; 8192 tokens over 16 adapters at random 959 us, over 64 (r = 16) 1521.
+// Few tokens of large ranks are bound by the second launch's reads of B: 64
+// tokens, gated, r = 16, 64, 256: 16, 25, 70 us; 256 tokens: r = 16 34, r = 256 219.
 #include "mfma_tile.h"
 
 namespace {

@@ -31,10 +31,14 @@
 //
 // What bounds it: large groups, the matrix units at the clock they leave (busy
 // 0.6 to 0.7 at 1.5 to 1.7 GHz; da 0.4 to 0.5, whose epilogue reads z and
-// writes two operands); few rows a group, the weight gradients' bytes (128
-// experts, d = 2048, inter = 768: 1.2 GB in 259 us); small calls, one launch
-// after another (4 to 26 us each).  64 groups of 2048 rows, d = 2048, inter =
-// 1024, bf16: forward 1.69 ms (977 TFLOP/s), backward 3.41 ms (967).
+// writes two operands); few rows a group, the weights and their gradients, at a
+// third to half of the memory's rate, since a 128-row tile mostly repeats rows
+// and a weight gradient's tile is one K step between its first loads and its
+// stores (128 experts of 11 to 63 rows, d = 2048, inter = 768: up 227 us for 0.42
+// GB read, the gradients 610 us for 1.7 GB); small calls, one launch after
+// another (5 to 47 us each).  64 groups of 2048 rows, d = 2048, inter = 1024,
+// bf16: forward 1.69 ms (977 TFLOP/s), backward 3.41 ms (967); the same rows in
+// groups of 995 to 4079: 5.0 ms both (990).
 #include "ffn_sched.h"
 #include "mfma_tile.h"
 
@@ -393,7 +397,11 @@ __global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict
 // ---------------------------------------------------------------- host
 
 // Tile height of a call (64 F, or 64 for fp32): 256 where the experts average
-// enough rows and the tiles still cover the compute units.
+// enough rows and the tiles still cover the compute units.  Routed (uneven)
+// rows, a whole step in us with 128 | 256, by rows an expert: 64 experts, d = 2048,
+// inter = 1024: 160: 965 | 994, 192: 1077 | 1032, 384: 1603 | 1400; 128 experts,
+// inter = 768: 160: 1457 | 1389, 256: 1807 | 1692; 16 experts, where the tiles
+// do not cover the units: 192: 271 | 302, 384: 400 | 445, 512: 513 | 492.
 int tile_rows(int rows, int E, int d, int inter, int dtype) {
   if (dtype != MOELB_BF16) return mt::S_BM;
   const int least = d < inter ? d : inter;

@@ -22,8 +22,9 @@
 //
 // What bounds it: reading h twice (for z and for dW) and writing dh.  T = 32768,
 // d = 4096, E = 128, bf16: step 1 and 2 in 77 us (3.5 TB/s of h), 3 and 4 in one
-// launch of 135 us, 5 in 6 us.  Small calls: three launches (T = 256, d = 256,
-// E = 16, fp32: 10, 8 and 2 us).
+// launch of 135 us, 5 in 6 us.  Beyond 128 experts z and dz go through memory and
+// W takes two buffers: E = 160 372 us, E = 256 386 (the call).  Small calls: three
+// launches (T = 256, d = 256, E = 16, fp32: 10, 8 and 2 us).
 #include "mfma_tile.h"
 
 namespace {

@@ -483,8 +483,9 @@ class MoELayer:
         The placement of pairs on ranks carries no gradient: a pair's row is
         its expert's output wherever it is computed.  The combine's gradient
         comes first, then the experts' (dx a row per pair), the router's and
-        the shared expert's; the hidden states' gradient is the sum of their
-        shares, each rounded to the layer's type once.  A step replayed from a
+        the shared expert's, each rounded to the layer's type once.  The hidden
+        states' gradient is the fp32 sum of the pairs' and the router's share,
+        rounded; a shared expert's share is added to that and rounded again.  A step replayed from a
         captured graph writes the layer's buffers unseen: its backward belongs
         into the same graph, and after a captured step is refused outside of a
         capture."""
@@ -506,7 +507,9 @@ class MoELayer:
         d13, d2 = b["dw13_shared"].view(shared_w13.shape), b["dw2_shared"].view(shared_w2.shape)
         M.moelb_grouped_ffn_backward(dout, h, self.T, self.shared_off, 1, shared_w13, shared_w2, b["z_shared"],
                                      b["ws_shared"], b["dx_shared"], d13, d2, stream=s0)
-        # dh += dx_shared: dh_router's buffer is free again
+        # dh += dx_shared: dh_router's buffer is free again.  The combine adds one
+        # tensor beside its rows, so this third share meets a sum already rounded
+        # (bf16: half a step of it, as much as each share's own rounding)
         M.moelb_combine(b["dx_shared"], b["own_row"], b["one"], b["dh_router"], shared=b["dh"], stream=s0)
         return Gradients(b["dh_router"], b["dw"], b["db"], b["dw13"], b["dw2"], d13, d2)
 

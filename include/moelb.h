@@ -553,8 +553,8 @@ int moelb_combine_backward(const void* dout, const void* y, int rows_y, const in
  *  dh   [T,d] dtype out or NULL;  dw [E,d] dtype out or NULL;  db [E] fp32 out
  *       or NULL (T = 0: dw and db are zero)
  * Ids outside [0,E) are left out; an id listed twice counts twice.
- * Requires 1 <= k <= min(E, 16), E <= 256, d % 8 == 0 (bf16: d <= 2^25; fp32: d < 2^28, or
- * d < 2^29 for only one of dh and dw), T >= 0,
+ * Requires 1 <= k <= min(E, 16), E <= 256, d % 8 == 0 (bf16: d <= 2^25; fp32: d <= 2^28 - 64, or
+ * 2^29 - 64 for only one of dh and dw), T >= 0,
  * T*d, E*d and T*E (E rounded up to 64) elements each below 2^32 - 2^21 bytes; h, w,
  * ws, dh and dw 16-byte aligned.
  */

@@ -280,6 +280,10 @@ class MoELayer:
         self.sched_cur, self.sched_next = self.sched_next, self.sched_cur
         return self.replica_spare
 
+    def _need_shared(self, shared_w13, shared_w2):
+        if self.shared is not None and (shared_w13 is None or shared_w2 is None):
+            raise ValueError("the layer has a shared expert: its weights shared_w13 and shared_w2 are missing")
+
     def _may_make(self, what):
         """Buffers made by a step are made outside of a capture: their constants
         are written once, not at every replay."""
@@ -412,6 +416,8 @@ class MoELayer:
             raise ValueError("train and shared_adapters take row-major weights")
         if shared_adapters is not None and (train or self.shared is None):
             raise ValueError("shared_adapters need a shared expert, and are not trained")
+        if train or shared_adapters is not None:
+            self._need_shared(shared_w13, shared_w2)
         if train:
             self._train_buffers()
         if shared_adapters is not None:
@@ -493,6 +499,7 @@ class MoELayer:
             raise RuntimeError("backward needs the layer's last step to be step(..., train=True)")
         if self._captured and not torch.cuda.is_current_stream_capturing():
             raise RuntimeError("backward: the layer's last step was captured, not run: capture backward with it")
+        self._need_shared(shared_w13, shared_w2)
         b = self._train
         s0 = stream if stream is not None else torch.cuda.current_stream()
         x = h if self.gather_rows else self.x_perm

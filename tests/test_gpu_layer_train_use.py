@@ -52,3 +52,30 @@ def test_backward_outside_of_the_steps_capture(moelb):
         assert torch.equal(got.h, want)
     step(L, t, train=True)
     assert torch.equal(L.backward(*args).h, want)
+
+
+def test_missing_shared_weights_are_refused_first(moelb):
+    """A layer with a shared expert, called without its weights: refused before anything is queued (it ended in an
+    AttributeError half-way, with the layer's buffers overwritten)."""
+    L, t = build("bf16", True)
+    ad = make_adapters(L, 3, 8, 8, BF)
+    args = (t["dout"], t["h"], t["wc"], t["bc"], t["w13"], t["w2"])
+    step(L, t, train=True)
+    want = L.backward(*args, t["s13"], t["s2"])
+    torch.cuda.synchronize()
+    held = {n: getattr(want, n).clone() for n in ("h", "w_cur", "w13", "w2")}
+    with pytest.raises(ValueError, match="shared"):
+        L.backward(-t["dout"], *args[1:])
+    with pytest.raises(ValueError, match="shared"):
+        L.backward(-t["dout"], *args[1:], t["s13"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(getattr(want, n), v) for n, v in held.items())
+    idx = L.idx.clone()
+    for kw in (dict(train=True), dict(shared_adapters=ad)):
+        for miss in (dict(s13=None), dict(s2=None)):
+            with pytest.raises(ValueError, match="shared"):
+                step(L, dict(t, h=-t["h"], **miss), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(L.idx, idx)
+    # nothing was queued, so the training step is still the layer's last one
+    assert torch.equal(L.backward(*args, t["s13"], t["s2"]).h, held["h"])

@@ -63,8 +63,9 @@ template <> struct Elem<uint16_t> {
   static __device__ __forceinline__ void store(uint16_t* p, size_t i, float v) { p[i] = f32_to_bf16(v); }
 };
 
-// SiLU(z) = z / (1 + e^-z) with the hardware exponential and reciprocal (each
-// within about one ulp); the IEEE division sequence would cost ten instructions.
+// SiLU(z) = z / (1 + e^-z) with the hardware exponential (off by about |z| 2^-24
+// of itself, from the rounding of its base-2 exponent) and reciprocal (one ulp);
+// the IEEE division sequence would cost ten instructions.
 __device__ __forceinline__ float silu_f32(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // ---------------------------------------------------------------- wave helpers

@@ -1,0 +1,463 @@
+"""Cases of the MoE layer's scored router and of its experts in microscaled 4-bit floating point.
+
+Five operators: the router's logits (current and lookahead router), the routing
+rule on them (softmax or sigmoid scores, a bias for balance, groups of experts,
+top-k, renormalised weights), the router's gradient, the quantisation to MX
+4-bit floating point with its reading back, and the gated FFN of ragged expert
+groups with tokens, activations and weights in that format.  ``own`` false: the
+operators written out in elementary torch operations.  ``own`` true: the calls
+of libmoelb.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+EPS = 1e-20  # beside the sum of renormalised weights
+
+
+# ---------------------------------------------------------------- cases
+
+
+def listed():
+    return [
+        # one token of one request, both routers: all of it launch latency
+        dict(name="logits one token", op="logits", dtype="bf16", T=1, d=4096, E=128, both=True),
+        # a prefill batch, both routers (Qwen3-235B shape)
+        dict(name="logits prefill", op="logits", dtype="bf16", T=32768, d=4096, E=128, both=True),
+        # a decode batch: softmax, renormalised (Qwen3-30B shape)
+        dict(name="route decode", op="route", T=512, E=128, k=8, score="softmax", bias=False, groups=1,
+             topk_groups=1, group_top=1, renorm=True, scale=1.0, masked=0.0),
+        # a prefill batch: sigmoid scores, balance bias, the best 4 of 8 groups
+        dict(name="route prefill groups", op="route", T=32768, E=256, k=8, score="sigmoid", bias=True, groups=8,
+             topk_groups=4, group_top=2, renorm=True, scale=2.5, masked=0.0),
+        # sizes off every lane count, experts switched off, padding tokens with every logit masked
+        dict(name="route ragged masked", op="route", T=1111, E=60, k=4, score="sigmoid", bias=True, groups=1,
+             topk_groups=1, group_top=1, renorm=True, scale=1.0, masked=0.05),
+        # the tiny fp32 configuration's router, and a training batch's
+        dict(name="route gradient tiny f32", op="gradient", dtype="f32", T=256, d=256, E=16, k=2, score="softmax",
+             renorm=True, scale=1.0),
+        dict(name="route gradient prefill", op="gradient", dtype="bf16", T=32768, d=4096, E=128, k=8,
+             score="sigmoid", renorm=True, scale=2.5),
+        # a decode batch's hidden states, and one expert matrix stack at load time
+        dict(name="mx4 hidden states", op="quantize", dtype="bf16", rows=512, K=2048),
+        dict(name="mx4 weights", op="quantize", dtype="bf16", rows=131072, K=2048),
+        # one token: eight experts' weights are read for it (Qwen3-30B shape)
+        dict(name="mx4 ffn one token", op="ffn", T=1, k=8, E=128, d=2048, inter=768),
+        # a decode batch: every expert's weights for a few rows each
+        dict(name="mx4 ffn decode", op="ffn", T=512, k=8, E=128, d=2048, inter=768),
+        # a prefill batch (OLMoE shape)
+        dict(name="mx4 ffn prefill", op="ffn", T=16384, k=8, E=64, d=2048, inter=1024),
+    ]
+
+
+def _log_int(rng, lo, hi, step=1):
+    v = math.exp(rng.uniform(math.log(lo), math.log(hi)))
+    return max(lo, int(round(v / step)) * step)
+
+
+def draw(rng):
+    op = rng.choice(["logits", "route", "route", "gradient", "quantize", "ffn", "ffn", "ffn"])
+    dtype = "f32" if rng.random() < 0.2 else "bf16"
+    E = rng.choice([8, 16, 60, 64, 96, 128, 160, 192, 256])
+    if op == "logits":
+        T = _log_int(rng, 1, 32768 if dtype == "bf16" else 4096)
+        return dict(op=op, dtype=dtype, T=T, d=_log_int(rng, 64, 4096, 8), E=min(E, 128),
+                    both=rng.random() < 0.5)
+    if op == "route":
+        groups = rng.choice([1, 1] + [g for g in (2, 4, 8, 16) if E % g == 0])
+        topk_groups = rng.randint(1, groups)
+        bias = rng.random() < 0.6
+        return dict(op=op, T=_log_int(rng, 1, 32768), E=E, k=rng.randint(1, min(16, topk_groups * (E // groups))),
+                    score=rng.choice(["softmax", "sigmoid"]), bias=bias, groups=groups, topk_groups=topk_groups,
+                    group_top=rng.choice([1, min(2, E // groups)]), renorm=rng.random() < 0.7,
+                    scale=rng.choice([1.0, 2.5]), masked=rng.choice([0.0, 0.0, 0.05]))
+    if op == "gradient":
+        E = min(E, 128)
+        k = rng.randint(1, min(8, E))
+        return dict(op=op, dtype=dtype, T=_log_int(rng, 16, 32768 if dtype == "bf16" else 4096),
+                    d=_log_int(rng, 64, 4096, 8), E=E, k=k, score=rng.choice(["softmax", "sigmoid"]),
+                    renorm=k > 1 and rng.random() < 0.6, scale=rng.choice([1.0, 2.5]))  # one renormalised weight is 1
+    if op == "quantize":
+        while True:
+            c = dict(op=op, dtype=dtype, rows=_log_int(rng, 1, 131072), K=_log_int(rng, 32, 8192, 32))
+            if c["rows"] * c["K"] <= (2 ** 28 if dtype == "bf16" else 2 ** 26):
+                return c
+    while True:
+        E = rng.choice([1, 1, 8, 16, 24, 64, 128])
+        c = dict(op=op, T=_log_int(rng, 1, 16384), k=1 if E == 1 else rng.randint(1, 8), E=E,
+                 d=_log_int(rng, 64, 4096, 32), inter=_log_int(rng, 64, 4096, 32))
+        if work(c)["flops"] <= 1.6e12 and E * c["d"] * c["inter"] <= 2 ** 28:
+            return c
+
+
+def work(case):
+    c = case
+    eb = 4 if c.get("dtype") == "f32" else 2
+    if c["op"] == "logits":
+        T, d, n = c["T"], c["d"], c["E"] * (2 if c["both"] else 1)
+        return dict(bytes=(T * d + n * d) * eb + T * n * 4, flops=2 * T * d * n)
+    if c["op"] == "route":
+        return dict(bytes=c["T"] * c["E"] * 4 + c["T"] * c["k"] * 8, flops=8 * c["T"] * c["E"])
+    if c["op"] == "gradient":
+        T, d, E, k = c["T"], c["d"], c["E"], c["k"]
+        return dict(bytes=(2 * T * d + 2 * E * d) * eb + T * E * 4 + 2 * T * k * 4 + E * 4, flops=4 * T * d * E)
+    if c["op"] == "quantize":
+        n = c["rows"] * c["K"]
+        return dict(bytes=2 * n * eb + n * 17 // 32, flops=8 * n)
+    P, d, i = c["T"] * c["k"], c["d"], c["inter"]
+    return dict(bytes=(c["T"] + P) * d * 2 + min(c["E"], P) * 3 * i * d * 17 // 32, flops=6 * P * d * i)
+
+
+# ---------------------------------------------------------------- the format
+
+
+def _mx4(x):
+    """(codes 0..15, exponent of each block of 32 along the last dimension)."""
+    b = x.reshape(*x.shape[:-1], -1, 32)
+    amax = b.abs().amax(-1, keepdim=True)
+    exp = (torch.frexp(amax).exponent - 3).clamp(-127, 127)
+    exp = torch.where(amax == 0, torch.full_like(exp, -127), exp)
+    a = torch.ldexp(b, -exp).abs()
+    code = ((a > 0.25).byte() + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
+    code = code + 8 * (b < 0)
+    return code.byte().reshape(x.shape), exp.squeeze(-1)
+
+
+def _values(code, exp, dtype):
+    """What codes and exponents stand for."""
+    table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0],
+                         dtype=dtype, device=code.device)
+    v = table[code.long()].view(*exp.shape, 32)
+    return torch.ldexp(v, exp.unsqueeze(-1)).reshape(code.shape)
+
+
+def _round4(x):
+    code, exp = _mx4(x)
+    return _values(code, exp, x.dtype)
+
+
+def _pack(code, exp):
+    """Two codes a byte, the even element low; one scale byte a block, rows of a multiple of 16 bytes."""
+    q = code[..., 0::2] | (code[..., 1::2] << 4)
+    blocks = exp.shape[-1]
+    scales = torch.zeros((*exp.shape[:-1], (blocks + 15) // 16 * 16), dtype=torch.uint8, device=code.device)
+    scales[..., :blocks] = (exp + 127).byte()
+    return q.contiguous(), scales
+
+
+def _unpack(q, scales):
+    code = torch.stack([q & 15, q >> 4], -1).reshape(*q.shape[:-1], q.shape[-1] * 2)
+    return code, scales[..., :code.shape[-1] // 32].int() - 127
+
+
+# ---------------------------------------------------------------- inputs
+
+
+def _normal(gen, shape, scale, dtype):
+    return (torch.randn(shape, generator=gen, device="cuda") * scale).to(dtype)
+
+
+def _logits(gen, T, E):
+    """Logits of a trained router: popular experts are offset from the others."""
+    rank = torch.randperm(E, generator=gen, device="cuda") + 1
+    return torch.randn((T, E), generator=gen, device="cuda") - 0.5 * torch.log(rank.float())
+
+
+def prepare(case, seed):
+    c, dev = case, "cuda"
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    dt = DTYPES[c.get("dtype", "bf16")]
+    s = dict(case=c)
+    if c["op"] == "logits":
+        T, d, E = c["T"], c["d"], c["E"]
+        s["h"] = _normal(gen, (T, d), 1.0, dt)
+        for n in ("cur", "next"):
+            s["w_" + n] = _normal(gen, (E, d), 1.0 / math.sqrt(d), dt)
+            s["b_" + n] = _normal(gen, (E,), 0.5, torch.float32)
+    elif c["op"] == "route":
+        T, E = c["T"], c["E"]
+        s["z"] = _logits(gen, T, E)
+        s["bias"] = _normal(gen, (E,), 0.05, torch.float32) if c["bias"] else None
+        if c["masked"]:
+            # experts that are switched off, and padding tokens
+            off = torch.rand((E,), generator=gen, device=dev) < c["masked"]
+            pad = torch.rand((T,), generator=gen, device=dev) < c["masked"]
+            s["z"] = s["z"].masked_fill(off[None, :] | pad[:, None], -math.inf)
+    elif c["op"] == "gradient":
+        T, d, E, k = c["T"], c["d"], c["E"], c["k"]
+        s["h"] = _normal(gen, (T, d), 1.0, dt)
+        s["w"] = _normal(gen, (E, d), 1.0 / math.sqrt(d), dt)
+        s["z"] = s["h"].float() @ s["w"].float().t()
+        s["idx"] = torch.sort(s["z"], dim=1, descending=True, stable=True).indices[:, :k].to(torch.int32).contiguous()
+        s["dwts"] = _normal(gen, (T, k), 1.0, torch.float32)
+    elif c["op"] == "quantize":
+        # rows of different magnitudes, a few values far out
+        x = torch.randn((c["rows"], c["K"]), generator=gen, device=dev)
+        x *= torch.exp(0.5 * torch.randn((c["rows"], 1), generator=gen, device=dev))
+        far = torch.rand(x.shape, generator=gen, device=dev) < 0.001
+        s["x"] = torch.where(far, 20 * x, x).to(dt)
+    else:
+        T, k, E, d, i = c["T"], c["k"], c["E"], c["d"], c["inter"]
+        P = T * k
+        s["x"] = _normal(gen, (T, d), 1.0, dt)
+        # weights as they are kept: quantised when they were loaded
+        s["w13"], s["s13"] = _pack(*_mx4(_normal(gen, (E, 2 * i, d), 0.02, dt).float()))
+        s["w2"], s["s2"] = _pack(*_mx4(_normal(gen, (E, d, i), 0.02, dt).float()))
+        # k distinct experts per token over uneven popularities, the pairs sorted by expert
+        pop = 0.3 * torch.randn((E,), generator=gen, device=dev)
+        u = torch.rand((T, E), generator=gen, device=dev).clamp(1e-6, 1.0 - 1e-6)
+        flat = torch.sort(pop - torch.log(-torch.log(u)), dim=1, descending=True).indices[:, :k].reshape(-1)
+        counts = torch.bincount(flat, minlength=E)
+        s["gather"] = torch.argsort(flat, stable=True).to(torch.int32)
+        s["group_off"] = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+        s["rows"], s["cap"] = P, int(counts.max())  # the plan's longest group
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+
+def _plain_logits(s):
+    h = s["h"].float()
+    out = dict(z=h @ s["w_cur"].float().t() + s["b_cur"])
+    if s["case"]["both"]:
+        out["z_next"] = h @ s["w_next"].float().t() + s["b_next"]
+    return out
+
+
+def _scores(z, score):
+    """Scores of logits, 0 where an expert is masked."""
+    on = z > -math.inf
+    if score == "sigmoid":
+        return on / (1 + torch.exp(-z))
+    top = z.amax(1, keepdim=True)
+    e = torch.where(on, torch.exp(z - torch.where(top > -math.inf, top, torch.zeros_like(top))), torch.zeros_like(z))
+    return e / e.sum(1, keepdim=True).clamp_min(1e-300)
+
+
+def _plain_route(s):
+    c = s["case"]
+    # in 64 bits: the picks turn on the last bits of scores next to each other
+    z = s["z"].double()
+    T, E, k, g = c["T"], c["E"], c["k"], c["groups"]
+    p = _scores(z, c["score"])
+    sel = p if s["bias"] is None else p + s["bias"].double()
+    sel = torch.where(z > -math.inf, sel, torch.full_like(sel, -math.inf))
+    if g > 1:
+        top = torch.sort(sel.view(T, g, E // g), dim=2, descending=True).values[:, :, :c["group_top"]].sum(2)
+        order = torch.sort(top, dim=1, descending=True, stable=True).indices[:, :c["topk_groups"]]
+        keep = torch.zeros_like(top).scatter_(1, order, 1.0).repeat_interleave(E // g, dim=1)
+        sel = torch.where(keep > 0, sel, torch.full_like(sel, -math.inf))
+    order = torch.sort(sel, dim=1, descending=True, stable=True)
+    idx = order.indices[:, :k]
+    picked = order.values[:, :k] > -math.inf
+    w = p.gather(1, idx) * picked
+    if c["renorm"]:
+        w = w / (w.sum(1, keepdim=True) + EPS)
+    return dict(idx=torch.where(picked, idx, torch.full_like(idx, -1)).to(torch.int32), wts=(w * c["scale"]).float())
+
+
+def _plain_gradient(s):
+    c, dt = s["case"], DTYPES[s["case"]["dtype"]]
+    p = _scores(s["z"], c["score"])
+    idx, q = s["idx"].long(), s["dwts"] * c["scale"]
+    w = p.gather(1, idx)
+    if c["renorm"]:
+        total = w.sum(1, keepdim=True) + EPS
+        q = (q - (q * w).sum(1, keepdim=True) / total) / total
+    if c["score"] == "sigmoid":
+        dz = torch.zeros_like(p).scatter_add_(1, idx, q * w / (1 + torch.exp(s["z"].gather(1, idx))))
+    else:
+        full = torch.zeros_like(p).scatter_add_(1, idx, q)
+        dz = p * (full - (p * full).sum(1, keepdim=True))
+    return dict(dh=(dz @ s["w"].float()).to(dt), dw=(dz.t() @ s["h"].float()).to(dt), db=dz.sum(0))
+
+
+def _plain_quantize(s):
+    return dict(x=_round4(s["x"].float()).to(s["x"].dtype))
+
+
+def _plain_ffn(s):
+    c = s["case"]
+    i, cap, P = c["inter"], s["cap"], s["rows"]
+    off = s["group_off"].long()
+    row = torch.arange(P, device=off.device)
+    e = torch.searchsorted(off, row, right=True) - 1  # a row's expert
+    r = (off[:-1, None] + torch.arange(cap, device=off.device)).clamp(max=P - 1)  # rows, each expert's padded
+    x = _round4(s["x"].float())[s["gather"].long()[r] // c["k"]]
+    w13 = _values(*_unpack(s["w13"], s["s13"]), torch.float32)
+    w2 = _values(*_unpack(s["w2"], s["s2"]), torch.float32)
+    z = torch.matmul(x, w13.transpose(1, 2))
+    g, u = z[..., :i], z[..., i:]
+    a = _round4(g / (1 + torch.exp(-g)) * u)
+    y = torch.matmul(a, w2.transpose(1, 2))
+    return dict(y=y[e, row - off[e]].to(torch.bfloat16))
+
+
+# ---------------------------------------------------------------- the framework's calls
+
+
+def _bytes(n):
+    return torch.empty((max(1, n),), dtype=torch.uint8, device="cuda")
+
+
+def _own_buffers(s):
+    """Outputs and workspaces, allocated once per layer as MoELayer does."""
+    from routed_expert_ffn_gate_amd import moelb as M
+    c = s["case"]
+    code = M.MOELB_F32 if c.get("dtype") == "f32" else M.MOELB_BF16
+    f = dict(dtype=torch.float32, device="cuda")
+    if c["op"] == "logits":
+        s["out"] = dict(z=torch.empty((c["T"], c["E"]), **f))
+        if c["both"]:
+            s["out"]["z_next"] = torch.empty((c["T"], c["E"]), **f)
+    elif c["op"] == "route":
+        s["out"] = dict(idx=torch.empty((c["T"], c["k"]), dtype=torch.int32, device="cuda"),
+                        wts=torch.empty((c["T"], c["k"]), **f))
+    elif c["op"] == "gradient":
+        s["out"] = dict(dh=torch.empty_like(s["h"]), dw=torch.empty_like(s["w"]), db=torch.empty((c["E"],), **f))
+        s["ws"] = _bytes(M.moelb_route_backward_workspace_bytes(c["T"], c["d"], c["E"], code))
+    elif c["op"] == "quantize":
+        s["q"] = torch.empty((c["rows"], c["K"] // 2), dtype=torch.uint8, device="cuda")
+        s["scales"] = torch.empty((c["rows"], M.moelb_mx4_scale_bytes(c["K"])), dtype=torch.uint8, device="cuda")
+        s["out"] = dict(x=torch.empty_like(s["x"]))
+    else:
+        s["out"] = dict(y=torch.empty((s["rows"], c["d"]), dtype=torch.bfloat16, device="cuda"))
+        s["ws"] = _bytes(M.moelb_mx4_grouped_ffn_workspace_bytes(c["T"], s["rows"], c["E"], c["E"], c["d"],
+                                                                 c["inter"]))
+    if "score" in c:
+        s["score"] = M.MOELB_SCORE_SIGMOID if c["score"] == "sigmoid" else M.MOELB_SCORE_SOFTMAX
+    s["M"] = M
+
+
+def _own(s):
+    if "M" not in s:
+        _own_buffers(s)
+    M, c, o = s["M"], s["case"], s["out"]
+    if c["op"] == "logits":
+        M.moelb_gate_logits(s["h"], s["w_cur"], s["b_cur"], s["w_next"] if c["both"] else None,
+                            s["b_next"] if c["both"] else None, o["z"], o.get("z_next"))
+    elif c["op"] == "route":
+        M.moelb_route(s["z"], o["idx"], o["wts"], score=s["score"], bias=s["bias"], groups=c["groups"],
+                      topk_groups=c["topk_groups"], group_top=c["group_top"], renorm=c["renorm"], scale=c["scale"])
+    elif c["op"] == "gradient":
+        M.moelb_route_backward(s["h"], s["w"], s["z"], s["idx"], s["dwts"], s["ws"], o["dh"], o["dw"], o["db"],
+                               score=s["score"], renorm=c["renorm"], scale=c["scale"])
+    elif c["op"] == "quantize":
+        M.moelb_mx4_quantize(s["x"], s["q"], s["scales"])
+        M.moelb_mx4_dequantize(s["q"], s["scales"], o["x"])
+    else:
+        M.moelb_mx4_grouped_ffn(s["x"], s["rows"], s["group_off"], c["E"], s["w13"], s["s13"], s["w2"], s["s2"],
+                                s["ws"], o["y"], gather=s["gather"], gather_k=c["k"])
+    return o
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"logits": _plain_logits, "route": _plain_route, "gradient": _plain_gradient, "quantize": _plain_quantize,
+            "ffn": _plain_ffn}[state["case"]["op"]](state)
+
+
+# ---------------------------------------------------------------- 64-bit values
+
+
+def _nearest4(v):
+    """The nearest of the format's sixteen values, by distance: ties to the even code."""
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=v.device)
+    a = v.abs().clamp(max=6.0)
+    hi = torch.searchsorted(grid, a).clamp(max=7)
+    lo = (hi - 1).clamp(min=0)
+    up, down = grid[hi] - a, a - grid[lo]
+    take_hi = (up < down) | ((up == down) & (hi % 2 == 0))
+    return torch.where(take_hi, grid[hi], grid[lo]) * torch.sign(v)
+
+
+def _exact4(x):
+    b = x.double().reshape(*x.shape[:-1], -1, 32)
+    top = b.abs().amax(-1, keepdim=True).clamp_min(2.0 ** -125)
+    e = torch.floor(torch.log2(top))
+    e = e + (torch.exp2(e + 1) <= top).double() - (torch.exp2(e) > top).double()  # log2 rounds near powers of two
+    scale = torch.exp2(e - 2)
+    return (_nearest4(b / scale) * scale).reshape(x.shape)
+
+
+def _exact_rows(w, scales, rows):
+    """Rows of a packed matrix as they stand."""
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=w.device)
+    w = w[rows].int()
+    both = torch.stack([w % 16, w // 16], -1).flatten(-2)
+    v = grid[(both % 8).long()] * (1 - 2 * (both // 8))
+    return v * torch.exp2(scales[rows].double() - 127).repeat_interleave(32, dim=-1)[..., :v.shape[-1]]
+
+
+def exact(case, seed):
+    s, c = prepare(case, seed), case
+    if c["op"] == "logits":
+        h = s["h"].double()
+        out = dict(z=torch.addmm(s["b_cur"].double(), h, s["w_cur"].double().t()))
+        if c["both"]:
+            out["z_next"] = torch.addmm(s["b_next"].double(), h, s["w_next"].double().t())
+        return out
+    if c["op"] in ("route", "gradient"):
+        z = s["z"].double()
+        off = z == -math.inf
+        if c["score"] == "sigmoid":
+            p = 0.5 * (1 + torch.tanh(0.5 * z.masked_fill(off, 0.0))).masked_fill(off, 0.0)
+        else:
+            p = torch.exp(z - torch.logsumexp(z, 1, keepdim=True)).masked_fill(off, 0.0)
+    if c["op"] == "route":
+        T, E, g = c["T"], c["E"], c["groups"]
+        size = E // g
+        key = p.clone() if s["bias"] is None else p + s["bias"].double()
+        key[off] = -math.inf
+        lane = torch.arange(E, device=z.device)
+        if g > 1:
+            best = key.view(T, g, size).clone()
+            mark = torch.zeros((T, g), dtype=torch.float64, device=z.device)
+            for _ in range(c["group_top"]):
+                mark += best.amax(2)
+                best.scatter_(2, best.argmax(2, keepdim=True), -math.inf)
+            kept = torch.zeros((T, g), dtype=torch.bool, device=z.device)
+            for _ in range(c["topk_groups"]):
+                top = mark.masked_fill(kept, -math.inf).amax(1, keepdim=True)
+                first = torch.where(~kept & (mark == top), torch.arange(g, device=z.device), g).amin(1, keepdim=True)
+                kept.scatter_(1, first, True)
+            key[~kept[:, lane // size]] = -math.inf
+        idx, w = [], []
+        for _ in range(c["k"]):
+            top = key.amax(1, keepdim=True)
+            first = torch.where(key == top, lane, E).amin(1, keepdim=True)
+            some = top > -math.inf
+            idx.append(torch.where(some, first, -1))
+            w.append(p.gather(1, first) * some)
+            key.scatter_(1, first, -math.inf)
+        w = torch.cat(w, 1)
+        if c["renorm"]:
+            w = w / (w.sum(1, keepdim=True) + EPS)
+        return dict(idx=torch.cat(idx, 1).to(torch.int32), wts=w * c["scale"])
+    if c["op"] == "gradient":
+        # the gradient of sum dwts w by differentiation
+        z = z.requires_grad_()
+        p = torch.sigmoid(z) if c["score"] == "sigmoid" else torch.softmax(z, 1)
+        w = p.gather(1, s["idx"].long())
+        if c["renorm"]:
+            w = w / (w.sum(1, keepdim=True) + EPS)
+        dz, = torch.autograd.grad((w * s["dwts"].double() * c["scale"]).sum(), z)
+        return dict(dh=dz @ s["w"].double(), dw=dz.t() @ s["h"].double(), db=dz.sum(0))
+    if c["op"] == "quantize":
+        return dict(x=_exact4(s["x"]))
+    ends, i = s["group_off"].tolist(), c["inter"]
+    src = s["gather"].long() // c["k"]
+    x = _exact4(s["x"])
+    y = torch.zeros((s["rows"], c["d"]), dtype=torch.float64, device=x.device)
+    for e in range(c["E"]):  # one expert after another
+        rows = slice(ends[e], ends[e + 1])
+        if ends[e] < ends[e + 1]:
+            g, u = (x[src[rows]] @ _exact_rows(s["w13"], s["s13"], e).t()).split(i, dim=1)
+            act = _exact4(0.5 * g * (1 + torch.tanh(0.5 * g)) * u)
+            y[rows] = act @ _exact_rows(s["w2"], s["s2"], e).t()
+    return dict(y=y)

@@ -322,11 +322,11 @@ def _own_buffers(s):
         s["ws"] = _bytes(M.moelb_route_backward_workspace_bytes(c["T"], c["d"], c["E"], code))
     elif c["op"] == "quantize":
         s["q"] = torch.empty((c["rows"], c["K"] // 2), dtype=torch.uint8, device="cuda")
-        s["scales"] = torch.empty((c["rows"], M.moelb_mx4_scale_bytes(c["K"])), dtype=torch.uint8, device="cuda")
+        s["scales"] = torch.empty((c["rows"], M.moelb_mx_scale_bytes(c["K"])), dtype=torch.uint8, device="cuda")
         s["out"] = dict(x=torch.empty_like(s["x"]))
     else:
         s["out"] = dict(y=torch.empty((s["rows"], c["d"]), dtype=torch.bfloat16, device="cuda"))
-        s["ws"] = _bytes(M.moelb_mx4_grouped_ffn_workspace_bytes(c["T"], s["rows"], c["E"], c["E"], c["d"],
+        s["ws"] = _bytes(M.moelb_mx_grouped_ffn_workspace_bytes(c["T"], s["rows"], c["E"], c["E"], c["d"],
                                                                  c["inter"]))
     if "score" in c:
         s["score"] = M.MOELB_SCORE_SIGMOID if c["score"] == "sigmoid" else M.MOELB_SCORE_SOFTMAX
@@ -347,10 +347,10 @@ def _own(s):
         M.moelb_route_backward(s["h"], s["w"], s["z"], s["idx"], s["dwts"], s["ws"], o["dh"], o["dw"], o["db"],
                                score=s["score"], renorm=c["renorm"], scale=c["scale"])
     elif c["op"] == "quantize":
-        M.moelb_mx4_quantize(s["x"], s["q"], s["scales"])
-        M.moelb_mx4_dequantize(s["q"], s["scales"], o["x"])
+        M.moelb_mx_quantize(s["x"], s["q"], s["scales"])
+        M.moelb_mx_dequantize(s["q"], s["scales"], o["x"])
     else:
-        M.moelb_mx4_grouped_ffn(s["x"], s["rows"], s["group_off"], c["E"], s["w13"], s["s13"], s["w2"], s["s2"],
+        M.moelb_mx_grouped_ffn(s["x"], s["rows"], s["group_off"], c["E"], s["w13"], s["s13"], s["w2"], s["s2"],
                                 s["ws"], o["y"], gather=s["gather"], gather_k=c["k"])
     return o
 

@@ -28,6 +28,15 @@
  * For serving requests with adapters of their own: a shared projection with
  * low-rank adapters beside it (moelb_adapter_projection).
  *
+ * Routers with other rules than moelb_gate_topk's: the logits
+ * (moelb_gate_logits), the rule on them -- softmax or sigmoid scores, a bias
+ * for balance, groups of experts, renormalised weights -- (moelb_route) and its
+ * gradient (moelb_route_backward).
+ *
+ * Experts in microscaled 4-bit floating point: quantisation and reading back
+ * (moelb_mx_quantize, moelb_mx_dequantize) and the grouped FFN on tokens,
+ * activations and weights in that format (moelb_mx_grouped_ffn).
+ *
  * Conventions for every entry point:
  *  - Plain C ABI.  Every pointer argument is DEVICE memory owned by the caller
  *    (e.g. a PyTorch tensor's data pointer), unless stated otherwise; the
@@ -597,6 +606,141 @@ int moelb_adapter_projection(const void* x, int T, int d_in, int d_out, int dtyp
                              const int32_t* ids, const void* a, const void* b, const float* scale,
                              int n, int r, int gated, void* ws, size_t ws_bytes, void* y,
                              void* stream);
+
+/*
+ * Logits of the current router and of the lookahead router:
+ *   z[t,e] = h[t,:] . w_cur[e,:] + b_cur[e], z_next likewise with w_next, b_next
+ * with fp32 accumulation, kept in fp32.
+ *  h      [T,d]  dtype
+ *  w_cur  [E,d]  dtype;  b_cur  [E] fp32 or NULL (no bias)
+ *  w_next [E,d]  dtype or NULL (no lookahead: z_next must be NULL);
+ *  b_next [E]    fp32 or NULL
+ *  z      [T,E]  fp32 out;  z_next [T,E] fp32 out, NULL iff w_next is NULL
+ * Requires T >= 0, E <= 256, d % 8 == 0, d <= 2^25, E*d elements below
+ * 2^32 - 2^21 bytes; h, w_cur and w_next 16-byte aligned.
+ */
+int moelb_gate_logits(const void* h, int T, int d, int E, int dtype, const void* w_cur,
+                      const float* b_cur, const void* w_next, const float* b_next, float* z,
+                      float* z_next, void* stream);
+
+enum moelb_score {
+  MOELB_SCORE_SOFTMAX = 0, /* s_e = exp(z_e) / sum_f exp(z_f), over all E       */
+  MOELB_SCORE_SIGMOID = 1  /* s_e = 1 / (1 + exp(-z_e))                         */
+};
+
+/*
+ * Routing rule on logits.  Per token t, with s the scores of z[t,:]:
+ *   c_e = s_e + bias[e]      what the picks go by (bias NULL: s_e, in the order
+ *                            of the logits)
+ *   groups > 1: the E experts are `groups` groups of E / groups neighbours; a
+ *     group's score is the sum of its group_top largest c; only the experts of
+ *     the topk_groups groups with the largest scores can be picked (ties: lower
+ *     group)
+ *   idx[t,:] = the k experts with the largest c, by descending c, ties to the
+ *              lower id
+ *   wts[t,j] = scale * s_idx[t,j]; renorm: scale * s_idx[t,j] / (sum + 1e-20),
+ *              sum that of the token's picked s (the bias is not in the weights)
+ *   gap[t]   = c_(k) - c_(k+1) among the experts that can be picked, +inf if
+ *              there are no k + 1
+ * An expert whose logit is -inf or NaN is masked: its score is 0 and it is never
+ * picked; nor is one whose bias is -inf or NaN.  Where fewer than k experts are
+ * left, the last entries are idx -1 and wts 0 (pairs that the histogram, the
+ * permutation and the combine leave out); a token whose logits are all masked has
+ * only those.  A group's score counts a masked expert as -inf.  Logits of +inf are
+ * taken as the largest float, and so is a c above it.
+ * The picks are those of exact arithmetic on the given logits and bias: scores that
+ * are near each other in fp32 are compared in 64 bits.  wts and gap are fp32.
+ *  z    [T,E] fp32, bias [E] fp32 or NULL
+ *  idx  [T,k] int32 out; wts [T,k] fp32 out or NULL; gap [T] fp32 out or NULL
+ * Requires T >= 0, 1 <= k <= min(E, 16), E <= 256, groups >= 1 dividing E,
+ * 1 <= topk_groups <= groups, topk_groups * (E / groups) >= k, group_top 1 or 2 and
+ * at most E / groups, scale finite.
+ */
+int moelb_route(const float* z, int T, int E, int k, int score, const float* bias, int groups,
+                int topk_groups, int group_top, int renorm, float scale, int32_t* idx, float* wts,
+                float* gap, void* stream);
+
+/*
+ * Gradients of a router through moelb_gate_logits and moelb_route, for dwts the
+ * gradient of the route's wts (idx, gap and the route's bias have none).  With s
+ * the scores of z, S = 1e-20 + the sum of s over the token's picks j:
+ *   ds_j = scale * dwts_j;  renorm: scale * (dwts_j - sum_i dwts_i s_i / S) / S
+ *   softmax: dz_e = s_e (sum of ds_j with idx_j = e, less sum_j s_j ds_j)
+ *   sigmoid: dz_e = (sum of ds_j with idx_j = e) s_e (1 - s_e)
+ *   dh[t] = dz . w, dw[e] = sum_t dz_e h[t], db[e] = sum_t dz_e
+ * dh and dw are rounded to dtype once, and so is dz as the operand of their
+ * products; db is summed from the fp32 dz.  Results do not depend on the order of
+ * execution.
+ *  h [T,d], w [E,d] dtype; z [T,E] fp32, idx [T,k] int32: the forward's; dwts [T,k] fp32
+ *  ws   workspace of moelb_route_backward_workspace_bytes(...) bytes; calls that may
+ *       run at the same time need one each
+ *  dh   [T,d] dtype out or NULL;  dw [E,d] dtype out or NULL;  db [E] fp32 out or
+ *       NULL (T = 0: dw and db are zero)
+ * Ids outside [0,E) are left out; an id listed twice counts twice.  Masked logits
+ * have dz 0.
+ * Requires what moelb_gate_backward requires, and scale finite.
+ */
+size_t moelb_route_backward_workspace_bytes(int T, int d, int E, int dtype);
+int moelb_route_backward(const void* h, int T, int d, int E, int k, int dtype, const void* w,
+                         const float* z, const int32_t* idx, const float* dwts, int score,
+                         int renorm, float scale, void* ws, size_t ws_bytes, void* dh, void* dw,
+                         float* db, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (OCP MX, "MXFP4"): each block of 32 neighbours
+ * of a row shares a power of two 2^X, and an element is a 4-bit e2m1 number (sign,
+ * 0, 0.5, 1, 1.5, 2, 3, 4 or 6) times it.
+ *   X = floor(log2(max |x| of the block)) - 2, in [-127, 127] (a block of zeros: -127)
+ *   code = x / 2^X to the nearest of the sixteen numbers, ties to the even code,
+ *          beyond 6 to 6
+ * A block with an infinity or a NaN becomes NaN as a whole (scale byte 255).
+ *  x      [rows,K]   dtype
+ *  q      [rows,K/2] out: element k in the low (k even) or high half of byte k / 2
+ *  scales [rows,moelb_mx_scale_bytes(K)] out: byte b is X + 127 of block b, the
+ *         bytes past K / 32 are zero
+ * moelb_mx_scale_bytes(K): K / 32 rounded up to a multiple of 16 (0 for K that the
+ * calls refuse).  moelb_mx_dequantize writes what codes and scales stand for,
+ * rounded to dtype (bf16 holds every such value up to 2^128 exactly).
+ * Requires rows >= 0, K >= 32, K % 32 == 0; x, q and scales 16-byte aligned.
+ * Outputs must not overlap the inputs.
+ */
+int moelb_mx_scale_bytes(int K);
+int moelb_mx_quantize(const void* x, long long rows, int K, int dtype, uint8_t* q, uint8_t* scales,
+                       void* stream);
+int moelb_mx_dequantize(const uint8_t* q, const uint8_t* scales, long long rows, int K, int dtype,
+                         void* x, void* stream);
+
+/*
+ * The grouped FFN with tokens, activations and weights in MX 4-bit floating point.
+ * Groups, rows, gather, rank and the clamping of device offsets are
+ * moelb_grouped_ffn's.  For each computed row, mx() being moelb_mx_quantize's
+ * rounding along the row:
+ *   a = mx(SiLU(mx(x_q) . W13[e, 0:I]^T) * (mx(x_q) . W13[e, I:2I]^T))
+ *   y[q] = a . W2[e]^T                                       (rounded to dtype)
+ * with fp32 accumulation; a is formed in fp32 and rounded once, to the format.
+ *  x          [rows_x,d]  dtype: quantised by the call
+ *  w13        [E,2*inter,d/2], w13_scales [E,2*inter,moelb_mx_scale_bytes(d)]
+ *  w2         [E,d,inter/2],   w2_scales  [E,d,moelb_mx_scale_bytes(inter)]
+ *             gate rows then up rows, as moelb_mx_quantize lays them out (the scale
+ *             bytes past the blocks must not be 255)
+ *  ws         workspace of moelb_mx_grouped_ffn_workspace_bytes(...) bytes (no
+ *             initial contents needed); calls that may run at the same time need
+ *             one each
+ *  y          [rows,d]    dtype out: rows outside every computed group are not
+ *             written
+ * Requires rows >= 0, rows_x >= 1 when rows > 0, d % 32 == 0, inter % 32 == 0, both
+ * up to 2^19, E <= 256, num_groups % E == 0 when rank >= 0, num_groups <= 32768, and
+ * rows_x*d/2, rows*inter/2, inter*d and rows*d*4 bytes each below 2^32 - 2^21; x, the
+ * weights, their scales, ws and y 16-byte aligned.  The workspace's size is 0 for
+ * counts and widths that the call refuses.
+ */
+size_t moelb_mx_grouped_ffn_workspace_bytes(int rows_x, int rows, int num_groups, int E, int d,
+                                             int inter);
+int moelb_mx_grouped_ffn(const void* x, int rows_x, int rows, const int32_t* group_off,
+                          int num_groups, int E, int G, int rank, const int32_t* gather,
+                          int gather_k, int d, int inter, int dtype, const uint8_t* w13,
+                          const uint8_t* w13_scales, const uint8_t* w2, const uint8_t* w2_scales,
+                          void* ws, size_t ws_bytes, void* y, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,5 @@
-// Gradients of the softmax router.
+// Gradients of the softmax router, and of a router with another rule
+// (moelb_route_backward, at the end: its dz, then the same products).
 //
 // Definition (FreeBalance, "FreeBalance: Pre-Routing Online MoE Load Balancing
 // via Residual Workload Prediction", section 2.1 and eq. 4; the forward is
@@ -25,6 +26,9 @@
 // launch of 135 us, 5 in 6 us.  Beyond 128 experts z and dz go through memory and
 // W takes two buffers: E = 160 372 us, E = 256 386 (the call).  Small calls: three
 // launches (T = 256, d = 256, E = 16, fp32: 10, 8 and 2 us).
+#include <float.h>
+#include <math.h>
+
 #include "mfma_tile.h"
 
 namespace {
@@ -311,6 +315,101 @@ __global__ __launch_bounds__(MOELB_WAVE * ROW_WAVES) void gate_softmax_backward_
     p.pdb[(size_t)blockIdx.x * p.Ep + e] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
 }
 
+// ---- the gradient of moelb_route's weights: dz from the kept logits
+//
+// With q_j the gradient of pick j's weight, s the scores and S = 1e-20 + the
+// picks' sum of s:
+//   ds_j = scale q_j, or scale (q_j - A / S) / S with A = sum_i q_i s_i (renorm)
+//   sigmoid: dz = ds s (1 - s) at the picks; softmax: dz_e = s_e (ds_e - C), C =
+//   sum_j s_j ds_j.  renorm: C = scale A 1e-20 / S^2, without the cancellation
+//   of two sums that are equal but for the 1e-20.
+// Lane l of a wave holds experts l, l + 64, ... of its token, and pick l.
+struct RouteRule {
+  const float* z;  // [T][E]
+  int sigmoid, renorm;
+  float scale;
+};
+
+template <typename T, int NE>
+__global__ __launch_bounds__(MOELB_WAVE * ROW_WAVES) void route_dz_kernel(GateArgs<T> p, RouteRule u) {
+  __shared__ float part[ROW_WAVES][NE * MOELB_WAVE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (p.Ttok + p.blocks - 1) / p.blocks;
+  const int t0 = blockIdx.x * per, t1 = min(p.Ttok, t0 + per);
+  float db[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) db[i] = 0.f;
+  for (int t = t0 + wave; t < t1; t += ROW_WAVES) {
+    const float* zr = u.z + (size_t)t * p.E;
+    int id = lane < p.k ? p.idx[(size_t)t * p.k + lane] : -1;
+    if (id < 0 || id >= p.E) id = -1;
+    const float q = id >= 0 ? p.dwts[(size_t)t * p.k + lane] : 0.f;
+    float zj = id >= 0 ? zr[id] : -INFINITY;
+    const bool on = zj > -INFINITY;  // neither -inf nor NaN
+    zj = on ? fminf(zj, FLT_MAX) : -INFINITY;
+    float s[NE];    // softmax: the scores of this lane's experts
+    float sj, cj;   // the pick's score, and 1 - s (sigmoid)
+    if (u.sigmoid) {
+      const float ex = expf(-fabsf(zj)), r = 1.0f / (1.0f + ex);
+      sj = on ? (zj >= 0.f ? r : ex * r) : 0.f;
+      cj = zj >= 0.f ? ex * r : r;
+    } else {
+      float m = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int e = lane + i * MOELB_WAVE;
+        const float v = e < p.E ? zr[e] : -INFINITY;
+        s[i] = v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY;
+        m = fmaxf(m, s[i]);
+      }
+      m = wave_max(m);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        s[i] = s[i] > -INFINITY ? expf(s[i] - m) : 0.f;
+        sum += s[i];
+      }
+      sum = wave_sum(sum);
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;  // 0: every logit is masked
+#pragma unroll
+      for (int i = 0; i < NE; ++i) s[i] *= inv;
+      sj = on ? expf(zj - m) * inv : 0.f;
+      cj = 0.f;
+    }
+    const float A = wave_sum(q * sj);
+    float ds = u.scale * q, C = u.scale * A;
+    if (u.renorm) {
+      const float S = wave_sum(sj) + 1e-20f;
+      ds = u.scale * (q - A / S) / S;
+      C = u.scale * (A / S) * (1e-20f / S);
+    }
+    if (id < 0) ds = 0.f;
+    const float dj = ds * sj * cj;  // sigmoid: the pick's share of dz
+    float dz[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) dz[i] = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+      const int e = __builtin_amdgcn_readlane(id, j);
+      const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(u.sigmoid ? dj : ds), j));
+#pragma unroll
+      for (int i = 0; i < NE; ++i) dz[i] += e == lane + i * MOELB_WAVE ? v : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = lane + i * MOELB_WAVE;
+      if (!u.sigmoid) dz[i] = s[i] * (dz[i] - C);
+      db[i] += dz[i];
+      // rounded to the storage type: the matrix products below read it as an
+      // operand, beside h and w of that type
+      if (e < p.Ep) Elem<T>::store(p.dz, (size_t)t * p.Ep + e, dz[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) part[wave][lane + i * MOELB_WAVE] = db[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.Ep; e += MOELB_WAVE * ROW_WAVES)
+    p.pdb[(size_t)blockIdx.x * p.Ep + e] = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
+}
+
 // ---- 3: dh and dW
 
 template <typename T>
@@ -581,7 +680,7 @@ int launch_grads(GateArgs<uint16_t> p, hipStream_t s) {
   return MOELB_OK;
 }
 
-int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
+int run_dz(const GateArgs<uint16_t>& p, bool fused, hipStream_t s) {
   constexpr size_t lds = mt::lds_bytes<GF>();
   if (p.Ttok > 0 && fused) {
     if (!moelb_allow_lds(gate_dz_kernel, lds)) return MOELB_ELAUNCH;
@@ -597,6 +696,10 @@ int run(GateArgs<uint16_t> p, bool fused, hipStream_t s) {
     const int st = launch_softmax(p, s);
     if (st != MOELB_OK) return st;
   }
+  return MOELB_OK;
+}
+
+int run_grads(const GateArgs<uint16_t>& p, hipStream_t s) {
   switch (p.Ep / 64) {
     case 1:
       return launch_grads<1>(p, s);
@@ -624,7 +727,7 @@ bool launches_ok(const GateArgs<float>& p) {
 // d / 128 workgroups of 256 threads and less
 bool launches_ok(const GateArgs<uint16_t>&) { return true; }
 
-int run(GateArgs<float> p, bool fused, hipStream_t s) {
+int run_dz(const GateArgs<float>& p, bool fused, hipStream_t s) {
   if (fused) {
     hipLaunchKernelGGL(gate_dz_f32_kernel, dim3(p.blocks), dim3(mt::S_THREADS), 0, s, p);
     MOELB_CHECK_LAUNCH();
@@ -637,6 +740,10 @@ int run(GateArgs<float> p, bool fused, hipStream_t s) {
     const int st = launch_softmax(p, s);
     if (st != MOELB_OK) return st;
   }
+  return MOELB_OK;
+}
+
+int run_grads(GateArgs<float> p, hipStream_t s) {
   size_t nh, nw;
   grads_grid(p, nh, nw);
   p.nh = (int)nh;
@@ -647,9 +754,10 @@ int run(GateArgs<float> p, bool fused, hipStream_t s) {
   return MOELB_OK;
 }
 
+// The products from dz, and the sums over their parts.
 template <typename T>
-int run_all(const GateArgs<T>& p, bool fused, hipStream_t s) {
-  const int st = run(p, fused, s);
+int run_products(const GateArgs<T>& p, hipStream_t s) {
+  const int st = run_grads(p, s);
   if (st != MOELB_OK) return st;
   const int sw = p.dw && p.splits > 1 ? (int)(((size_t)p.E * p.d / 8 + 255) / 256) : 0;
   const int sb = p.db ? (p.E + 3) / 4 : 0;
@@ -658,6 +766,66 @@ int run_all(const GateArgs<T>& p, bool fused, hipStream_t s) {
     MOELB_CHECK_LAUNCH();
   }
   return MOELB_OK;
+}
+
+template <typename T>
+int run_all(const GateArgs<T>& p, bool fused, hipStream_t s) {
+  const int st = run_dz(p, fused, s);
+  return st != MOELB_OK ? st : run_products(p, s);
+}
+
+// moelb_route_backward: dz from the caller's logits, then the products.
+template <typename T>
+int run_route(const GateArgs<T>& p, const RouteRule& u, hipStream_t s) {
+  const dim3 grid(p.blocks), wg(MOELB_WAVE * ROW_WAVES);
+  switch (p.Ep / 64) {
+    case 1:
+      hipLaunchKernelGGL((route_dz_kernel<T, 1>), grid, wg, 0, s, p, u);
+      break;
+    case 2:
+      hipLaunchKernelGGL((route_dz_kernel<T, 2>), grid, wg, 0, s, p, u);
+      break;
+    case 3:
+      hipLaunchKernelGGL((route_dz_kernel<T, 3>), grid, wg, 0, s, p, u);
+      break;
+    default:
+      hipLaunchKernelGGL((route_dz_kernel<T, 4>), grid, wg, 0, s, p, u);
+  }
+  MOELB_CHECK_LAUNCH();
+  return run_products(p, s);
+}
+
+// The route's layout: as the softmax router's, without z, and dz by a token a
+// wave at any E.
+GateLayout route_layout(int T, int d, int E, int dtype) {
+  GateLayout l = gate_layout(T, d, E, dtype);
+  const int blocks = (T + 3) / 4;
+  l.blocks = blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks;
+  const size_t pdw = l.total - l.pdw;
+  l.dz = 0;
+  l.pdb = moelb_align256((size_t)T * l.Ep * moelb_elem_bytes(dtype));
+  l.pdw = l.pdb + moelb_align256((size_t)l.blocks * l.Ep * 4);
+  l.total = l.pdw + pdw;
+  return l;
+}
+
+// What both entry points require of sizes, operands and outputs.
+bool backward_args_ok(const void* h, int T, int d, int E, int k, int dtype, const void* w, const int32_t* idx,
+                      const float* dwts, const void* dh, const void* dw) {
+  if (T < 0 || d <= 0 || d % 8 != 0 || E < 1 || E > MOELB_MAX_E || k < 1 || k > E || k > MOELB_MAX_K ||
+      !moelb_dtype_ok(dtype))
+    return false;
+  if (!w || (T > 0 && (!h || !idx || !dwts))) return false;
+  if ((reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(dh) |
+       reinterpret_cast<uintptr_t>(dw)) & 15)
+    return false;
+  const size_t eb = moelb_elem_bytes(dtype);
+  // a column operand's 64 rows of a step, those past the last included, have
+  // 32-bit offsets
+  if (dtype == MOELB_BF16 && d > 1 << 25) return false;
+  // h, w and dz are operands of the tile
+  const size_t Ep = ((size_t)E + 63) / 64 * 64, most = mt::MAX_BYTES;
+  return (size_t)T * d * eb < most && (size_t)E * d * eb < most && (size_t)T * Ep * eb < most;
 }
 
 }  // namespace
@@ -670,20 +838,7 @@ extern "C" size_t moelb_gate_backward_workspace_bytes(int T, int d, int E, int d
 extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, int dtype, const void* w, const float* b,
                                    const int32_t* idx, const float* dwts, void* ws, size_t ws_bytes, void* dh,
                                    void* dw, float* db, void* stream) {
-  if (T < 0 || d <= 0 || d % 8 != 0 || E < 1 || E > MOELB_MAX_E || k < 1 || k > E || k > MOELB_MAX_K ||
-      !moelb_dtype_ok(dtype))
-    return MOELB_EINVAL;
-  if (!w || !b || (T > 0 && (!h || !idx || !dwts))) return MOELB_EINVAL;
-  if ((reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(dh) |
-       reinterpret_cast<uintptr_t>(dw)) & 15)
-    return MOELB_EINVAL;
-  const size_t eb = moelb_elem_bytes(dtype);
-  // a column operand's 64 rows of a step, those past the last included, have
-  // 32-bit offsets
-  if (dtype == MOELB_BF16 && d > 1 << 25) return MOELB_EINVAL;
-  // h, w and dz are operands of the tile
-  const size_t Ep = ((size_t)E + 63) / 64 * 64, most = mt::MAX_BYTES;
-  if ((size_t)T * d * eb >= most || (size_t)E * d * eb >= most || (size_t)T * Ep * eb >= most) return MOELB_EINVAL;
+  if (!backward_args_ok(h, T, d, E, k, dtype, w, idx, dwts, dh, dw) || !b) return MOELB_EINVAL;
   const GateLayout l = gate_layout(T, d, E, dtype);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < l.total) return MOELB_EWORKSPACE;
   if (!dh && !dw && !db) return MOELB_OK;
@@ -704,6 +859,41 @@ extern "C" int moelb_gate_backward(const void* h, int T, int d, int E, int k, in
     p.Ttok = T, p.d = d, p.E = E, p.Ep = l.Ep, p.k = k, p.splits = l.splits, p.blocks = l.blocks;
     if (!launches_ok(p)) return (int)MOELB_EINVAL;
     return run_all<U>(p, l.fused && T > 0, static_cast<hipStream_t>(stream));
+  };
+  return dtype == MOELB_BF16 ? go(static_cast<uint16_t*>(nullptr)) : go(static_cast<float*>(nullptr));
+}
+
+extern "C" size_t moelb_route_backward_workspace_bytes(int T, int d, int E, int dtype) {
+  if (T < 0 || d < 1 || E < 1 || E > MOELB_MAX_E || !moelb_dtype_ok(dtype)) return 0;
+  return route_layout(T, d, E, dtype).total;
+}
+
+extern "C" int moelb_route_backward(const void* h, int T, int d, int E, int k, int dtype, const void* w, const float* z,
+                                    const int32_t* idx, const float* dwts, int score, int renorm, float scale, void* ws,
+                                    size_t ws_bytes, void* dh, void* dw, float* db, void* stream) {
+  if (!backward_args_ok(h, T, d, E, k, dtype, w, idx, dwts, dh, dw) || (T > 0 && !z)) return MOELB_EINVAL;
+  if (score != MOELB_SCORE_SOFTMAX && score != MOELB_SCORE_SIGMOID) return MOELB_EINVAL;
+  if (!(fabsf(scale) <= FLT_MAX)) return MOELB_EINVAL;
+  const GateLayout l = route_layout(T, d, E, dtype);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < l.total) return MOELB_EWORKSPACE;
+  if (!dh && !dw && !db) return MOELB_OK;
+  char* base = static_cast<char*>(ws);
+  auto go = [&](auto* t) {
+    using U = std::remove_pointer_t<decltype(t)>;
+    GateArgs<U> p = {};
+    p.h = static_cast<const U*>(h);
+    p.w = static_cast<const U*>(w);
+    p.idx = idx, p.dwts = dwts;
+    p.dz = reinterpret_cast<U*>(base + l.dz);
+    p.pdb = reinterpret_cast<float*>(base + l.pdb);
+    p.pdw = reinterpret_cast<float*>(base + l.pdw);
+    p.dh = static_cast<U*>(dh);
+    p.dw = static_cast<U*>(dw);
+    p.db = db;
+    p.Ttok = T, p.d = d, p.E = E, p.Ep = l.Ep, p.k = k, p.splits = l.splits, p.blocks = l.blocks;
+    if (!launches_ok(p)) return (int)MOELB_EINVAL;
+    const RouteRule u = {z, score == MOELB_SCORE_SIGMOID, renorm != 0, scale};
+    return run_route<U>(p, u, static_cast<hipStream_t>(stream));
   };
   return dtype == MOELB_BF16 ? go(static_cast<uint16_t*>(nullptr)) : go(static_cast<float*>(nullptr));
 }

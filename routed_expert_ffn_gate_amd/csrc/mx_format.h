@@ -1,0 +1,41 @@
+// Microscaled 4-bit floating point (OCP MX): blocks of 32 e2m1 numbers with a
+// shared power of two 2^X, kept as the byte X + 127.
+#pragma once
+
+#include "common.h"
+
+namespace mx {
+
+constexpr int BLOCK = 32;
+
+// Bytes of a row's scales: one a block, padded so that every row starts on 16.
+__host__ __device__ inline int scale_bytes(int K) { return (K / BLOCK + 15) / 16 * 16; }
+
+// X + 127 of a block whose largest magnitude has these bits: X = floor(log2) - 2,
+// at least -127 (subnormals and zeros have exponent 0 here and end there too).
+// Infinities and NaN (integer order puts them last): 255, the format's NaN.
+__device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23);
+  return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+}
+// 2^-X, exact: X is in [-127, 125].  255: 0.
+__device__ __forceinline__ float inverse(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0u : (254u - byte) << 23);
+}
+// 2^X, X = -127 a subnormal.
+__device__ __forceinline__ float power(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Four values times inv to codes in 16 bits (HI: the upper half of `old`).  The
+// conversion rounds to nearest even; 6 is the largest number.
+template <bool HI>
+__device__ __forceinline__ uint32_t codes4(uint32_t old, float a, float b, float c, float d, float inv) {
+  auto s = [&](float x) { return __builtin_amdgcn_fmed3f(x * inv, -6.f, 6.f); };
+  old = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, s(a), s(b), 1.0f, HI ? 2 : 0);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, s(c), s(d), 1.0f, HI ? 3 : 1);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+}  // namespace mx

@@ -21,9 +21,11 @@ MOELB_OK, MOELB_EINVAL, MOELB_ELAUNCH, MOELB_EWORKSPACE = 0, 1, 2, 3
 MOELB_F32, MOELB_BF16 = 0, 1
 MOELB_FFN_SCHEDULE, MOELB_FFN_GATE_UP, MOELB_FFN_DOWN, MOELB_FFN_ALL = 1, 2, 4, 7
 MOELB_FFN_PACKED_WEIGHTS = 8
+MOELB_SCORE_SOFTMAX, MOELB_SCORE_SIGMOID = 0, 1
 
 # name -> (restype, argtypes)
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_LL, _F = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "moelb_version": (_I, []),
     "moelb_status_string": (ctypes.c_char_p, [_I]),
@@ -56,6 +58,16 @@ SIGNATURES = {
     "moelb_adapter_projection_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "moelb_adapter_projection": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P, _P]),
     "moelb_pack_weights": (_I, [_P, _I, _I, _I, _I, _P, _P]),
+    "moelb_gate_logits": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "moelb_route": (_I, [_P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
+    "moelb_route_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moelb_route_backward": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _F, _P, _SZ, _P, _P, _P, _P]),
+    "moelb_mx_scale_bytes": (_I, [_I]),
+    "moelb_mx_quantize": (_I, [_P, _LL, _I, _I, _P, _P, _P]),
+    "moelb_mx_dequantize": (_I, [_P, _P, _LL, _I, _I, _P, _P]),
+    "moelb_mx_grouped_ffn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moelb_mx_grouped_ffn": (_I, [_P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P,
+                                   _P]),
 }
 
 
@@ -433,3 +445,115 @@ def moelb_adapter_projection(x, w, ids, a, b, scale, ws, y, gated=False, stream=
                                           _arg(name, "scale", scale, (n,), torch.float32, dev), n, r, int(gated), pws,
                                           nws, _arg(name, "y", y, (T, d_out // 2 if gated else d_out), t, dev),
                                           _queue(stream, dev)), name)
+
+
+def moelb_gate_logits(h, w_cur, b_cur, w_next, b_next, z, z_next=None, stream=None):
+    """z [T, E] fp32 = h w_cur^T + b_cur, z_next with the lookahead router; a bias may be None."""
+    name = "moelb_gate_logits"
+    dev = _device(name, h)
+    T, d = h.shape
+    E = w_cur.shape[0]
+    t, f = h.dtype, torch.float32
+    _check(lib().moelb_gate_logits(_arg(name, "h", h, (T, d), t, dev), T, d, E, dtype_code(h),
+                                   _arg(name, "w_cur", w_cur, (E, d), t, dev), _arg(name, "b_cur", b_cur, (E,), f, dev),
+                                   _arg(name, "w_next", w_next, (E, d), t, dev),
+                                   _arg(name, "b_next", b_next, (E,), f, dev), _arg(name, "z", z, (T, E), f, dev),
+                                   _arg(name, "z_next", z_next, (T, E), f, dev), _queue(stream, dev)), name)
+
+
+def moelb_route(z, idx, wts, gap=None, score=MOELB_SCORE_SOFTMAX, bias=None, groups=1, topk_groups=1, group_top=1,
+                renorm=False, scale=1.0, stream=None):
+    """The k picks of each row of logits: idx [T, k] int32, wts [T, k] and gap [T] fp32 (None: not wanted)."""
+    name = "moelb_route"
+    dev = _device(name, z)
+    T, E = z.shape
+    k = idx.shape[1]
+    f = torch.float32
+    _check(lib().moelb_route(_arg(name, "z", z, (T, E), f, dev), T, E, k, score, _arg(name, "bias", bias, (E,), f, dev),
+                             groups, topk_groups, group_top, int(renorm), scale,
+                             _arg(name, "idx", idx, (T, k), torch.int32, dev), _arg(name, "wts", wts, (T, k), f, dev),
+                             _arg(name, "gap", gap, (T,), f, dev), _queue(stream, dev)), name)
+
+
+def moelb_route_backward_workspace_bytes(T, d, E, dtype) -> int:
+    return int(lib().moelb_route_backward_workspace_bytes(T, d, E, dtype))
+
+
+def moelb_route_backward(h, w, z, idx, dwts, ws, dh=None, dw=None, db=None, score=MOELB_SCORE_SOFTMAX, renorm=False,
+                         scale=1.0, stream=None):
+    """Gradients of moelb_route's weights through moelb_gate_logits: dh as h, dw as w, db [E] fp32 (None: not
+    computed)."""
+    name = "moelb_route_backward"
+    dev = _device(name, h)
+    T, d = h.shape
+    E, k = w.shape[0], idx.shape[1]
+    t, f = h.dtype, torch.float32
+    pws, nws = _workspace(name, ws, dev)
+    _check(lib().moelb_route_backward(_arg(name, "h", h, (T, d), t, dev), T, d, E, k, dtype_code(h),
+                                      _arg(name, "w", w, (E, d), t, dev), _arg(name, "z", z, (T, E), f, dev),
+                                      _arg(name, "idx", idx, (T, k), torch.int32, dev),
+                                      _arg(name, "dwts", dwts, (T, k), f, dev), score, int(renorm), scale, pws, nws,
+                                      _arg(name, "dh", dh, (T, d), t, dev), _arg(name, "dw", dw, (E, d), t, dev),
+                                      _arg(name, "db", db, (E,), f, dev), _queue(stream, dev)), name)
+
+
+def moelb_mx_scale_bytes(K) -> int:
+    """Bytes of a row of K elements' scales (0: no such rows)."""
+    return int(lib().moelb_mx_scale_bytes(K))
+
+
+def _mx_args(name, x, q, scales, dev):
+    *lead, K = x.shape
+    ld = moelb_mx_scale_bytes(K)
+    if ld == 0:
+        raise MoelbError(f"{name}: rows of {K} elements, not a multiple of 32")
+    u8 = torch.uint8
+    return (x.numel() // K, K, dtype_code(x), _arg(name, "x", x, x.shape, x.dtype, dev),
+            _arg(name, "q", q, (*lead, K // 2), u8, dev), _arg(name, "scales", scales, (*lead, ld), u8, dev))
+
+
+def moelb_mx_quantize(x, q, scales, stream=None):
+    """x [..., K] to MX 4-bit: q [..., K/2] and scales [..., moelb_mx_scale_bytes(K)] uint8."""
+    name = "moelb_mx_quantize"
+    dev = _device(name, x)
+    rows, K, code, px, pq, ps = _mx_args(name, x, q, scales, dev)
+    _check(lib().moelb_mx_quantize(px, rows, K, code, pq, ps, _queue(stream, dev)), name)
+
+
+def moelb_mx_dequantize(q, scales, x, stream=None):
+    """What q and scales stand for, to x [..., K]."""
+    name = "moelb_mx_dequantize"
+    dev = _device(name, x)
+    rows, K, code, px, pq, ps = _mx_args(name, x, q, scales, dev)
+    _check(lib().moelb_mx_dequantize(pq, ps, rows, K, code, px, _queue(stream, dev)), name)
+
+
+def moelb_mx_grouped_ffn_workspace_bytes(rows_x, rows, num_groups, E, d, inter) -> int:
+    return int(lib().moelb_mx_grouped_ffn_workspace_bytes(rows_x, rows, num_groups, E, d, inter))
+
+
+def moelb_mx_grouped_ffn(x, rows, group_off, E, w13, w13_scales, w2, w2_scales, ws, y, G=1, rank=-1, gather=None,
+                          gather_k=1, stream=None):
+    """The grouped FFN in MX 4-bit: w13 [E, 2*inter, d/2], w2 [E, d, inter/2] uint8 with their scales (one expert's
+    may lack the leading dimension); x and y [rows, d] in bf16 or fp32."""
+    name = "moelb_mx_grouped_ffn"
+    dev = _device(name, x)
+    rows_x, d = x.shape
+    inter = w2.shape[-1] * 2
+    lead = () if w13.dim() == 2 else (E,)
+    if w13.dim() == 2 and E != 1:
+        raise MoelbError(f"{name}: weights of one expert for E = {E}")
+    if gather is not None and (gather.dtype != torch.int32 or gather.numel() < rows):
+        raise MoelbError(f"{name}: gather holds {gather.numel()} {gather.dtype}, not {rows} int32")
+    if gather is None and rows > rows_x:
+        raise MoelbError(f"{name}: {rows} rows of {rows_x} without a gather")
+    u8, pws_nws = torch.uint8, _workspace(name, ws, dev)
+    _check(lib().moelb_mx_grouped_ffn(
+        _arg(name, "x", x, (rows_x, d), x.dtype, dev), rows_x, rows,
+        _arg(name, "group_off", group_off, (group_off.numel(),), torch.int32, dev), group_off.numel() - 1, E, G, rank,
+        _arg(name, "gather", gather, gather.shape if gather is not None else None, torch.int32, dev), gather_k, d,
+        inter, dtype_code(x), _arg(name, "w13", w13, (*lead, 2 * inter, d // 2), u8, dev),
+        _arg(name, "w13_scales", w13_scales, (*lead, 2 * inter, moelb_mx_scale_bytes(d)), u8, dev),
+        _arg(name, "w2", w2, (*lead, d, inter // 2), u8, dev),
+        _arg(name, "w2_scales", w2_scales, (*lead, d, moelb_mx_scale_bytes(inter)), u8, dev), *pws_nws,
+        _arg(name, "y", y, (rows, d), x.dtype, dev), _queue(stream, dev)), name)

@@ -1,0 +1,321 @@
+"""GPU: the scored router (logits, picks and weights, gradients) against 64-bit references.
+
+Tolerances, before any run; f = 2^-24, u = eps / 2 of the storage type.
+Logits: sums of d products in fp32, off by at most (d + 8) f of the sum of
+magnitudes.  Picks: equal.  Weights: a sum of up to E exponentials whose
+exponents are rounded (|z - max| f each, |z| f for a sigmoid's) and a few
+roundings of 1 f each: (2 max|x| + E + 32) f relative, plus 2^-120 where a score
+underflows.  gap: the same of the larger c, |bias| included.  Gradients: dz is
+rounded once (u) and formed in fp32 with the terms' magnitudes mag: u |dz| + (2
+max|x| + E + 64) f mag; dh and dw are sums of products with that, in fp32, and
+rounded once.
+"""
+import math
+
+import pytest
+import torch
+
+from oracle import scored_router as R
+from tests.gpu_layer import log
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+f = 2.0 ** -24
+
+
+def code(score):
+    from routed_expert_ffn_gate_amd import moelb as M
+    return {"softmax": M.MOELB_SCORE_SOFTMAX, "sigmoid": M.MOELB_SCORE_SIGMOID}[score]
+
+
+def close(got, want, allow, what):
+    d = (got.double() - want).abs()
+    assert torch.isfinite(got).all(), what
+    over = (d / allow).max().item() if d.numel() else 0.0
+    log(f"    {what}: at most {over:.3f} of the allowed error")
+    assert over <= 1.0, what
+
+
+# ---------------------------------------------------------------- logits
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,both", [(1, 8, 1, False), (1, 4096, 128, True), (3, 72, 60, True), (17, 1000, 8, False),
+                                        (64, 2048, 128, True), (65, 520, 256, False), (130, 192, 256, True),
+                                        (512, 256, 160, True), (700, 136, 96, True), (1031, 64, 65, False),
+                                        (9000, 128, 64, True), (33000, 64, 128, True)])
+def test_logits(moelb, dtype, T, d, E, both):
+    from routed_expert_ffn_gate_amd import moelb as M
+    gen = torch.Generator(device="cuda").manual_seed(T + d + E)
+    N = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    h, w, b, wn = N(T, d).to(dtype), (N(E, d) / d ** 0.5).to(dtype), N(E), (N(E, d) / d ** 0.5).to(dtype)
+    z = torch.full((T, E), 7.0, device="cuda")
+    zn = torch.full((T, E), 7.0, device="cuda") if both else None
+    log(f"[logits] {dtype} T={T} d={d} E={E} both={both}")
+    M.moelb_gate_logits(h, w, b, wn if both else None, None, z, zn)  # no bias for the lookahead router
+    torch.cuda.synchronize()
+    H, A = h.double(), h.double().abs()
+    close(z, H @ w.double().t() + b.double(), (d + 8) * f * (A @ w.double().abs().t() + b.double().abs()) + 1e-30, "z")
+    if both:
+        close(zn, H @ wn.double().t(), (d + 8) * f * (A @ wn.double().abs().t()) + 1e-30, "z_next")
+
+
+def test_logits_leave_other_memory(moelb):
+    from routed_expert_ffn_gate_amd import moelb as M
+    for T, E in ((5, 60), (70, 33), (300, 128)):
+        h, w = torch.ones((T, 64), dtype=BF, device="cuda"), torch.ones((E, 64), dtype=BF, device="cuda")
+        out = torch.full((T * E + 256,), 7.0, device="cuda")
+        M.moelb_gate_logits(h, w, None, None, None, out[128:128 + T * E].view(T, E))
+        torch.cuda.synchronize()
+        assert (out[:128] == 7).all() and (out[128 + T * E:] == 7).all() and (out[128:128 + T * E] == 64).all()
+
+
+# ---------------------------------------------------------------- picks
+
+
+def run_route(z, k, score, bias=None, groups=1, topk_groups=1, group_top=1, renorm=False, scale=1.0, gap=True):
+    from routed_expert_ffn_gate_amd import moelb as M
+    T = z.shape[0]
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    wts = torch.full((T, k), math.nan, device="cuda")
+    g = torch.full((T,), math.nan, device="cuda") if gap else None
+    M.moelb_route(z, idx, wts, g, score=code(score), bias=bias, groups=groups, topk_groups=topk_groups,
+                  group_top=group_top, renorm=renorm, scale=scale)
+    torch.cuda.synchronize()
+    return idx, wts, g
+
+
+def check_route(z, k, score, **kw):
+    idx, wts, gap = run_route(z, k, score, **kw)
+    want_idx, want_w, want_gap = (v.cuda() for v in R.route(z, k, score, **kw))
+    wrong = (idx != want_idx).any(1).nonzero()[:, 0]
+    assert wrong.numel() == 0, (wrong[:4], idx[wrong[:2]], want_idx[wrong[:2]])
+    fin = z[z > -math.inf].double().clamp(min=-104.0, max=104.0)
+    span = 0.0 if fin.numel() == 0 else float(fin.max() - fin.min() if score == "softmax" else fin.abs().max())
+    rel = (2 * span + z.shape[1] + 32) * f
+    close(wts, want_w, rel * want_w.abs() + 2.0 ** -120, "wts")
+    some = torch.isfinite(want_gap)
+    assert torch.equal(torch.isfinite(gap), some)
+    c = 1.0 + (float(kw["bias"][torch.isfinite(kw["bias"])].abs().max()) if kw.get("bias") is not None else 0.0)
+    close(gap[some], want_gap[some], torch.full_like(want_gap[some], 4 * rel * c), "gap")
+
+
+def logits(T, E, seed, std=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return std * torch.randn((T, E), generator=gen, device="cuda")
+
+
+SHAPES = [(1, 1, 1), (1, 8, 8), (3, 2, 1), (2, 3, 3), (64, 60, 4), (33, 64, 16), (129, 65, 6), (257, 128, 8),
+          (100, 160, 9), (77, 192, 2), (300, 256, 8), (5, 256, 16), (1, 256, 8), (40, 31, 7), (1000, 16, 2)]
+
+
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", SHAPES)
+def test_route(moelb, T, E, k, score, biased):
+    z = logits(T, E, T + E + k)
+    bias = 0.1 * logits(1, E, 5)[0] if biased else None
+    log(f"[route] T={T} E={E} k={k} {score} bias={biased}")
+    check_route(z, k, score, bias=bias, renorm=bool(k % 2), scale=2.5)
+
+
+GROUPS = [(64, 4, 8, 4, 2), (256, 8, 8, 4, 2), (256, 8, 8, 1, 2), (256, 16, 16, 3, 1), (160, 6, 8, 3, 1),
+          (160, 6, 5, 5, 2), (60, 4, 15, 2, 2), (60, 4, 60, 7, 1), (96, 8, 2, 1, 2), (128, 8, 4, 2, 2), (8, 2, 4, 1, 2),
+          (256, 16, 128, 9, 2), (256, 8, 256, 8, 1), (33, 3, 11, 1, 2)]
+
+
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,topk_groups,group_top", GROUPS)
+def test_groups(moelb, E, k, groups, topk_groups, group_top, score, biased):
+    z = logits(150, E, E + groups)
+    bias = 0.1 * logits(1, E, 6)[0] if biased else None
+    log(f"[route] E={E} k={k} groups={groups}/{topk_groups} top={group_top} {score} bias={biased}")
+    check_route(z, k, score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top, renorm=True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 8])
+def test_ties_go_to_the_lower_id(moelb, score, groups):
+    """Few different logits: most neighbours in the order are equal."""
+    z = torch.round(logits(200, 64, 9) * 1.5) / 2
+    kw = dict(groups=groups, topk_groups=min(groups, 3), group_top=min(groups, 2))
+    check_route(z, 8, score, renorm=True, **kw)
+    check_route(torch.zeros_like(z), 8, score, **kw)
+    check_route(z, 8, score, bias=torch.full((64,), 0.25, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_neighbours_one_step_apart(moelb, score, biased):
+    """Logits that differ in their last bits: their scores are equal in fp32, not in exact arithmetic."""
+    base = torch.tensor([0.7, -0.3, 2.0, 5.0, -4.0, 9.0], device="cuda").repeat(40)[:, None]
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    steps = torch.argsort(torch.rand((240, 96), generator=gen, device="cuda"), dim=1)
+    z = (base.double() * (1 + steps.double() * 2.0 ** -23)).float()
+    bias = torch.full((96,), 0.125, device="cuda") if biased else None
+    check_route(z, 7, score, bias=bias)
+    check_route(z, 7, score, bias=bias, groups=8, topk_groups=2, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("std", [30.0, 1e-6, 1e4])
+def test_far_and_near_logits(moelb, score, std):
+    """Scores that underflow or saturate; without a bias the order is the logits'."""
+    check_route(logits(120, 128, 4, std), 8, score, renorm=True)
+    check_route(logits(120, 128, 4, std), 8, score, scale=0.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_large_bias(moelb, score):
+    """A bias that outweighs every score, and one that leaves only its own rounding between experts."""
+    z = logits(120, 64, 8)
+    b = logits(1, 64, 3)[0]
+    for size in (100.0, 3e5, 1e30):
+        check_route(z, 6, score, bias=size * b, renorm=True)
+
+
+@pytest.mark.parametrize("groups,topk_groups,group_top", [(1, 1, 1), (8, 4, 1), (8, 4, 2)])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masked(moelb, score, biased, groups, topk_groups, group_top):
+    """Masked logits (-inf, NaN), rows of nothing else, rows with fewer left than k, +inf, and experts whose bias
+    excludes them."""
+    z = logits(160, 64, 11)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    hit = torch.rand(z.shape, generator=gen, device="cuda")
+    z[hit < 0.3] = -math.inf
+    z[hit > 0.95] = math.nan
+    z[5], z[6], z[7, 3:] = -math.inf, math.nan, -math.inf
+    z[8], z[9], z[10] = -math.inf, 1e38, -1e38
+    z[8, 40], z[11, 7], z[12, 3], z[12, 9] = 1.0, math.inf, math.inf, math.inf
+    bias = None
+    if biased:
+        bias = 0.1 * logits(1, 64, 7)[0]
+        bias[3], bias[20] = -math.inf, math.nan
+    kw = dict(bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)
+    check_route(z, 8, score, renorm=True, **kw)
+    idx, wts, gap = run_route(z, 8, score, renorm=True, **kw)
+    assert (idx[5:7] == -1).all() and (wts[5:7] == 0).all() and torch.isinf(gap[5:7]).all()
+
+
+def test_route_outputs_that_are_not_wanted(moelb):
+    from routed_expert_ffn_gate_amd import moelb as M
+    z = logits(50, 40, 1)
+    full = run_route(z, 5, "softmax")
+    idx = torch.empty((50, 5), dtype=torch.int32, device="cuda")
+    M.moelb_route(z, idx, None)
+    assert torch.equal(idx, full[0])
+    # rows that start at any float, and memory behind the outputs
+    store = torch.empty((50 * 40 + 1,), device="cuda")
+    store[1:] = z.reshape(-1)
+    out, w = torch.full((50 * 5 + 8,), 9, dtype=torch.int32, device="cuda"), torch.full((50 * 5 + 8,), 9.0, device="cuda")
+    M.moelb_route(store[1:].view(50, 40), out[:250].view(50, 5), w[:250].view(50, 5))
+    torch.cuda.synchronize()
+    assert torch.equal(out[:250].view(50, 5), full[0]) and torch.equal(w[:250].view(50, 5), full[1])
+    assert (out[250:] == 9).all() and (w[250:] == 9).all()
+
+
+# ---------------------------------------------------------------- gradients
+
+
+def check_gradient(T, d, E, k, dtype, score, renorm, idx=None, z=None, scale=1.5):
+    from routed_expert_ffn_gate_amd import moelb as M
+    gen = torch.Generator(device="cuda").manual_seed(T + d + E + k)
+    N = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    h, w, g = N(T, d).to(dtype), (N(E, d) / d ** 0.5).to(dtype), N(T, k)
+    if z is None:
+        z = N(T, E)
+    if idx is None:
+        idx = z.topk(k, dim=1).indices.to(torch.int32)
+    dh, dw, db = torch.full_like(h, 7.0), torch.full_like(w, 7.0), torch.full((E,), 7.0, device="cuda")
+    ws = torch.full((M.moelb_route_backward_workspace_bytes(T, d, E, M.dtype_code(h)),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    kw = dict(score=code(score), renorm=renorm, scale=scale)
+    M.moelb_route_backward(h, w, z, idx, g, ws, dh, dw, db, **kw)
+    torch.cuda.synchronize()
+    u = torch.finfo(dtype).eps / 2
+    dz, mag = R.route_dz(z, idx, g, score, renorm, scale)
+    fin = z[z > -math.inf].double().clamp(min=-104.0, max=104.0)
+    span = 0.0 if fin.numel() == 0 else float(fin.max() - fin.min() if score == "softmax" else fin.abs().max())
+    e32 = (2 * span + E + 64) * f * mag  # of the fp32 dz
+    ez = u * dz.abs() + 1.01 * e32 + 2.0 ** -120
+    W, H = w.double(), h.double()
+    want = dz @ W
+    close(dh, want, ez @ W.abs() + (E + 8) * f * (dz.abs() @ W.abs()) + 1.01 * u * want.abs() + 1e-30, "dh")
+    want = dz.t() @ H
+    close(dw, want, ez.t() @ H.abs() + (T + 8) * f * (dz.abs().t() @ H.abs()) + 1.01 * u * want.abs() + 1e-30, "dw")
+    close(db, dz.sum(0), (e32 + (T + 8) * f * dz.abs()).sum(0) + 1e-30, "db")
+    # the same call gives the same bits, and each output alone
+    for keep in ("dh", "dw", "db"):
+        one = {n: torch.full_like(v, 3.0) for n, v in (("dh", dh), ("dw", dw), ("db", db)) if n == keep}
+        M.moelb_route_backward(h, w, z, idx, g, ws, **one, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(one[keep], dict(dh=dh, dw=dw, db=db)[keep]), keep
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["scores", "renorm"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,k", [(1, 8, 2, 2), (3, 72, 60, 4), (256, 256, 16, 2), (129, 520, 64, 8),
+                                     (700, 136, 130, 6), (513, 264, 256, 16), (5000, 64, 96, 3)])
+def test_route_gradient(moelb, T, d, E, k, dtype, score, renorm):
+    log(f"[route gradient] T={T} d={d} E={E} k={k} {dtype} {score} renorm={renorm}")
+    check_gradient(T, d, E, k, dtype, score, renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True], ids=["scores", "renorm"])
+def test_route_gradient_of_masked_and_left_out(moelb, score, renorm):
+    z = logits(90, 48, 3)
+    idx = z.topk(5, dim=1).indices.to(torch.int32)
+    idx[4], idx[5, 2:], idx[6, 1], idx[7] = -1, -1, 99, idx[7, 0].clone()
+    z[8], z[9, ::2], z[10, :7] = -math.inf, -math.inf, math.nan
+    z[11], z[12] = 60.0, -60.0
+    check_gradient(90, 64, 48, 5, BF, score, renorm, idx=idx, z=z)
+    check_gradient(90, 64, 48, 5, F32, score, renorm, idx=idx, z=z)
+
+
+def test_route_gradient_of_no_tokens(moelb):
+    from routed_expert_ffn_gate_amd import moelb as M
+    for dtype in (BF, F32):
+        E, d = 24, 64
+        w = torch.ones((E, d), dtype=dtype, device="cuda")
+        dw, db = torch.full_like(w, 7.0), torch.full((E,), 7.0, device="cuda")
+        ws = torch.empty((M.moelb_route_backward_workspace_bytes(0, d, E, M.dtype_code(w)),), dtype=torch.uint8,
+                         device="cuda")
+        M.moelb_route_backward(w[:0], w, db[None][:0], torch.empty((0, 2), dtype=torch.int32, device="cuda"),
+                               torch.empty((0, 2), device="cuda"), ws, w[:0].clone(), dw, db)
+        torch.cuda.synchronize()
+        assert (dw == 0).all() and (db == 0).all()
+
+
+def test_captured_chain(moelb):
+    """Logits, picks and gradients as one graph, replayed on new inputs between eager calls."""
+    from routed_expert_ffn_gate_amd import moelb as M
+    T, d, E, k = 200, 128, 32, 4
+    h, w = torch.empty((T, d), dtype=BF, device="cuda"), logits(E, d, 1).to(BF)
+    b, bias, g = 0.1 * logits(1, E, 2)[0], 0.05 * logits(1, E, 4)[0], logits(T, k, 3)
+    ws = torch.empty((M.moelb_route_backward_workspace_bytes(T, d, E, M.MOELB_BF16),), dtype=torch.uint8, device="cuda")
+    new = lambda: (torch.empty((T, E), device="cuda"), torch.empty((T, k), dtype=torch.int32, device="cuda"),  # noqa: E731
+                   torch.empty((T, k), device="cuda"), torch.empty_like(h), torch.empty_like(w),
+                   torch.empty((E,), device="cuda"))
+
+    def chain(z, idx, wts, dh, dw, db):
+        M.moelb_gate_logits(h, w, b, None, None, z)
+        M.moelb_route(z, idx, wts, score=M.MOELB_SCORE_SIGMOID, bias=bias, groups=4, topk_groups=2, group_top=2,
+                      renorm=True, scale=2.5)
+        M.moelb_route_backward(h, w, z, idx, g, ws, dh, dw, db, score=M.MOELB_SCORE_SIGMOID, renorm=True, scale=2.5)
+    outs, eager = new(), new()
+    h.copy_(logits(T, d, 0))
+    chain(*eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(*outs)
+    for seed in range(4):
+        h.copy_(logits(T, d, 10 + seed))
+        graph.replay()
+        chain(*eager)
+        torch.cuda.synchronize()
+        for a, c in zip(outs, eager):
+            assert torch.equal(a, c)

@@ -101,13 +101,18 @@ struct MxArgs {
   uint8_t* q;         // gate/up: activations' codes [rows][inter/2]
   uint8_t* qs;        // and scales [rows][ldq]
   void* y;            // down: [rows][N]
-  int rows, K, N, lda, inter, ldq, ntn;
+  int rows_x, rows, K, N, lda, inter, ldq, ntn;
 };
 
-__device__ __forceinline__ f32x16_t mx_mfma(uint4 a, uint4 b, f32x16_t c, int sa, int sb) {
+// a . b over 64 k, the scales in byte 0 (HIGH: 2) of sa and sb.
+template <bool HIGH>
+__device__ __forceinline__ f32x16_t mx_mfma(uint4 a, uint4 b, f32x16_t c, uint32_t sa, uint32_t sb) {
   const i32x8_t x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const i32x8_t y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, HIGH ? 2 : 0, (int)sa, HIGH ? 2 : 0, (int)sb);
+}
+__device__ __forceinline__ f32x16_t mx_mfma_at(uint4 a, uint4 b, f32x16_t c, uint32_t sa, uint32_t sb, int high) {
+  return high ? mx_mfma<true>(a, b, c, sa, sb) : mx_mfma<false>(a, b, c, sa, sb);
 }
 
 // Block of 32 activations of a row, 16 in this lane (columns 8 i + 4 fh + j) and
@@ -150,52 +155,216 @@ __device__ __forceinline__ void store_block(float* o, const f32x16_t& a, int fh)
     *reinterpret_cast<float4*>(o + q * 8 + fh * 4) = make_float4(a[q * 4], a[q * 4 + 1], a[q * 4 + 2], a[q * 4 + 3]);
 }
 
-// Tile of 64 rows x 64 columns, four waves.  DOWN: rows are the activations',
-// columns y's; else rows through the map, columns the gate's and the up's.
-template <bool DOWN, typename T>
-__global__ __launch_bounds__(256) void mx_tile_kernel(MxArgs p) {
-  const int n = *p.s.n_mtiles, t = blockIdx.x;
-  if (t >= n * p.ntn) return;
-  const int mt_ = t / p.ntn, nt = t % p.ntn;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int fr = lane & 31, fh = lane >> 5;
-  const int e = p.s.mt_e[mt_], v0 = p.s.mt_v0[mt_] + (wave >> 1) * 32, end = p.s.eoff[e + 1];
-  const int c0 = nt * 64 + (wave & 1) * 32;  // the wave's columns
-  const int cols = DOWN ? p.N : p.inter;
-  if (v0 >= end || c0 >= cols) return;
-  const int v = v0 + fr < end ? v0 + fr : v0;
-  const size_t ar = DOWN ? v : p.s.asrc[v], br = (size_t)e * p.N + c0 + fr;
-  const uint8_t* a = p.a + ar * (p.K / 2);
-  const uint8_t* as = p.as + ar * p.lda;
-  const uint8_t* b = p.w + br * (p.K / 2);
-  const uint8_t* bs = p.ws + br * p.lda;
-  const size_t up = (size_t)p.inter * (p.K / 2), ups = (size_t)p.inter * p.lda;
-  f32x16_t acc, acc2;
+// ---- the tile
+//
+// BM rows x BN weight rows a workgroup, four waves as WM x WN.  K steps of 256
+// (128 bytes a row) stream memory -> LDS into a ring of three stages, two steps
+// ahead; the scales come 16 bytes a row, two steps at a time, into a ring of two
+// beside them.  Gate/up: the first half of the tile's weight rows are gate rows,
+// the second the matching up rows, and a wave takes the same columns of both.
+// Loads go through buffer descriptors: a lane that asks for OUTSIDE gets zeros,
+// which is how K ends inside a step (a zero code times any scale but NaN is 0).
+template <int BM, int BN, int WM>
+struct Tile {
+  static constexpr int WN = 4 / WM, MI = BM / 32 / WM, NI = BN / 32 / WN;
+  static constexpr int JA = BM / 32, JB = BN / 32;         // 1 KiB DMA instructions a wave and step
+  static constexpr int JS = (BM + BN + 255) / 256;         // of scales, a wave and two steps
+  static constexpr int STAGE = (BM + BN) * 128, CHUNK = JS * 4096;
+  static constexpr int STAGES = 3;
+  static constexpr size_t LDS = (size_t)STAGES * STAGE + 2 * CHUNK;
+};
+
+__device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ (((row >> 1) ^ (row << 2)) & 7); }
+
+// Virtual rows, expert and columns of a tile.
+struct Place {
+  int e, v0, end, nt;
+};
+__device__ __forceinline__ bool find_tile(const MxArgs& p, int bid, Place& o) {
+  const int n = *p.s.n_mtiles, t = xcd_tile(bid, n * p.ntn);
+  if (t < 0) return false;
+  int mt_;
+  grouped_tile(t, n, p.ntn, mt_, o.nt);
+  o.e = p.s.mt_e[mt_];
+  o.v0 = p.s.mt_v0[mt_];
+  o.end = p.s.eoff[o.e + 1];
+  return true;
+}
+// Memory row of the tile's row r: through the row map (gate/up), or the virtual row.
+template <bool DOWN>
+__device__ __forceinline__ uint32_t row_of(const MxArgs& p, const Place& o, int r) {
+  const int v = o.v0 + r < o.end ? o.v0 + r : o.v0;  // rows past the expert's end repeat its first
+  return DOWN ? (uint32_t)v : (uint32_t)p.s.asrc[v];
+}
+// Weight row (of the expert's N) of the tile's weight row r; past the last: row 0.
+template <bool DOWN, int BN>
+__device__ __forceinline__ uint32_t weight_of(const MxArgs& p, const Place& o, int r) {
+  if (DOWN) {
+    const int c = o.nt * BN + r;
+    return (uint32_t)(c < p.N ? c : 0);
+  }
+  const int c = o.nt * (BN / 2) + r % (BN / 2), cc = c < p.inter ? c : 0;
+  return (uint32_t)(r < BN / 2 ? cc : p.inter + cc);
+}
+// The tile's weight row where block ni of wave column wn starts.
+template <bool DOWN, int BN, int NI>
+__device__ __forceinline__ int block_row(int wn, int ni) {
+  return DOWN ? (wn * NI + ni) * 32 : (wn * (NI / 2) + ni % (NI / 2)) * 32 + ni / (NI / 2) * (BN / 2);
+}
+
+// What a wave has in its accumulators to memory: block (mi, ni) is transposed,
+// lane -> row lane % 32, element j -> column (j / 4) * 8 + (lane / 32) * 4 + j % 4.
+// row0: the wave's first row of the tile.
+template <bool DOWN, typename T, int BN, int MI, int NI>
+__device__ __forceinline__ void put_tile(const MxArgs& p, const Place& o, int row0, int wn,
+                                         const f32x16_t (&acc)[MI][NI]) {
+  const int lane = threadIdx.x & 63, fr = lane & 31, fh = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = acc2[i] = 0.f;
-  for (int k0 = 0; k0 < p.K; k0 += 64) {
-    const int k = k0 + fh * 32;
-    const bool in = k < p.K;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 fa = in ? *reinterpret_cast<const uint4*>(a + k / 2) : zero;
-    const uint4 fb = in ? *reinterpret_cast<const uint4*>(b + k / 2) : zero;
-    const int sa = in ? as[k / 32] : 0, sb = in ? bs[k / 32] : 0;
-    acc = mx_mfma(fb, fa, acc, sb, sa);
-    if constexpr (!DOWN) {
-      const uint4 fu = in ? *reinterpret_cast<const uint4*>(b + up + k / 2) : zero;
-      acc2 = mx_mfma(fu, fa, acc2, in ? bs[ups + k / 32] : 0, sa);
+  for (int mi = 0; mi < MI; ++mi) {
+    const int v = o.v0 + row0 + mi * 32 + fr;
+    const bool in = v < o.end;
+    if constexpr (DOWN) {
+      T* y = static_cast<T*>(p.y) + (size_t)(in ? p.s.rowmap[v] : 0) * p.N;
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const int c = o.nt * BN + block_row<true, BN, NI>(wn, ni);
+        if (in && c < p.N) store_block(y + c, acc[mi][ni], fh);
+      }
+    } else {
+#pragma unroll
+      for (int ni = 0; ni < NI / 2; ++ni) {
+        const int c = o.nt * (BN / 2) + block_row<false, BN, NI>(wn, ni);
+        uint32_t byte;
+        const uint2 codes = act_block(acc[mi][ni], acc[mi][ni + NI / 2], byte);
+        if (in && c < p.inter) {
+          *reinterpret_cast<uint2*>(p.q + (size_t)v * (p.inter / 2) + c / 2 + fh * 8) = codes;
+          uint8_t* s = p.qs + (size_t)v * p.ldq + c / 32;
+          if (fh == 0) *s = (uint8_t)byte;
+          if (fh == 1 && c + 32 == p.inter)  // the row's scales end here: zeros to the next 16 bytes
+            for (int i = 1; c / 32 + i < p.ldq; ++i) s[i] = 0;
+        }
+      }
     }
   }
-  if constexpr (DOWN) {
-    if (v0 + fr < end) store_block(static_cast<T*>(p.y) + (size_t)p.s.rowmap[v] * p.N + c0, acc, fh);
-  } else {
-    uint32_t byte;
-    const uint2 o = act_block(acc, acc2, byte);
-    if (v0 + fr < end) {
-      *reinterpret_cast<uint2*>(p.q + (size_t)v * (p.inter / 2) + c0 / 2 + fh * 8) = o;
-      if (fh == 0) p.qs[(size_t)v * p.ldq + c0 / 32] = (uint8_t)byte;
+}
+
+template <bool DOWN, typename T, int BM, int BN, int WM>
+__global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs p) {
+  using G = Tile<BM, BN, WM>;
+  constexpr int MI = G::MI, NI = G::NI, JA = G::JA, JB = G::JB, JS = G::JS, STAGE = G::STAGE;
+  extern __shared__ __align__(16) char smem[];
+  Place o;
+  if (!find_tile(p, blockIdx.x, o)) return;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / G::WN, wn = wave % G::WN, fr = lane & 31, fh = lane >> 5;
+  const int KT = (p.K + 255) / 256, half = p.K / 2;
+  const uint32_t rows_a = DOWN ? (uint32_t)p.rows : (uint32_t)p.rows_x;
+  const mt::i32x4_t da = mt::descriptor(p.a, rows_a * (uint32_t)half);
+  const mt::i32x4_t db = mt::descriptor(p.w + (size_t)o.e * p.N * half, (uint32_t)p.N * (uint32_t)half);
+  const mt::i32x4_t dsa = mt::descriptor(p.as, rows_a * (uint32_t)p.lda);
+  const mt::i32x4_t dsb = mt::descriptor(p.ws + (size_t)o.e * p.N * p.lda, (uint32_t)p.N * (uint32_t)p.lda);
+
+  // DMA: instruction j of a wave fills the 8 LDS rows (J wave + j) * 8 ..; lane l
+  // row l / 8 of them, 16-byte slot l % 8
+  uint32_t aoff[JA], boff[JB], soff[JS];
+  const int whole = half / 128;  // steps below it lie in K with all their bytes
+  uint32_t tail_a = 0, tail_b = 0;  // in step `whole`: which instructions' pieces lie in K
+#pragma unroll
+  for (int j = 0; j < JA; ++j) {
+    const int r = (wave * JA + j) * 8 + (lane >> 3), c = slot_of(r, lane & 7) * 16;
+    aoff[j] = row_of<DOWN>(p, o, r) * (uint32_t)half + c;
+    tail_a |= (uint32_t)(whole * 128 + c < half) << j;
+  }
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int r = (wave * JB + j) * 8 + (lane >> 3), c = slot_of(r, lane & 7) * 16;
+    boff[j] = weight_of<DOWN, BN>(p, o, r) * (uint32_t)half + c;
+    tail_b |= (uint32_t)(whole * 128 + c < half) << j;
+  }
+#pragma unroll
+  for (int j = 0; j < JS; ++j) {
+    const int r = (wave * JS + j) * 64 + lane;  // the tile's rows, then its weight rows
+    soff[j] = r < BM        ? row_of<DOWN>(p, o, r) * (uint32_t)p.lda
+              : r < BM + BN ? weight_of<DOWN, BN>(p, o, r - BM) * (uint32_t)p.lda
+                            : mt::OUTSIDE;
+  }
+  auto issue = [&](int t) {
+    const uint32_t st = lds0 + (uint32_t)(t % G::STAGES * STAGE);
+#pragma unroll
+    for (int j = 0; j < JA; ++j)
+      mt::copy16(t < whole || (tail_a >> j & 1) ? aoff[j] : mt::OUTSIDE, da, (uint32_t)t * 128u,
+                 st + (uint32_t)((wave * JA + j) * 1024));
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+      mt::copy16(t < whole || (tail_b >> j & 1) ? boff[j] : mt::OUTSIDE, db, (uint32_t)t * 128u,
+                 st + (uint32_t)(BM * 128 + (wave * JB + j) * 1024));
+  };
+  const uint32_t sc0 = (uint32_t)(G::STAGES * STAGE);
+  auto issue_scales = [&](int c) {
+    const uint32_t st = lds0 + sc0 + (uint32_t)((c & 1) * G::CHUNK);
+#pragma unroll
+    for (int j = 0; j < JS; ++j)  // an instruction's 64 rows are all of one operand: BM is a multiple of 64
+      mt::copy16(soff[j], (wave * JS + j) * 64 < BM ? dsa : dsb, (uint32_t)c * 16u,
+                 st + (uint32_t)((wave * JS + j) * 1024));
+  };
+  int arow[MI], brow[NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) arow[i] = (wm * MI + i) * 32 + fr;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) brow[i] = block_row<DOWN, BN, NI>(wn, i) + fr;
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
+  issue_scales(0);
+  issue(0);
+  if (KT > 1) issue(1);
+  for (int t = 0; t < KT; ++t) {
+    // step t and its scales landed (only step t + 1 may be in flight), and every
+    // wave is done with step t - 1, whose stage the refill takes
+    if (t + 1 < KT)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(JA + JB) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if ((t & 1) == 0 && t + 2 < KT) issue_scales(t / 2 + 1);
+    if (t + 2 < KT) issue(t + 2);
+    const char* st = smem + t % G::STAGES * STAGE;
+    const char* sc = smem + sc0 + ((t >> 1) & 1) * G::CHUNK + (t & 1) * 8;
+    // bytes 2 ks + fh of a row's eight are its scales in sub-step ks
+    uint32_t sa[MI][2], sb[NI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + arow[i] * 16);
+      sa[i][0] = v.x >> (8 * fh), sa[i][1] = v.y >> (8 * fh);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + (BM + brow[i]) * 16);
+      sb[i][0] = v.x >> (8 * fh), sb[i][1] = v.y >> (8 * fh);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint4 fa[MI], fb[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        fb[i] = *reinterpret_cast<const uint4*>(st + BM * 128 + brow[i] * 128 + slot_of(fr, ks * 2 + fh) * 16);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        fa[i] = *reinterpret_cast<const uint4*>(st + arow[i] * 128 + slot_of(fr, ks * 2 + fh) * 16);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+          acc[mi][ni] = mx_mfma_at(fb[ni], fa[mi], acc[mi][ni], sb[ni][ks >> 1], sa[mi][ks >> 1], ks & 1);
     }
   }
+  put_tile<DOWN, T, BN, MI, NI>(p, o, wm * MI * 32, wn, acc);
 }
 
 // ---------------------------------------------------------------- host
@@ -239,21 +408,31 @@ int launch_quantize(const void* x, long long rows, int K, uint8_t* q, uint8_t* s
   return MOELB_OK;
 }
 
+constexpr int BN = 128;
+
+template <bool DOWN, typename T, int BM, int WM>
+int launch_tiles(const MxArgs& p, size_t mtiles, hipStream_t s) {
+  using G = Tile<BM, BN, WM>;
+  if (!moelb_allow_lds(mx_stream_kernel<DOWN, T, BM, BN, WM>, G::LDS)) return MOELB_ELAUNCH;
+  hipLaunchKernelGGL((mx_stream_kernel<DOWN, T, BM, BN, WM>), dim3((unsigned)(mtiles * p.ntn + 8)), dim3(256), G::LDS, s,
+                     p);
+  MOELB_CHECK_LAUNCH();
+  return MOELB_OK;
+}
+
 template <typename T>
-int run_ffn(const MxArgs& base, const void* x, int rows_x, int d, int inter, const uint8_t* w13, const uint8_t* w13s,
+int run_ffn(const MxArgs& base, const void* x, int d, int inter, const uint8_t* w13, const uint8_t* w13s,
             const uint8_t* w2, const uint8_t* w2s, uint8_t* xq, uint8_t* xs, hipStream_t s, size_t mtiles) {
-  int st = launch_quantize<T>(x, rows_x, d, xq, xs, s);
+  int st = launch_quantize<T>(x, base.rows_x, d, xq, xs, s);
   if (st != MOELB_OK) return st;
   MxArgs p = base;
   p.a = xq, p.as = xs, p.w = w13, p.ws = w13s;
-  p.K = d, p.N = 2 * inter, p.lda = mx::scale_bytes(d), p.ntn = (inter + 63) / 64;
-  hipLaunchKernelGGL((mx_tile_kernel<false, T>), dim3((unsigned)(mtiles * p.ntn)), dim3(256), 0, s, p);
-  MOELB_CHECK_LAUNCH();
+  p.K = d, p.N = 2 * inter, p.lda = mx::scale_bytes(d), p.ntn = (2 * inter + BN - 1) / BN;
+  st = launch_tiles<false, T, 64, 2>(p, mtiles, s);
+  if (st != MOELB_OK) return st;
   p.a = p.q, p.as = p.qs, p.w = w2, p.ws = w2s;
-  p.K = inter, p.N = d, p.lda = p.ldq, p.ntn = (d + 63) / 64;
-  hipLaunchKernelGGL((mx_tile_kernel<true, T>), dim3((unsigned)(mtiles * p.ntn)), dim3(256), 0, s, p);
-  MOELB_CHECK_LAUNCH();
-  return MOELB_OK;
+  p.K = inter, p.N = d, p.lda = p.ldq, p.ntn = (d + BN - 1) / BN;
+  return launch_tiles<true, T, 64, 2>(p, mtiles, s);
 }
 
 }  // namespace
@@ -306,7 +485,7 @@ extern "C" int moelb_mx_grouped_ffn(const void* x, int rows_x, int rows, const i
   if (!group_off || !w13 || !w13_scales || !w2 || !w2_scales) return MOELB_EINVAL;
   if (rows > 0 && (!x || !y || rows_x < 1)) return MOELB_EINVAL;
   if (!aligned16({x, w13, w13_scales, w2, w2_scales, y})) return MOELB_EINVAL;
-  const size_t mtiles = max_mtiles(rows, E), ntn = (size_t)((d > inter ? d : inter) + 63) / 64;
+  const size_t mtiles = max_mtiles(rows, E), ntn = (size_t)((d > inter ? d : inter) + 63) / 64 + 1;
   if (mtiles * ntn > moelb_most_blocks(256)) return MOELB_EINVAL;
   const MxLayout l = mx_layout(rows_x, rows, num_groups, E, d, inter);
   if (!ws || !aligned16({ws}) || ws_bytes < l.total) return MOELB_EWORKSPACE;
@@ -317,13 +496,13 @@ extern "C" int moelb_mx_grouped_ffn(const void* x, int rows_x, int rows, const i
   p.q = reinterpret_cast<uint8_t*>(base + l.aq);
   p.qs = reinterpret_cast<uint8_t*>(base + l.as);
   p.y = y;
-  p.rows = rows, p.inter = inter, p.ldq = mx::scale_bytes(inter);
+  p.rows_x = rows_x, p.rows = rows, p.inter = inter, p.ldq = mx::scale_bytes(inter);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, SCHED_MIN_BM, gather, gather_k, rows_x, p.s, s);
   if (st != MOELB_OK) return st;
   uint8_t* xq = reinterpret_cast<uint8_t*>(base + l.xq);
   uint8_t* xs = reinterpret_cast<uint8_t*>(base + l.xs);
   return dtype == MOELB_BF16
-             ? run_ffn<uint16_t>(p, x, rows_x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s, mtiles)
-             : run_ffn<float>(p, x, rows_x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s, mtiles);
+             ? run_ffn<uint16_t>(p, x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s, mtiles)
+             : run_ffn<float>(p, x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s, mtiles);
 }

@@ -730,7 +730,7 @@ int moelb_mx_dequantize(const uint8_t* q, const uint8_t* scales, long long rows,
  *             written
  * Requires rows >= 0, rows_x >= 1 when rows > 0, d % 32 == 0, inter % 32 == 0, both
  * up to 2^19, E <= 256, num_groups % E == 0 when rank >= 0, num_groups <= 32768, and
- * rows_x*d/2, rows*inter/2, inter*d and rows*d*4 bytes each below 2^32 - 2^21; x, the
+ * rows_x*d/2, rows*inter/2 and inter*d bytes each below 2^32 - 2^21; x, the
  * weights, their scales, ws and y 16-byte aligned.  The workspace's size is 0 for
  * counts and widths that the call refuses.
  */

@@ -157,20 +157,27 @@ __device__ __forceinline__ void store_block(float* o, const f32x16_t& a, int fh)
 
 // ---- the tile
 //
-// BM rows x BN weight rows a workgroup, four waves as WM x WN.  K steps of 256
-// (128 bytes a row) stream memory -> LDS into a ring of three stages, two steps
-// ahead; the scales come 16 bytes a row, two steps at a time, into a ring of two
-// beside them.  Gate/up: the first half of the tile's weight rows are gate rows,
-// the second the matching up rows, and a wave takes the same columns of both.
-// Loads go through buffer descriptors: a lane that asks for OUTSIDE gets zeros,
-// which is how K ends inside a step (a zero code times any scale but NaN is 0).
-template <int BM, int BN, int WM>
+// BM rows x BN weight rows a workgroup, NW waves, WM of them along the rows.  K
+// steps of 256 (128 bytes a row) stream memory -> LDS into a ring of STAGES; the
+// scales come 16 bytes a row, two steps at a time, into a ring of two beside them.
+// Gate/up: the first half of the tile's weight rows are gate rows, the second the
+// matching up rows, and a wave takes the same columns of both.  Loads go through
+// buffer descriptors: a lane that asks for OUTSIDE gets zeros, which is how K ends
+// inside a step (a zero code times any scale but NaN is 0).
+//
+// A step is four sub-steps of 64 k.  The fragments of a sub-step are read while the
+// one before computes.  The barrier stands before the last sub-step: by then every
+// wave has read the step's stage, which the refill takes, and has its part of the
+// next step landed, whose first fragments the last sub-step reads.
+template <int BM_, int BN_, int NW_, int WM_, int STAGES_>
 struct Tile {
-  static constexpr int WN = 4 / WM, MI = BM / 32 / WM, NI = BN / 32 / WN;
-  static constexpr int JA = BM / 32, JB = BN / 32;         // 1 KiB DMA instructions a wave and step
-  static constexpr int JS = (BM + BN + 255) / 256;         // of scales, a wave and two steps
-  static constexpr int STAGE = (BM + BN) * 128, CHUNK = JS * 4096;
-  static constexpr int STAGES = 3;
+  static constexpr int BM = BM_, BN = BN_, NW = NW_, WM = WM_, STAGES = STAGES_;
+  static constexpr int THREADS = NW * 64, EU = BM * BN / NW > 8192 ? 1 : 2;
+  static constexpr int WN = NW / WM, MI = BM / 32 / WM, NI = BN / 32 / WN;
+  static constexpr int JA = BM / 8 / NW, JB = BN / 8 / NW;       // 1 KiB DMA instructions a wave and step
+  static constexpr int J = JA + JB;
+  static constexpr int JS = (BM + BN + 64 * NW - 1) / (64 * NW); // of scales, a wave and two steps
+  static constexpr int STAGE = (BM + BN) * 128, CHUNK = JS * NW * 1024;
   static constexpr size_t LDS = (size_t)STAGES * STAGE + 2 * CHUNK;
 };
 
@@ -248,10 +255,10 @@ __device__ __forceinline__ void put_tile(const MxArgs& p, const Place& o, int ro
   }
 }
 
-template <bool DOWN, typename T, int BM, int BN, int WM>
-__global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs p) {
-  using G = Tile<BM, BN, WM>;
-  constexpr int MI = G::MI, NI = G::NI, JA = G::JA, JB = G::JB, JS = G::JS, STAGE = G::STAGE;
+template <bool DOWN, typename T, class G>
+__global__ __launch_bounds__(G::THREADS) __attribute__((amdgpu_waves_per_eu(G::EU))) void mx_stream_kernel(MxArgs p) {
+  constexpr int BM = G::BM, BN = G::BN, MI = G::MI, NI = G::NI, JA = G::JA, JB = G::JB, J = G::J, JS = G::JS;
+  constexpr int STAGE = G::STAGE, S = G::STAGES;
   extern __shared__ __align__(16) char smem[];
   Place o;
   if (!find_tile(p, blockIdx.x, o)) return;
@@ -269,18 +276,18 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs p) {
   // row l / 8 of them, 16-byte slot l % 8
   uint32_t aoff[JA], boff[JB], soff[JS];
   const int whole = half / 128;  // steps below it lie in K with all their bytes
-  uint32_t tail_a = 0, tail_b = 0;  // in step `whole`: which instructions' pieces lie in K
+  uint32_t tail = 0;             // in step `whole`: which instructions' pieces lie in K
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
     const int r = (wave * JA + j) * 8 + (lane >> 3), c = slot_of(r, lane & 7) * 16;
     aoff[j] = row_of<DOWN>(p, o, r) * (uint32_t)half + c;
-    tail_a |= (uint32_t)(whole * 128 + c < half) << j;
+    tail |= (uint32_t)(whole * 128 + c < half) << j;
   }
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
     const int r = (wave * JB + j) * 8 + (lane >> 3), c = slot_of(r, lane & 7) * 16;
     boff[j] = weight_of<DOWN, BN>(p, o, r) * (uint32_t)half + c;
-    tail_b |= (uint32_t)(whole * 128 + c < half) << j;
+    tail |= (uint32_t)(whole * 128 + c < half) << (JA + j);
   }
 #pragma unroll
   for (int j = 0; j < JS; ++j) {
@@ -289,30 +296,32 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs p) {
               : r < BM + BN ? weight_of<DOWN, BN>(p, o, r - BM) * (uint32_t)p.lda
                             : mt::OUTSIDE;
   }
-  auto issue = [&](int t) {
-    const uint32_t st = lds0 + (uint32_t)(t % G::STAGES * STAGE);
-#pragma unroll
-    for (int j = 0; j < JA; ++j)
-      mt::copy16(t < whole || (tail_a >> j & 1) ? aoff[j] : mt::OUTSIDE, da, (uint32_t)t * 128u,
+  // instruction j (0 .. J-1) of step t
+  auto issue = [&](int t, int j) {
+    const uint32_t st = lds0 + (uint32_t)(t % S * STAGE);
+    const bool in = t < whole || (tail >> j & 1);
+    if (j < JA)
+      mt::copy16(in ? aoff[j < JA ? j : 0] : mt::OUTSIDE, da, (uint32_t)t * 128u,
                  st + (uint32_t)((wave * JA + j) * 1024));
-#pragma unroll
-    for (int j = 0; j < JB; ++j)
-      mt::copy16(t < whole || (tail_b >> j & 1) ? boff[j] : mt::OUTSIDE, db, (uint32_t)t * 128u,
-                 st + (uint32_t)(BM * 128 + (wave * JB + j) * 1024));
+    else
+      mt::copy16(in ? boff[j < JA ? 0 : j - JA] : mt::OUTSIDE, db, (uint32_t)t * 128u,
+                 st + (uint32_t)(BM * 128 + (wave * JB + j - JA) * 1024));
   };
-  const uint32_t sc0 = (uint32_t)(G::STAGES * STAGE);
+  constexpr uint32_t SC = (uint32_t)(S * STAGE);
   auto issue_scales = [&](int c) {
-    const uint32_t st = lds0 + sc0 + (uint32_t)((c & 1) * G::CHUNK);
 #pragma unroll
     for (int j = 0; j < JS; ++j)  // an instruction's 64 rows are all of one operand: BM is a multiple of 64
       mt::copy16(soff[j], (wave * JS + j) * 64 < BM ? dsa : dsb, (uint32_t)c * 16u,
-                 st + (uint32_t)((wave * JS + j) * 1024));
+                 lds0 + SC + (uint32_t)((c & 1) * G::CHUNK + (wave * JS + j) * 1024));
   };
   int arow[MI], brow[NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i) arow[i] = (wm * MI + i) * 32 + fr;
 #pragma unroll
   for (int i = 0; i < NI; ++i) brow[i] = block_row<DOWN, BN, NI>(wn, i) + fr;
+  int at[4];  // byte of a row in sub-step ks: rows are a multiple of 32 and fr
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) at[ks] = slot_of(fr, ks * 2 + fh) * 16;
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
@@ -320,50 +329,80 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs p) {
     for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
+  // scales: bytes 2 ks + fh of a row's eight are those of sub-step ks
+  uint32_t sa[MI][2], sb[NI][2];
+  auto read_scales = [&](int t, uint2 (&ra)[MI], uint2 (&rb)[NI]) {
+    const char* sc = smem + SC + ((t >> 1) & 1) * G::CHUNK + (t & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) ra[i] = *reinterpret_cast<const uint2*>(sc + arow[i] * 16);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) rb[i] = *reinterpret_cast<const uint2*>(sc + (BM + brow[i]) * 16);
+  };
+  auto take_scales = [&](const uint2 (&ra)[MI], const uint2 (&rb)[NI]) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i][0] = ra[i].x >> (8 * fh), sa[i][1] = ra[i].y >> (8 * fh);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) sb[i][0] = rb[i].x >> (8 * fh), sb[i][1] = rb[i].y >> (8 * fh);
+  };
+  uint4 xa[MI], xb[NI], ya[MI], yb[NI];
+  uint2 ra[MI], rb[NI];
   issue_scales(0);
-  issue(0);
-  if (KT > 1) issue(1);
-  for (int t = 0; t < KT; ++t) {
-    // step t and its scales landed (only step t + 1 may be in flight), and every
-    // wave is done with step t - 1, whose stage the refill takes
-    if (t + 1 < KT)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(JA + JB) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if ((t & 1) == 0 && t + 2 < KT) issue_scales(t / 2 + 1);
-    if (t + 2 < KT) issue(t + 2);
-    const char* st = smem + t % G::STAGES * STAGE;
-    const char* sc = smem + sc0 + ((t >> 1) & 1) * G::CHUNK + (t & 1) * 8;
-    // bytes 2 ks + fh of a row's eight are its scales in sub-step ks
-    uint32_t sa[MI][2], sb[NI][2];
+  if (KT > 2) issue_scales(1);
+  for (int t = 0; t < S && t < KT; ++t)
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2*>(sc + arow[i] * 16);
-      sa[i][0] = v.x >> (8 * fh), sa[i][1] = v.y >> (8 * fh);
-    }
+    for (int j = 0; j < J; ++j) issue(t, j);
+  if (S >= 3 && KT >= 3)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * J) : "memory");
+  else if (KT >= 2)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(J) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2*>(sc + (BM + brow[i]) * 16);
-      sb[i][0] = v.x >> (8 * fh), sb[i][1] = v.y >> (8 * fh);
-    }
+  for (int i = 0; i < NI; ++i) xb[i] = *reinterpret_cast<const uint4*>(smem + BM * 128 + brow[i] * 128 + at[0]);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint4 fa[MI], fb[NI];
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        fb[i] = *reinterpret_cast<const uint4*>(st + BM * 128 + brow[i] * 128 + slot_of(fr, ks * 2 + fh) * 16);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        fa[i] = *reinterpret_cast<const uint4*>(st + arow[i] * 128 + slot_of(fr, ks * 2 + fh) * 16);
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
-          acc[mi][ni] = mx_mfma_at(fb[ni], fa[mi], acc[mi][ni], sb[ni][ks >> 1], sa[mi][ks >> 1], ks & 1);
-    }
+  for (int i = 0; i < MI; ++i) xa[i] = *reinterpret_cast<const uint4*>(smem + arow[i] * 128 + at[0]);
+  read_scales(0, ra, rb);
+  take_scales(ra, rb);
+  // One sub-step: per block row mi, part of the next sub-step's fragments (KS of the
+  // stage at ST, if RD), NI MFMAs, the instructions j with j % MI = mi of step TI (if DO).
+#define MX_SUB(FA, FB, KS, NA, NB, ST, NKS, RD, DO, TI)                                                    \
+  _Pragma("unroll") for (int mi = 0; mi < MI; ++mi) {                                                      \
+    if (RD) {                                                                                              \
+      _Pragma("unroll") for (int q = mi * NI / MI; q < (mi + 1) * NI / MI; ++q)                            \
+        NB[q] = *reinterpret_cast<const uint4*>((ST) + BM * 128 + brow[q] * 128 + at[NKS]);                \
+      NA[mi] = *reinterpret_cast<const uint4*>((ST) + arow[mi] * 128 + at[NKS]);                           \
+    }                                                                                                      \
+    _Pragma("unroll") for (int ni = 0; ni < NI; ++ni)                                                      \
+      acc[mi][ni] = mx_mfma_at(FB[ni], FA[mi], acc[mi][ni], sb[ni][(KS) >> 1], sa[mi][(KS) >> 1], (KS)&1); \
+    if (DO) {                                                                                              \
+      _Pragma("unroll") for (int j = mi; j < J; j += MI) issue((TI), j);                                   \
+    }                                                                                                      \
+    __builtin_amdgcn_sched_barrier(0);                                                                     \
   }
+  for (int t = 0; t < KT; ++t) {
+    const char* st = smem + t % S * STAGE;
+    const char* nx = smem + (t + 1) % S * STAGE;
+    const bool more = t + 1 < KT;
+    MX_SUB(xa, xb, 0, ya, yb, st, 1, true, false, 0)
+    MX_SUB(ya, yb, 1, xa, xb, st, 2, true, false, 0)
+    MX_SUB(xa, xb, 2, ya, yb, st, 3, true, false, 0)
+    if (more) {
+      // lgkmcnt(0): this wave's reads of step t are done before its stage is refilled
+      if (S >= 3 && t + 2 < KT)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * J) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if ((t & 1) && t + 3 < KT) issue_scales((t + 3) / 2);
+      read_scales(t + 1, ra, rb);
+    }
+    MX_SUB(ya, yb, 3, xa, xb, nx, 0, more, t + S < KT, t + S)
+    if (more) take_scales(ra, rb);
+  }
+#undef MX_SUB
   put_tile<DOWN, T, BN, MI, NI>(p, o, wm * MI * 32, wn, acc);
 }
 
@@ -388,7 +427,7 @@ bool sizes_ok(int rows_x, int rows, int num_groups, int E, int d, int inter) {
   return rows >= 0 && rows_x >= 0 && num_groups >= 1 && num_groups <= 32768 && E >= 1 && E <= MOELB_MAX_E && d >= 32 &&
          d % 32 == 0 && d <= MAX_WIDTH && inter >= 32 && inter % 32 == 0 && inter <= MAX_WIDTH &&
          (size_t)rows_x * (d / 2) < mt::MAX_BYTES && (size_t)rows * (inter / 2) < mt::MAX_BYTES &&
-         (size_t)inter * d < mt::MAX_BYTES && (size_t)rows * d * 4 < mt::MAX_BYTES;
+         (size_t)inter * d < mt::MAX_BYTES;
 }
 
 bool aligned16(std::initializer_list<const void*> ps) {
@@ -408,13 +447,14 @@ int launch_quantize(const void* x, long long rows, int K, uint8_t* q, uint8_t* s
   return MOELB_OK;
 }
 
-constexpr int BN = 128;
+using Small = Tile<256,256,4,2,2>;
 
-template <bool DOWN, typename T, int BM, int WM>
-int launch_tiles(const MxArgs& p, size_t mtiles, hipStream_t s) {
-  using G = Tile<BM, BN, WM>;
-  if (!moelb_allow_lds(mx_stream_kernel<DOWN, T, BM, BN, WM>, G::LDS)) return MOELB_ELAUNCH;
-  hipLaunchKernelGGL((mx_stream_kernel<DOWN, T, BM, BN, WM>), dim3((unsigned)(mtiles * p.ntn + 8)), dim3(256), G::LDS, s,
+template <bool DOWN, typename T, class G>
+int launch_tiles(MxArgs p, size_t mtiles, hipStream_t s) {
+  if (!moelb_allow_lds(mx_stream_kernel<DOWN, T, G>, G::LDS)) return MOELB_ELAUNCH;
+  p.ntn = (p.N + G::BN - 1) / G::BN;
+  if (!DOWN) p.ntn = (p.inter + G::BN / 2 - 1) / (G::BN / 2);
+  hipLaunchKernelGGL((mx_stream_kernel<DOWN, T, G>), dim3((unsigned)(mtiles * p.ntn + 8)), dim3(G::THREADS), G::LDS, s,
                      p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
@@ -427,12 +467,12 @@ int run_ffn(const MxArgs& base, const void* x, int d, int inter, const uint8_t* 
   if (st != MOELB_OK) return st;
   MxArgs p = base;
   p.a = xq, p.as = xs, p.w = w13, p.ws = w13s;
-  p.K = d, p.N = 2 * inter, p.lda = mx::scale_bytes(d), p.ntn = (2 * inter + BN - 1) / BN;
-  st = launch_tiles<false, T, 64, 2>(p, mtiles, s);
+  p.K = d, p.N = 2 * inter, p.lda = mx::scale_bytes(d);
+  st = launch_tiles<false, T, Small>(p, mtiles, s);
   if (st != MOELB_OK) return st;
   p.a = p.q, p.as = p.qs, p.w = w2, p.ws = w2s;
-  p.K = inter, p.N = d, p.lda = p.ldq, p.ntn = (d + BN - 1) / BN;
-  return launch_tiles<true, T, 64, 2>(p, mtiles, s);
+  p.K = inter, p.N = d, p.lda = p.ldq;
+  return launch_tiles<true, T, Small>(p, mtiles, s);
 }
 
 }  // namespace

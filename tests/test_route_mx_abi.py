@@ -105,7 +105,7 @@ def mx_ffn(lib, **kw):
                                  dict(i=1 << 20), dict(dt=2), dict(rank=0, groups=7), dict(rank=2), dict(rank=0, G=0),
                                  dict(gather=P, gk=0), dict(off=N), dict(w13=N), dict(s13=N), dict(w2=N), dict(s2=N),
                                  dict(x=N), dict(y=N), dict(x=ODD), dict(w13=ODD), dict(s13=ODD), dict(w2=ODD),
-                                 dict(s2=ODD), dict(y=ODD), dict(rows=1 << 28, rows_x=1 << 28), dict(rows=1 << 24),
+                                 dict(s2=ODD), dict(y=ODD), dict(rows=1 << 28, rows_x=1 << 28), dict(rows=1 << 27),
                                  dict(rows_x=1 << 28), dict(d=1 << 17, i=1 << 15)], ids=str)
 def test_mx_ffn_refuses(lib, bad):
     assert mx_ffn(lib, **bad) == EINVAL

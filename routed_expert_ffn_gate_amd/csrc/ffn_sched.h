@@ -179,10 +179,9 @@ __device__ __forceinline__ long long block_incl_scan_256(long long v, long long*
 // single workgroup's serial tile writes were most of the schedule's time.
 constexpr int SCHED_FUSED_GROUPS = 4096;
 
-__global__ __launch_bounds__(256) void sched_rowmap_kernel(const int32_t* __restrict__ group_off, int num_groups,
-                                                           int E, int G, int rank, int rows, int BM,
-                                                           const int32_t* __restrict__ gather, int gather_k,
-                                                           int rows_x, FfnSched s) {
+__device__ __forceinline__ void sched_rowmap(int block, const int32_t* __restrict__ group_off, int num_groups, int E,
+                                             int G, int rank, int rows, int BM, const int32_t* __restrict__ gather,
+                                             int gather_k, int rows_x, const FfnSched& s) {
   __shared__ int goff[SCHED_FUSED_GROUPS + 1];
   __shared__ int gvb[SCHED_FUSED_GROUPS];
   __shared__ int eoff[MOELB_MAX_E + 1];
@@ -224,7 +223,7 @@ __global__ __launch_bounds__(256) void sched_rowmap_kernel(const int32_t* __rest
     toff[E] = (int)tincl;
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
+  if (block == 0) {
     for (int i = tid; i <= E; i += blockDim.x) s.eoff[i] = eoff[i];
     for (int g = tid; g < num_groups; g += blockDim.x) s.gvb[g] = gvb[g];
     if (tid == 0) *s.n_mtiles = toff[E];
@@ -241,7 +240,7 @@ __global__ __launch_bounds__(256) void sched_rowmap_kernel(const int32_t* __rest
     }
     if (s.order) write_order(eoff, E, s.order);
   }
-  const int v = blockIdx.x * blockDim.x + tid;
+  const int v = block * blockDim.x + tid;
   if (v >= eoff[E]) return;
   int lo = 0, hi = E - 1;  // eoff[0] = 0 <= v
   while (lo < hi) {
@@ -260,6 +259,13 @@ __global__ __launch_bounds__(256) void sched_rowmap_kernel(const int32_t* __rest
   s.rowmap[v] = q;
   const int src = gather ? gather[q] / gather_k : q;
   s.asrc[v] = (src >= 0 && src < rows_x) ? src : 0;
+}
+
+__global__ __launch_bounds__(256) void sched_rowmap_kernel(const int32_t* __restrict__ group_off, int num_groups,
+                                                           int E, int G, int rank, int rows, int BM,
+                                                           const int32_t* __restrict__ gather, int gather_k,
+                                                           int rows_x, FfnSched s) {
+  sched_rowmap(blockIdx.x, group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, s);
 }
 
 // Virtual -> physical row map, and the row of x each virtual row reads

@@ -39,10 +39,9 @@ __device__ __forceinline__ void load8_f32(const T* p, float* v) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void mx_quantize_kernel(const T* __restrict__ x, long long pieces, int per_row,
-                                                          int K, int ld, uint8_t* __restrict__ q,
-                                                          uint8_t* __restrict__ scales) {
-  const long long first = (long long)blockIdx.x * 256;
+__device__ __forceinline__ void quantize_pieces(int block, const T* __restrict__ x, long long pieces, int per_row, int K,
+                                                int ld, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  const long long first = (long long)block * 256;
   const long long row0 = first / per_row;  // the same in every thread
   const int at = (int)(first - row0 * per_row) + threadIdx.x;
   const long long row = row0 + at / per_row;
@@ -66,6 +65,29 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const T* __restrict__ 
   uint8_t* s = scales + row * ld;
   if ((c & 3) == 0) s[c >> 2] = (uint8_t)byte;
   for (int i = K / mx::BLOCK + c; i < ld; i += per_row) s[i] = 0;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(const T* __restrict__ x, long long pieces, int per_row, int K,
+                                                          int ld, uint8_t* __restrict__ q,
+                                                          uint8_t* __restrict__ scales) {
+  quantize_pieces(blockIdx.x, x, pieces, per_row, K, ld, q, scales);
+}
+
+// The FFN's schedule and its tokens' quantisation in one launch: the first `ns`
+// workgroups the one (it takes longer), the rest the other.  Two launches cost the
+// small calls 2 us more.
+template <typename T>
+__global__ __launch_bounds__(256) void mx_prepare_kernel(int ns, const int32_t* __restrict__ group_off, int num_groups,
+                                                         int E, int G, int rank, int rows, int BM,
+                                                         const int32_t* __restrict__ gather, int gather_k, int rows_x,
+                                                         FfnSched s, const T* __restrict__ x, long long pieces,
+                                                         int per_row, int K, int ld, uint8_t* __restrict__ q,
+                                                         uint8_t* __restrict__ scales) {
+  if ((int)blockIdx.x < ns)
+    sched_rowmap(blockIdx.x, group_off, num_groups, E, G, rank, rows, BM, gather, gather_k, rows_x, s);
+  else
+    quantize_pieces(blockIdx.x - ns, x, pieces, per_row, K, ld, q, scales);
 }
 
 template <typename T>
@@ -139,16 +161,6 @@ __device__ __forceinline__ uint2 act_block(const f32x16_t& g, const f32x16_t& u,
 }
 
 // A row's 32 columns to memory: 16 in this lane, 16 in the lane 32 away.
-__device__ __forceinline__ void store_block(uint16_t* o, const f32x16_t& a, int fh) {
-#pragma unroll
-  for (int q = 0; q < 4; q += 2) {
-    uint32_t x0 = bf16x2_pack(a[q * 4], a[q * 4 + 1]), x1 = bf16x2_pack(a[q * 4 + 2], a[q * 4 + 3]);
-    uint32_t y0 = bf16x2_pack(a[q * 4 + 4], a[q * 4 + 5]), y1 = bf16x2_pack(a[q * 4 + 6], a[q * 4 + 7]);
-    const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-    const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-    *reinterpret_cast<uint4*>(o + q * 8 + fh * 8) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
-  }
-}
 __device__ __forceinline__ void store_block(float* o, const f32x16_t& a, int fh) {
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -165,20 +177,20 @@ __device__ __forceinline__ void store_block(float* o, const f32x16_t& a, int fh)
 // buffer descriptors: a lane that asks for OUTSIDE gets zeros, which is how K ends
 // inside a step (a zero code times any scale but NaN is 0).
 //
-// A step is four sub-steps of 64 k.  The fragments of a sub-step are read while the
-// one before computes.  The barrier stands before the last sub-step: by then every
-// wave has read the step's stage, which the refill takes, and has its part of the
-// next step landed, whose first fragments the last sub-step reads.
+// A step is four sub-steps of 64 k.  The barrier stands behind the last sub-step's
+// reads: by then every wave has read the step's stage, which the refill takes, and
+// has its part of the next step landed.
 template <int BM_, int BN_, int NW_, int WM_, int STAGES_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, NW = NW_, WM = WM_, STAGES = STAGES_;
-  static constexpr int THREADS = NW * 64, EU = BM * BN / NW > 8192 ? 1 : 2;
+  static constexpr int THREADS = NW * 64, EU = BM * BN / NW > 4096 ? 1 : 2;
   static constexpr int WN = NW / WM, MI = BM / 32 / WM, NI = BN / 32 / WN;
   static constexpr int JA = BM / 8 / NW, JB = BN / 8 / NW;       // 1 KiB DMA instructions a wave and step
   static constexpr int J = JA + JB;
   static constexpr int JS = (BM + BN + 64 * NW - 1) / (64 * NW); // of scales, a wave and two steps
   static constexpr int STAGE = (BM + BN) * 128, CHUNK = JS * NW * 1024;
   static constexpr size_t LDS = (size_t)STAGES * STAGE + 2 * CHUNK;
+  static_assert(STAGES >= 2 && STAGES <= 4, "wait_stages");
 };
 
 __device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ (((row >> 1) ^ (row << 2)) & 7); }
@@ -198,10 +210,12 @@ __device__ __forceinline__ bool find_tile(const MxArgs& p, int bid, Place& o) {
   return true;
 }
 // Memory row of the tile's row r: through the row map (gate/up), or the virtual row.
+// Rows past the expert's end read some other row, and are not stored; the map's
+// entries past the last row of all are not set, so what it gives is kept in range.
 template <bool DOWN>
 __device__ __forceinline__ uint32_t row_of(const MxArgs& p, const Place& o, int r) {
-  const int v = o.v0 + r < o.end ? o.v0 + r : o.v0;  // rows past the expert's end repeat its first
-  return DOWN ? (uint32_t)v : (uint32_t)p.s.asrc[v];
+  const int v = min(o.v0 + r, p.rows - 1);
+  return DOWN ? (uint32_t)v : min((uint32_t)p.s.asrc[v], (uint32_t)p.rows_x - 1u);
 }
 // Weight row (of the expert's N) of the tile's weight row r; past the last: row 0.
 template <bool DOWN, int BN>
@@ -222,16 +236,49 @@ __device__ __forceinline__ int block_row(int wn, int ni) {
 // What a wave has in its accumulators to memory: block (mi, ni) is transposed,
 // lane -> row lane % 32, element j -> column (j / 4) * 8 + (lane / 32) * 4 + j % 4.
 // row0: the wave's first row of the tile.
+// spare: LDS of the wave alone, through which bf16 rows leave in whole 128-byte
+// lines (32-byte pieces straight from the accumulators: 308 against 285 us for the
+// down product of 131072 rows, d = 2048, inter = 1024).
 template <bool DOWN, typename T, int BN, int MI, int NI>
 __device__ __forceinline__ void put_tile(const MxArgs& p, const Place& o, int row0, int wn,
-                                         const f32x16_t (&acc)[MI][NI]) {
+                                         const f32x16_t (&acc)[MI][NI], char* spare) {
   const int lane = threadIdx.x & 63, fr = lane & 31, fh = lane >> 5;
+  if constexpr (DOWN && sizeof(T) == 2) {
+    static_assert(NI == 2, "a wave's 64 columns are a line");
+    const int c0 = o.nt * BN + wn * 64, chunk = lane & 7;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      int to[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int v = o.v0 + row0 + mi * 32 + i * 8 + (lane >> 3);
+        to[i] = v < o.end ? p.s.rowmap[v] : -1;
+      }
+      // row r of the block, 16-byte chunk c at c ^ (r % 8)
+#pragma unroll
+      for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16_t& a = acc[mi][ni];
+          *reinterpret_cast<uint2*>(spare + fr * 128 + (((ni * 4 + q) ^ (fr & 7)) * 16) + fh * 8) =
+              make_uint2(bf16x2_pack(a[q * 4], a[q * 4 + 1]), bf16x2_pack(a[q * 4 + 2], a[q * 4 + 3]));
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 3);
+        const uint4 x = *reinterpret_cast<const uint4*>(spare + r * 128 + ((chunk ^ (r & 7)) * 16));
+        if (to[i] >= 0 && c0 + chunk * 8 < p.N)
+          store_nt16(static_cast<uint16_t*>(p.y) + (size_t)to[i] * p.N + c0 + chunk * 8, x);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const int v = o.v0 + row0 + mi * 32 + fr;
     const bool in = v < o.end;
     if constexpr (DOWN) {
-      T* y = static_cast<T*>(p.y) + (size_t)(in ? p.s.rowmap[v] : 0) * p.N;
+      float* y = static_cast<float*>(p.y) + (size_t)(in ? p.s.rowmap[v] : 0) * p.N;
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
         const int c = o.nt * BN + block_row<true, BN, NI>(wn, ni);
@@ -255,8 +302,23 @@ __device__ __forceinline__ void put_tile(const MxArgs& p, const Place& o, int ro
   }
 }
 
+// Waits until only the newest n stages' loads (J a stage) may be in flight, and for
+// this wave's LDS reads.
+template <int J>
+__device__ __forceinline__ void wait_stages(int n) {
+  static_assert(3 * J < 64, "the counter has six bits");
+  if (n >= 3)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * J) : "memory");
+  else if (n == 2)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * J) : "memory");
+  else if (n == 1)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(J) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+
 template <bool DOWN, typename T, class G>
-__global__ __launch_bounds__(G::THREADS) __attribute__((amdgpu_waves_per_eu(G::EU))) void mx_stream_kernel(MxArgs p) {
+__global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) {
   constexpr int BM = G::BM, BN = G::BN, MI = G::MI, NI = G::NI, JA = G::JA, JB = G::JB, J = G::J, JS = G::JS;
   constexpr int STAGE = G::STAGE, S = G::STAGES;
   extern __shared__ __align__(16) char smem[];
@@ -329,81 +391,58 @@ __global__ __launch_bounds__(G::THREADS) __attribute__((amdgpu_waves_per_eu(G::E
     for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
-  // scales: bytes 2 ks + fh of a row's eight are those of sub-step ks
-  uint32_t sa[MI][2], sb[NI][2];
-  auto read_scales = [&](int t, uint2 (&ra)[MI], uint2 (&rb)[NI]) {
-    const char* sc = smem + SC + ((t >> 1) & 1) * G::CHUNK + (t & 1) * 8;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) ra[i] = *reinterpret_cast<const uint2*>(sc + arow[i] * 16);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) rb[i] = *reinterpret_cast<const uint2*>(sc + (BM + brow[i]) * 16);
-  };
-  auto take_scales = [&](const uint2 (&ra)[MI], const uint2 (&rb)[NI]) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i][0] = ra[i].x >> (8 * fh), sa[i][1] = ra[i].y >> (8 * fh);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) sb[i][0] = rb[i].x >> (8 * fh), sb[i][1] = rb[i].y >> (8 * fh);
-  };
-  uint4 xa[MI], xb[NI], ya[MI], yb[NI];
-  uint2 ra[MI], rb[NI];
   issue_scales(0);
   if (KT > 2) issue_scales(1);
   for (int t = 0; t < S && t < KT; ++t)
 #pragma unroll
     for (int j = 0; j < J; ++j) issue(t, j);
-  if (S >= 3 && KT >= 3)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * J) : "memory");
-  else if (KT >= 2)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(J) : "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_stages<J>(min(S, KT) - 1);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < NI; ++i) xb[i] = *reinterpret_cast<const uint4*>(smem + BM * 128 + brow[i] * 128 + at[0]);
-#pragma unroll
-  for (int i = 0; i < MI; ++i) xa[i] = *reinterpret_cast<const uint4*>(smem + arow[i] * 128 + at[0]);
-  read_scales(0, ra, rb);
-  take_scales(ra, rb);
-  // One sub-step: per block row mi, part of the next sub-step's fragments (KS of the
-  // stage at ST, if RD), NI MFMAs, the instructions j with j % MI = mi of step TI (if DO).
-#define MX_SUB(FA, FB, KS, NA, NB, ST, NKS, RD, DO, TI)                                                    \
-  _Pragma("unroll") for (int mi = 0; mi < MI; ++mi) {                                                      \
-    if (RD) {                                                                                              \
-      _Pragma("unroll") for (int q = mi * NI / MI; q < (mi + 1) * NI / MI; ++q)                            \
-        NB[q] = *reinterpret_cast<const uint4*>((ST) + BM * 128 + brow[q] * 128 + at[NKS]);                \
-      NA[mi] = *reinterpret_cast<const uint4*>((ST) + arow[mi] * 128 + at[NKS]);                           \
-    }                                                                                                      \
-    _Pragma("unroll") for (int ni = 0; ni < NI; ++ni)                                                      \
-      acc[mi][ni] = mx_mfma_at(FB[ni], FA[mi], acc[mi][ni], sb[ni][(KS) >> 1], sa[mi][(KS) >> 1], (KS)&1); \
-    if (DO) {                                                                                              \
-      _Pragma("unroll") for (int j = mi; j < J; j += MI) issue((TI), j);                                   \
-    }                                                                                                      \
-    __builtin_amdgcn_sched_barrier(0);                                                                     \
-  }
   for (int t = 0; t < KT; ++t) {
     const char* st = smem + t % S * STAGE;
-    const char* nx = smem + (t + 1) % S * STAGE;
-    const bool more = t + 1 < KT;
-    MX_SUB(xa, xb, 0, ya, yb, st, 1, true, false, 0)
-    MX_SUB(ya, yb, 1, xa, xb, st, 2, true, false, 0)
-    MX_SUB(xa, xb, 2, ya, yb, st, 3, true, false, 0)
-    if (more) {
-      // lgkmcnt(0): this wave's reads of step t are done before its stage is refilled
-      if (S >= 3 && t + 2 < KT)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * J) : "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      if ((t & 1) && t + 3 < KT) issue_scales((t + 3) / 2);
-      read_scales(t + 1, ra, rb);
+    const char* sc = smem + SC + ((t >> 1) & 1) * G::CHUNK + (t & 1) * 8;
+    // scales: bytes 2 ks + fh of a row's eight are those of sub-step ks
+    uint32_t sa[MI][2], sb[NI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + arow[i] * 16);
+      sa[i][0] = v.x >> (8 * fh), sa[i][1] = v.y >> (8 * fh);
     }
-    MX_SUB(ya, yb, 3, xa, xb, nx, 0, more, t + S < KT, t + S)
-    if (more) take_scales(ra, rb);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + (BM + brow[i]) * 16);
+      sb[i][0] = v.x >> (8 * fh), sb[i][1] = v.y >> (8 * fh);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint4 fa[MI], fb[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) fb[i] = *reinterpret_cast<const uint4*>(st + BM * 128 + brow[i] * 128 + at[ks]);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[i] = *reinterpret_cast<const uint4*>(st + arow[i] * 128 + at[ks]);
+      if (ks == 3 && t + 1 < KT) {
+        // lgkmcnt(0): this wave's reads of step t are done before its stage is refilled
+        wait_stages<J>(min(S - 2, KT - 2 - t));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if ((t & 1) && t + 3 < KT) issue_scales((t + 3) / 2);
+      }
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+          acc[mi][ni] = mx_mfma_at(fb[ni], fa[mi], acc[mi][ni], sb[ni][ks >> 1], sa[mi][ks >> 1], ks & 1);
+        if (ks == 3 && t + S < KT) {
+#pragma unroll
+          for (int j = mi; j < J; j += MI) issue(t + S, j);
+        }
+      }
+    }
   }
-#undef MX_SUB
-  put_tile<DOWN, T, BN, MI, NI>(p, o, wm * MI * 32, wn, acc);
+  // the stage of the last step but one: every wave is past it, and nothing refills it
+  char* spare = smem + (KT + S - 2) % S * STAGE + wave * (STAGE / G::NW);
+  put_tile<DOWN, T, BN, MI, NI>(p, o, wm * MI * 32, wn, acc, spare);
 }
 
 // ---------------------------------------------------------------- host
@@ -447,7 +486,14 @@ int launch_quantize(const void* x, long long rows, int K, uint8_t* q, uint8_t* s
   return MOELB_OK;
 }
 
-using Small = Tile<256,256,4,2,2>;
+// Tiles of 128 or 64 rows, both two workgroups a compute unit.  128 rows read the
+// weights half as often where experts have the rows; 64 waste less of the matrix
+// instructions and load three steps ahead where the weights' stream is the time.
+// d = 2048, inter = 768, 128 experts (128 | 64): 32 rows an expert 100 | 89 us, 64
+// rows 111 | 102, 128 rows 137 | 144; 64 experts, inter = 1024, 512 rows 190 | 235.
+using Large = Tile<128, 128, 4, 2, 2>;
+using Small = Tile<64, 128, 4, 2, 3>;
+bool large_rows(int rows, int E) { return (size_t)rows >= (size_t)96 * E; }
 
 template <bool DOWN, typename T, class G>
 int launch_tiles(MxArgs p, size_t mtiles, hipStream_t s) {
@@ -460,19 +506,47 @@ int launch_tiles(MxArgs p, size_t mtiles, hipStream_t s) {
   return MOELB_OK;
 }
 
-template <typename T>
-int run_ffn(const MxArgs& base, const void* x, int d, int inter, const uint8_t* w13, const uint8_t* w13s,
-            const uint8_t* w2, const uint8_t* w2s, uint8_t* xq, uint8_t* xs, hipStream_t s, size_t mtiles) {
-  int st = launch_quantize<T>(x, base.rows_x, d, xq, xs, s);
-  if (st != MOELB_OK) return st;
+template <typename T, class G>
+int launch_ffn(const MxArgs& base, int d, int inter, const uint8_t* w13, const uint8_t* w13s, const uint8_t* w2,
+               const uint8_t* w2s, const uint8_t* xq, const uint8_t* xs, hipStream_t s, size_t mtiles) {
   MxArgs p = base;
   p.a = xq, p.as = xs, p.w = w13, p.ws = w13s;
   p.K = d, p.N = 2 * inter, p.lda = mx::scale_bytes(d);
-  st = launch_tiles<false, T, Small>(p, mtiles, s);
+  const int st = launch_tiles<false, T, G>(p, mtiles, s);
   if (st != MOELB_OK) return st;
   p.a = p.q, p.as = p.qs, p.w = w2, p.ws = w2s;
   p.K = inter, p.N = d, p.lda = p.ldq;
-  return launch_tiles<true, T, Small>(p, mtiles, s);
+  return launch_tiles<true, T, G>(p, mtiles, s);
+}
+
+struct Groups {
+  const int32_t* off;
+  int num, E, G, rank;
+  const int32_t* gather;
+  int gather_k;
+};
+
+template <typename T>
+int run_ffn(const MxArgs& p, const Groups& g, const void* x, int d, int inter, const uint8_t* w13, const uint8_t* w13s,
+            const uint8_t* w2, const uint8_t* w2s, uint8_t* xq, uint8_t* xs, hipStream_t s) {
+  const bool large = large_rows(p.rows, g.E);
+  const int bm = large ? Large::BM : Small::BM;
+  const long long pieces = (long long)p.rows_x * (d / 8), nq = (pieces + 255) / 256;
+  const int ns = (p.rows + 255) / 256;
+  if (g.num <= SCHED_FUSED_GROUPS && ns + nq <= (long long)moelb_most_blocks(256)) {
+    hipLaunchKernelGGL((mx_prepare_kernel<T>), dim3((unsigned)(ns + nq)), dim3(256), 0, s, ns, g.off, g.num, g.E,
+                       g.G < 1 ? 1 : g.G, g.rank, p.rows, bm, g.gather, g.gather_k, p.rows_x, p.s,
+                       static_cast<const T*>(x), pieces, d / 8, d, mx::scale_bytes(d), xq, xs);
+    MOELB_CHECK_LAUNCH();
+  } else {
+    int st = launch_schedule(g.off, g.num, g.E, g.G, g.rank, p.rows, bm, g.gather, g.gather_k, p.rows_x, p.s, s);
+    if (st != MOELB_OK) return st;
+    st = launch_quantize<T>(x, p.rows_x, d, xq, xs, s);
+    if (st != MOELB_OK) return st;
+  }
+  const size_t mtiles = (size_t)(p.rows + bm - 1) / bm + g.E;
+  return large ? launch_ffn<T, Large>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles)
+               : launch_ffn<T, Small>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
 }
 
 }  // namespace
@@ -538,11 +612,9 @@ extern "C" int moelb_mx_grouped_ffn(const void* x, int rows_x, int rows, const i
   p.y = y;
   p.rows_x = rows_x, p.rows = rows, p.inter = inter, p.ldq = mx::scale_bytes(inter);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int st = launch_schedule(group_off, num_groups, E, G, rank, rows, SCHED_MIN_BM, gather, gather_k, rows_x, p.s, s);
-  if (st != MOELB_OK) return st;
+  const Groups g = {group_off, num_groups, E, G, rank, gather, gather_k};
   uint8_t* xq = reinterpret_cast<uint8_t*>(base + l.xq);
   uint8_t* xs = reinterpret_cast<uint8_t*>(base + l.xs);
-  return dtype == MOELB_BF16
-             ? run_ffn<uint16_t>(p, x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s, mtiles)
-             : run_ffn<float>(p, x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s, mtiles);
+  return dtype == MOELB_BF16 ? run_ffn<uint16_t>(p, g, x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s)
+                             : run_ffn<float>(p, g, x, d, inter, w13, w13_scales, w2, w2_scales, xq, xs, s);
 }

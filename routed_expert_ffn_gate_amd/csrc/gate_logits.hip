@@ -4,8 +4,11 @@
 // via Residual Workload Prediction"), section 2.1 and eq. 2-4: the router that
 // moelb_gate_topk fuses with its selection, here with the logits as the result.
 //
-// On the tile of mfma_tile.h: 128 tokens x 128 experts in bf16, 64 x 64 in fp32,
-// a router after the other.
+// Many tokens: the tile of mfma_tile.h, 128 tokens x 128 experts in bf16, 64 x 64 in
+// fp32; the tiles of the same tokens run side by side on one XCD, so its L2 serves
+// h to all but the first.  Few tokens: a tile of 16 x 16 by one workgroup, its waves
+// taking the products' k in turn, so that a router's rows are read by E / 16 compute
+// units at once.
 #include "mfma_tile.h"
 
 namespace {
@@ -19,57 +22,164 @@ struct LogitArgs {
   const float* b[2];
   float* z[2];
   int Ttok, d, E;
+  int nt;   // expert tiles of all routers
+  int vec;  // rows of z start at 16 bytes
 };
 
 // 8 logits of row t from column c: the bias added, columns past E left out.
-__device__ __forceinline__ void put_logits(float* z, const float* b, int E, size_t t, int c, const float* v) {
+template <typename T>
+__device__ __forceinline__ void put_logits(const LogitArgs<T>& p, float* z, const float* b, size_t t, int c,
+                                           const float* v) {
+  float* o = z + t * p.E + c;
+  if (p.vec) {
+#pragma unroll
+    for (int h = 0; h < 8; h += 4)
+      if (c + h < p.E) {
+        float4 x = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+        if (b) x.x += b[c + h], x.y += b[c + h + 1], x.z += b[c + h + 2], x.w += b[c + h + 3];
+        *reinterpret_cast<float4*>(o + h) = x;
+      }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c + i < E) z[t * E + c + i] = v[i] + (b ? b[c + i] : 0.f);
+    if (c + i < p.E) o[i] = v[i] + (b ? b[c + i] : 0.f);
+}
+
+// Workgroup b's token tile, router and expert tile: XCD b % 8 (workgroups go round)
+// takes every eighth token tile, with all of its expert tiles in turn.
+struct Where {
+  int m, router, n;
+};
+template <typename T>
+__device__ __forceinline__ Where where_of(const LogitArgs<T>& p, int b, int per_router) {
+  const int j = b >> 3, n = j % p.nt;
+  return {(j / p.nt) * 8 + (b & 7), n / per_router, n % per_router};
 }
 
 __global__ __launch_bounds__(mt::THREADS) void logits_kernel(LogitArgs<uint16_t> p) {
   extern __shared__ __align__(16) char smem[];
   uint16_t* lds = reinterpret_cast<uint16_t*>(smem);
-  const int m0 = blockIdx.x * LB, n0 = blockIdx.y * LB;
-  const uint16_t* w = blockIdx.z ? p.w[1] : p.w[0];
-  const float* b = blockIdx.z ? p.b[1] : p.b[0];
-  float* z = blockIdx.z ? p.z[1] : p.z[0];
+  const Where at = where_of(p, blockIdx.x, (p.E + LB - 1) / LB);
+  const int m0 = at.m * LB, n0 = at.n * LB;
+  if (m0 >= p.Ttok) return;
+  const uint16_t* w = at.router ? p.w[1] : p.w[0];
+  const float* b = at.router ? p.b[1] : p.b[0];
+  float* z = at.router ? p.z[1] : p.z[0];
   mt::RowOp<LF> oa, ob;
   oa.init(p.h, (uint32_t)((size_t)p.Ttok * p.d * 2), p.d, p.d, [&](int r) { return min(m0 + r, p.Ttok - 1); });
   ob.init(w, (uint32_t)((size_t)p.E * p.d * 2), p.d, p.d, [&](int r) { return min(n0 + r, p.E - 1); });
+  const int KT = (p.d + mt::BK - 1) / mt::BK;
   f32x16_t acc[LF][LF];
-  mt::k_loop<LF, false>(lds, oa, ob, (p.d + mt::BK - 1) / mt::BK, acc);
+  mt::k_loop<LF, false>(lds, oa, ob, KT, acc, at.m % KT);
   mt::drain<LF, false>(lds, acc, [&](int r, int c, const float* v) {
-    if (m0 + r < p.Ttok) put_logits(z, b, p.E, m0 + r, n0 + c, v);
+    if (m0 + r < p.Ttok) put_logits(p, z, b, m0 + r, n0 + c, v);
   });
 }
 
 __global__ __launch_bounds__(mt::S_THREADS) void logits_f32_kernel(LogitArgs<float> p) {
   __shared__ __align__(16) float lds[mt::STile<64>::FLOATS];
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  const float* w = blockIdx.z ? p.w[1] : p.w[0];
-  const float* b = blockIdx.z ? p.b[1] : p.b[0];
-  float* z = blockIdx.z ? p.z[1] : p.z[0];
+  const Where at = where_of(p, blockIdx.x, (p.E + 63) / 64);
+  const int m0 = at.m * 64, n0 = at.n * 64;
+  if (m0 >= p.Ttok) return;
+  const float* w = at.router ? p.w[1] : p.w[0];
+  const float* b = at.router ? p.b[1] : p.b[0];
+  float* z = at.router ? p.z[1] : p.z[0];
   f32x16_t acc;
   auto pa = [&](int r, int k) { return m0 + r < p.Ttok ? p.h + (size_t)(m0 + r) * p.d + k : nullptr; };
   auto pb = [&](int r, int k) { return n0 + r < p.E ? w + (size_t)(n0 + r) * p.d + k : nullptr; };
   mt::k_loop_f32<64, false, false>(lds, pa, pb, p.d, acc);
   mt::drain_f32<64, false>(lds, acc, [&](int r, int c, const float* v) {
-    if (m0 + r < p.Ttok) put_logits(z, b, p.E, m0 + r, n0 + c, v);
+    if (m0 + r < p.Ttok) put_logits(p, z, b, m0 + r, n0 + c, v);
   });
 }
 
-int launch(const LogitArgs<uint16_t>& p, int routers, hipStream_t s) {
-  if (!moelb_allow_lds(logits_kernel, mt::lds_bytes<LF>())) return MOELB_ELAUNCH;
-  hipLaunchKernelGGL(logits_kernel, dim3((p.Ttok + LB - 1) / LB, (p.E + LB - 1) / LB, routers), dim3(mt::THREADS),
-                     mt::lds_bytes<LF>(), s, p);
+// Few tokens.  A lane holds 16 bytes of a row: k (4 s + lane / 16) x 16 bytes of step
+// s, token or expert lane % 16.  bf16: one v_mfma_f32_16x16x32_bf16 a step.  fp32: four
+// v_mfma_f32_16x16x4_f32, the i-th with the i-th float of every lane (both operands
+// take their k in the same order).  Wave w takes the steps w, w + FEW_WAVES, ..., four
+// loads ahead of their use; the waves' sums are added in order.
+constexpr int FEW_WAVES = 16;
+
+template <typename T>
+__global__ __launch_bounds__(FEW_WAVES * MOELB_WAVE) void logits_few_kernel(LogitArgs<T> p) {
+  __shared__ float red[FEW_WAVES][256];
+  constexpr int CH = 16 / (int)sizeof(T), AHEAD = 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+  const T* w = blockIdx.z ? p.w[1] : p.w[0];
+  const float* b = blockIdx.z ? p.b[1] : p.b[0];
+  float* z = blockIdx.z ? p.z[1] : p.z[0];
+  const int r = lane & 15, k0 = (lane >> 4) * CH;
+  const T* hr = p.h + (size_t)min(t0 + r, p.Ttok - 1) * p.d;
+  const T* wr = w + (size_t)min(e0 + r, p.E - 1) * p.d;
+  const int steps = (p.d + 4 * CH - 1) / (4 * CH);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = wave; s0 < steps; s0 += FEW_WAVES * AHEAD) {
+    uint4 x[AHEAD], y[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = (s0 + i * FEW_WAVES) * 4 * CH + k0;
+      const bool in = k < p.d;  // d is a multiple of CH
+      x[i] = in ? *reinterpret_cast<const uint4*>(hr + k) : make_uint4(0, 0, 0, 0);
+      y[i] = in ? *reinterpret_cast<const uint4*>(wr + k) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x[i]),
+                                                      __builtin_bit_cast(bf16x8_t, y[i]), acc, 0, 0, 0);
+      } else {
+        const f32x4_t u = __builtin_bit_cast(f32x4_t, x[i]), v = __builtin_bit_cast(f32x4_t, y[i]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(u[q], v[q], acc, 0, 0, 0);
+      }
+    }
+  }
+  *reinterpret_cast<f32x4_t*>(&red[wave][lane * 4]) = acc;  // token (lane / 16) * 4 + i, expert lane % 16
+  __syncthreads();
+  const int tok = threadIdx.x >> 4, e = threadIdx.x & 15;
+  if (threadIdx.x < 256 && t0 + tok < p.Ttok && e0 + e < p.E) {
+    float v = b ? b[e0 + e] : 0.f;
+    const int at = ((tok >> 2) * 16 + e) * 4 + (tok & 3);
+#pragma unroll
+    for (int i = 0; i < FEW_WAVES; ++i) v += red[i][at];
+    z[(size_t)(t0 + tok) * p.E + e0 + e] = v;
+  }
+}
+
+// Whether a call runs faster in tiles of 16 x 16: up to about three of them a compute
+// unit (fp32: six), where the large tiles would leave most units without work.  us,
+// small | large tiles, bf16, both routers: 1 token, d = 4096, 128 experts 6.5 | 23.8;
+// 512 tokens, d = 2048, 128 experts (512 tiles) 9.6 | 17.6; 1024 tokens, d = 4096, 128
+// experts (1024) 31 | 28; 2048 tokens, d = 2048, 128 experts (2048) 31 | 18.  fp32:
+// 1024 tokens, d = 4096, 128 experts 61 | 92; 2048 tokens, d = 2048, 128 experts 59 | 49.
+template <typename T>
+bool few_tokens(const LogitArgs<T>& p, int routers) {
+  const size_t tiles = ((size_t)p.Ttok + 15) / 16 * ((p.E + 15) / 16) * routers;
+  return tiles <= (sizeof(T) == 2 ? 768u : 1536u);
+}
+
+template <typename T>
+int launch_few(const LogitArgs<T>& p, int routers, hipStream_t s) {
+  hipLaunchKernelGGL((logits_few_kernel<T>), dim3((p.E + 15) / 16, (p.Ttok + 15) / 16, routers),
+                     dim3(FEW_WAVES * MOELB_WAVE), 0, s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
-int launch(const LogitArgs<float>& p, int routers, hipStream_t s) {
-  hipLaunchKernelGGL(logits_f32_kernel, dim3((p.Ttok + 63) / 64, (p.E + 63) / 64, routers), dim3(mt::S_THREADS), 0, s,
-                     p);
+
+int launch(LogitArgs<uint16_t> p, int routers, hipStream_t s) {
+  if (!moelb_allow_lds(logits_kernel, mt::lds_bytes<LF>())) return MOELB_ELAUNCH;
+  const int m = (p.Ttok + LB - 1) / LB;
+  p.nt = (p.E + LB - 1) / LB * routers;
+  hipLaunchKernelGGL(logits_kernel, dim3((m + 7) / 8 * 8 * p.nt), dim3(mt::THREADS), mt::lds_bytes<LF>(), s, p);
+  MOELB_CHECK_LAUNCH();
+  return MOELB_OK;
+}
+int launch(LogitArgs<float> p, int routers, hipStream_t s) {
+  const int m = (p.Ttok + 63) / 64;
+  p.nt = (p.E + 63) / 64 * routers;
+  hipLaunchKernelGGL(logits_f32_kernel, dim3((m + 7) / 8 * 8 * p.nt), dim3(mt::S_THREADS), 0, s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
@@ -79,13 +189,13 @@ int launch(const LogitArgs<float>& p, int routers, hipStream_t s) {
 template <typename T>
 int run_parts(LogitArgs<T> p, int T_all, int routers, hipStream_t s) {
   const size_t most = (mt::MAX_BYTES - 1) / ((size_t)p.d * sizeof(T));
-  const int part = (int)(most < (1u << 24) ? (most > 128 ? most / 128 * 128 : most) : 1u << 24);
+  const int part = (int)(most < (1u << 22) ? (most > 128 ? most / 128 * 128 : most) : 1u << 22);
   for (long long t0 = 0; t0 < T_all; t0 += part) {
     LogitArgs<T> q = p;
     q.Ttok = (int)(T_all - t0 < part ? T_all - t0 : part);
     q.h += t0 * p.d;
     for (int r = 0; r < routers; ++r) q.z[r] += t0 * p.E;
-    const int st = launch(q, routers, s);
+    const int st = few_tokens(q, routers) ? launch_few(q, routers, s) : launch(q, routers, s);
     if (st != MOELB_OK) return st;
   }
   return MOELB_OK;
@@ -106,7 +216,8 @@ extern "C" int moelb_gate_logits(const void* h, int T, int d, int E, int dtype, 
   auto go = [&](auto* t) {
     using U = std::remove_pointer_t<decltype(t)>;
     LogitArgs<U> p = {static_cast<const U*>(h), {static_cast<const U*>(w_cur), static_cast<const U*>(w_next)},
-                      {b_cur, b_next}, {z, z_next}, 0, d, E};
+                      {b_cur, b_next}, {z, z_next}, 0, d, E, 0, 0};
+    p.vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(z) | reinterpret_cast<uintptr_t>(z_next)) & 15) == 0;
     return run_parts<U>(p, T, w_next ? 2 : 1, static_cast<hipStream_t>(stream));
   };
   return dtype == MOELB_BF16 ? go(static_cast<uint16_t*>(nullptr)) : go(static_cast<float*>(nullptr));

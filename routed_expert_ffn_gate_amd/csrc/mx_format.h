@@ -36,6 +36,15 @@ __device__ __forceinline__ uint32_t codes4(uint32_t old, float a, float b, float
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, s(c), s(d), 1.0f, HI ? 3 : 1);
 }
 
+// The eight numbers in w, times f.
+__device__ __forceinline__ void values8(uint32_t w, float f, float* v) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+  const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+  v[0] = a.x * f, v[1] = a.y * f, v[2] = b.x * f, v[3] = b.y * f;
+  v[4] = c.x * f, v[5] = c.y * f, v[6] = d.x * f, v[7] = d.y * f;
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 }  // namespace mx

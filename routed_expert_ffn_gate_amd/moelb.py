@@ -504,9 +504,9 @@ def moelb_mx_scale_bytes(K) -> int:
 
 def _mx_args(name, x, q, scales, dev):
     *lead, K = x.shape
-    ld = moelb_mx_scale_bytes(K)
-    if ld == 0:
+    if K < 32 or K % 32:
         raise MoelbError(f"{name}: rows of {K} elements, not a multiple of 32")
+    ld = (K // 32 + 15) // 16 * 16  # moelb_mx_scale_bytes(K)
     u8 = torch.uint8
     return (x.numel() // K, K, dtype_code(x), _arg(name, "x", x, x.shape, x.dtype, dev),
             _arg(name, "q", q, (*lead, K // 2), u8, dev), _arg(name, "scales", scales, (*lead, ld), u8, dev))

@@ -22,6 +22,11 @@ respect to the hidden states, the router and the experts (shared expert
 included).  Serving requests with adapters of their own: ``step(...,
 shared_adapters=...)`` runs the shared expert's two projections with each
 token's low-rank adapters beside them.
+
+Routers with another rule than the fused gate's (``router=RouterRule(...)``): the
+logits of both routers, then the rule on them, for the picks, the lookahead and
+the gradient.  ``mx_weights=True``: the experts (shared expert included) in
+microscaled 4-bit floating point; the steps take ``MxWeights``.
 """
 from __future__ import annotations
 
@@ -62,6 +67,48 @@ def pack_expert_weights(w: torch.Tensor, stream=None) -> torch.Tensor:
     p = torch.empty_like(w)
     M.moelb_pack_weights(w, p, stream=stream)
     return p
+
+
+@dataclass
+class MxWeights:
+    """Weights in MX 4-bit floating point, as moelb_mx_quantize lays them out."""
+    q: torch.Tensor       # [..., rows, K / 2] uint8
+    scales: torch.Tensor  # [..., rows, moelb_mx_scale_bytes(K)] uint8
+
+
+def quantize_expert_weights(w: torch.Tensor, stream=None) -> MxWeights:
+    """Expert weights ([E, rows, K] or one expert's [rows, K], bf16 or fp32) for a
+    layer built with mx_weights=True: done once, when the weights are loaded."""
+    K = w.shape[-1]
+    u8 = dict(dtype=torch.uint8, device=w.device)
+    m = MxWeights(torch.empty((*w.shape[:-1], K // 2), **u8),
+                  torch.empty((*w.shape[:-1], M.moelb_mx_scale_bytes(K)), **u8))
+    M.moelb_mx_quantize(w, m.q, m.scales, stream=stream)
+    return m
+
+
+@dataclass(frozen=True)
+class RouterRule:
+    """How picks and weights follow from the logits (moelb_route): softmax or
+    sigmoid scores, the best ``topk_groups`` of ``groups`` groups of experts by the
+    sum of their ``group_top`` best, weights renormalised over the picks, scaled."""
+    score: str = "softmax"
+    groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 1
+    renorm: bool = False
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError(self.score)
+
+    def weights_kw(self):
+        code = M.MOELB_SCORE_SIGMOID if self.score == "sigmoid" else M.MOELB_SCORE_SOFTMAX
+        return dict(score=code, renorm=self.renorm, scale=self.scale)
+
+    def kw(self):
+        return dict(groups=self.groups, topk_groups=self.topk_groups, group_top=self.group_top, **self.weights_kw())
 
 
 class HipEvents:
@@ -149,7 +196,8 @@ class MoELayer:
 
     def __init__(self, T, d, E, k, inter, G, N, L, dtype, device="cuda", shared_inter=0, passes=12,
                  gather_rows=True, materialize_x=False, balancer="libra", fb_tau=0, fb_gamma=None,
-                 fb_budget=None, packed_weights=False, overlap_split=None):
+                 fb_budget=None, packed_weights=False, overlap_split=None, router: Optional[RouterRule] = None,
+                 mx_weights=False):
         """balancer "libra": replication plan (N slots, L locality imports)
         and the per-step split; "freebalance": expert swaps instead (no
         replicas; at most fb_budget swaps per rank, default N; threshold
@@ -158,7 +206,16 @@ class MoELayer:
         are in moelb_pack_weights' layout.  overlap_split: run the split
         beside the local half of the permutation (default: wherever the
         permutation is not a single launch anyway, i.e. more than 8192 pairs,
-        E*G > 2048 or rows copied)."""
+        E*G > 2048 or rows copied).  router: the rule of the routers (default: the
+        fused gate's, softmax over all experts and plain top-k); the steps then take
+        its balance biases.  mx_weights: the weights passed to the steps are
+        MxWeights (inference only; d, inter and shared_inter multiples of 32)."""
+        if mx_weights and packed_weights:
+            raise ValueError("packed_weights is a layout of bf16 weights")
+        if mx_weights and (d % 32 or inter % 32 or shared_inter % 32):
+            raise ValueError("mx_weights need d, inter and shared_inter in multiples of 32")
+        self.router = router
+        self.mx = mx_weights
         self.T, self.d, self.E, self.k, self.inter = T, d, E, k, inter
         self.ffn_opt = M.MOELB_FFN_PACKED_WEIGHTS if packed_weights else 0
         self.G, self.N, self.L, self.passes = G, N, L, passes
@@ -198,8 +255,14 @@ class MoELayer:
         code = M.MOELB_BF16 if dtype == "bf16" else M.MOELB_F32
         self.ws_perm = torch.empty((max(1, M.moelb_permute_workspace_bytes(T, k, E, G)),), dtype=torch.uint8,
                                    device=self.dev)
-        self.ws_ffn = torch.empty((max(1, M.moelb_grouped_ffn_workspace_bytes(P, 2 * G * E, E, d, inter, code)),),
-                                  dtype=torch.uint8, device=self.dev)
+        if self.mx:
+            ffn_bytes = M.moelb_mx_grouped_ffn_workspace_bytes(T if gather_rows else P, P, 2 * G * E, E, d, inter)
+        else:
+            ffn_bytes = M.moelb_grouped_ffn_workspace_bytes(P, 2 * G * E, E, d, inter, code)
+        self.ws_ffn = torch.empty((max(1, ffn_bytes),), dtype=torch.uint8, device=self.dev)
+        # logits of the current and the lookahead router
+        self.z, self.z_next = (torch.empty((2, T, E), dtype=torch.float32, device=self.dev) if router is not None
+                               else (None, None))
         self.side = torch.cuda.Stream(device=self.dev)  # default priority
         self.ev_gate = torch.cuda.Event()
         self.ev_side = torch.cuda.Event()
@@ -231,27 +294,51 @@ class MoELayer:
         self._adapter_mid = None
         self.ws_shared = None
         if shared_inter > 0:
-            self.ws_shared = torch.empty((M.moelb_grouped_ffn_workspace_bytes(T, 1, 1, d, shared_inter, code),),
-                                         dtype=torch.uint8, device=self.dev)
+            shared_bytes = (M.moelb_mx_grouped_ffn_workspace_bytes(T, T, 1, 1, d, shared_inter) if self.mx else
+                            M.moelb_grouped_ffn_workspace_bytes(T, 1, 1, d, shared_inter, code))
+            self.ws_shared = torch.empty((max(1, shared_bytes),), dtype=torch.uint8, device=self.dev)
 
     # -- stages ---------------------------------------------------------------
 
-    def predict_plan(self, h_prev, w_cur, b_cur, home, replica_out, stream=None):
+    def _check_bias(self, *biases):
+        if self.router is None and any(b is not None for b in biases):
+            raise ValueError("a balance bias needs a layer with a router rule")
+
+    def _gate(self, h, w_cur, b_cur, w_next, b_next, bias, bias_next, stream):
+        """Picks and weights of the step, and the lookahead's picks."""
+        if self.router is None:
+            M.moelb_gate_topk(h, w_cur, b_cur, w_next, b_next, self.idx, self.wts, self.gap, self.idx_next,
+                              stream=stream)
+            return
+        kw = self.router.kw()
+        M.moelb_gate_logits(h, w_cur, b_cur, w_next, b_next, self.z, self.z_next, stream=stream)
+        M.moelb_route(self.z, self.idx, self.wts, self.gap, bias=bias, stream=stream, **kw)
+        M.moelb_route(self.z_next, self.idx_next, None, bias=bias_next, stream=stream, **kw)
+
+    def _early_gate(self, h_prev, w_cur, b_cur, bias, stream):
+        """This layer's router on the previous hidden states, into idx_next."""
+        self._check_bias(bias)
+        self._kept = False  # the gate writes the layer's wts
+        if self.router is None:
+            M.moelb_gate_topk(h_prev, w_cur, b_cur, None, None, self.idx_next, self.wts, None, None, stream=stream)
+            return
+        M.moelb_gate_logits(h_prev, w_cur, b_cur, None, None, self.z_next, stream=stream)
+        M.moelb_route(self.z_next, self.idx_next, None, bias=bias, stream=stream, **self.router.kw())
+
+    def predict_plan(self, h_prev, w_cur, b_cur, home, replica_out, stream=None, route_bias=None):
         """Prologue: the previous step's lookahead for this layer (gate of this
         layer on the previous hidden states), its histogram and plan."""
-        self._kept = False  # the gate writes the layer's wts
-        M.moelb_gate_topk(h_prev, w_cur, b_cur, None, None, self.idx_next, self.wts, None, None, stream=stream)
+        self._early_gate(h_prev, w_cur, b_cur, route_bias, stream)
         M.moelb_histogram(self.idx_next, self.G, self.counts_next, stream=stream)
         M.moelb_plan(self.counts_next, home, self.L, replica_out, None, stream=stream)
         M.moelb_split_schedule(home, replica_out, self.sched_cur, self.G, stream=stream)
 
-    def predict_placement(self, h_prev, w_cur, b_cur, home_base, home_out, stream=None):
+    def predict_placement(self, h_prev, w_cur, b_cur, home_base, home_out, stream=None, route_bias=None):
         """FreeBalance prologue: the early router (this layer's gate on the
         previous hidden states), its histogram, and the swaps from the base
         placement ``home_base`` (kept as the next layer's starting placement)
         into ``home_out``."""
-        self._kept = False
-        M.moelb_gate_topk(h_prev, w_cur, b_cur, None, None, self.idx_next, self.wts, None, None, stream=stream)
+        self._early_gate(h_prev, w_cur, b_cur, route_bias, stream)
         M.moelb_histogram(self.idx_next, self.G, self.counts_next, stream=stream)
         self.home_base = home_base
         self._plan_swaps(home_out, stream)
@@ -284,6 +371,10 @@ class MoELayer:
         if self.shared is not None and (shared_w13 is None or shared_w2 is None):
             raise ValueError("the layer has a shared expert: its weights shared_w13 and shared_w2 are missing")
 
+    def _check_mx(self, *weights):
+        if any(w is not None and isinstance(w, MxWeights) != self.mx for w in weights):
+            raise ValueError("the layer takes MxWeights" if self.mx else "MxWeights need a layer with mx_weights=True")
+
     def _may_make(self, what):
         """Buffers made by a step are made outside of a capture: their constants
         are written once, not at every replay."""
@@ -313,7 +404,8 @@ class MoELayer:
                      dw=torch.empty((E, d), **t), db=torch.empty((E,), **f),
                      dw13=torch.empty((E, 2 * i, d), **t), dw2=torch.empty((E, d, i), **t),
                      ws=bytes_(M.moelb_grouped_ffn_backward_workspace_bytes(P, 2 * self.G * E, E, d, i, code)),
-                     ws_gate=bytes_(M.moelb_gate_backward_workspace_bytes(T, d, E, code)))
+                     ws_gate=bytes_((M.moelb_gate_backward_workspace_bytes if self.router is None else
+                                     M.moelb_route_backward_workspace_bytes)(T, d, E, code)))
             if si > 0:
                 b.update(z_shared=torch.empty((T, 2 * si), **f), dx_shared=torch.empty((T, d), **t),
                          dw13_shared=torch.empty((2 * si, d), **t), dw2_shared=torch.empty((d, si), **t),
@@ -329,16 +421,21 @@ class MoELayer:
 
     def _ffn(self, h, w13, w2, mark=None, stream=None, train=False):
         """The grouped FFN over every group; with ``mark``, its three stages
-        are launched apart and marks 8..11 recorded around them (train: the
-        whole call between marks 9 and 10)."""
+        are launched apart and marks 8..11 recorded around them (train and
+        mx_weights: the whole call between marks 9 and 10)."""
         x = h if self.gather_rows else self.x_perm
         kw = dict(G=self.G, stream=stream, **self._gather())
-        if train:
-            b = self._train_buffers()
+        if train or self.mx:
+            b = self._train_buffers() if train else None
             if mark is not None:
                 mark(8)
                 mark(9)
-            M.moelb_grouped_ffn_train(x, self.P, self.group_off, self.E, w13, w2, self.ws_ffn, b["z"], self.y, **kw)
+            if self.mx:
+                M.moelb_mx_grouped_ffn(x, self.P, self.group_off, self.E, w13.q, w13.scales, w2.q, w2.scales,
+                                       self.ws_ffn, self.y, **kw)
+            else:
+                M.moelb_grouped_ffn_train(x, self.P, self.group_off, self.E, w13, w2, self.ws_ffn, b["z"], self.y,
+                                          **kw)
             if mark is not None:
                 mark(10)
                 mark(11)
@@ -356,6 +453,10 @@ class MoELayer:
     def _shared_ffn(self, h, shared_w13, shared_w2, stream, train=False, adapters=None):
         if adapters is not None:
             self._shared_with_adapters(h, shared_w13, shared_w2, adapters, stream)
+            return
+        if self.mx:
+            M.moelb_mx_grouped_ffn(h, self.T, self.shared_off, 1, shared_w13.q, shared_w13.scales, shared_w2.q,
+                                   shared_w2.scales, self.ws_shared, self.shared, stream=stream)
             return
         if train:
             M.moelb_grouped_ffn_train(h, self.T, self.shared_off, 1, shared_w13, shared_w2, self.ws_shared,
@@ -400,8 +501,9 @@ class MoELayer:
 
     def step(self, h, w_cur, b_cur, w_next, b_next, home, replica_cur, w13, w2, shared_w13=None, shared_w2=None,
              stream=None, events: Optional[HipEvents] = None, ev_base: int = 0, sched=None, train: bool = False,
-             shared_adapters: Optional[SharedAdapters] = None) -> StepOut:
-        """One layer step.  ``train``: keep what ``backward`` needs (row-major
+             shared_adapters: Optional[SharedAdapters] = None, route_bias=None, route_bias_next=None) -> StepOut:
+        """One layer step.  ``route_bias``, ``route_bias_next``: the balance biases
+        [E] of the two routers, with a router rule.  ``train``: keep what ``backward`` needs (row-major
         weights only).  ``shared_adapters``: the shared expert with each
         token's low-rank adapters (row-major weights only; not with ``train``).
         The first step of either kind, and one with adapters of more rank than
@@ -412,8 +514,10 @@ class MoELayer:
         side stream's work. ``sched``: the split's round schedule for
         ``replica_cur`` (default: the one ``predict_plan`` or ``advance`` left
         in force)."""
-        if self.ffn_opt and (train or shared_adapters is not None):
+        if (self.ffn_opt or self.mx) and (train or shared_adapters is not None):
             raise ValueError("train and shared_adapters take row-major weights")
+        self._check_bias(route_bias, route_bias_next)
+        self._check_mx(w13, w2, shared_w13, shared_w2)
         if shared_adapters is not None and (train or self.shared is None):
             raise ValueError("shared_adapters need a shared expert, and are not trained")
         if train or shared_adapters is not None:
@@ -431,7 +535,7 @@ class MoELayer:
                 ev.record(ev_base + i, st if st is not None else s0)
 
         mark(0)
-        M.moelb_gate_topk(h, w_cur, b_cur, w_next, b_next, self.idx, self.wts, self.gap, self.idx_next, stream=s0)
+        self._gate(h, w_cur, b_cur, w_next, b_next, route_bias, route_bias_next, s0)
         self.ev_gate.record(s0)
         # side stream: lookahead histogram and the next layer's plan
         self.side.wait_event(self.ev_gate)
@@ -506,8 +610,12 @@ class MoELayer:
         M.moelb_combine_backward(dout, self.y, self.pos, self.wts, b["dy"], b["dwts"], stream=s0)
         M.moelb_grouped_ffn_backward(b["dy"], x, self.P, self.group_off, self.E, w13, w2, b["z"], b["ws"], b["dx"],
                                      b["dw13"], b["dw2"], G=self.G, stream=s0, **self._gather())
-        M.moelb_gate_backward(h, w_cur, b_cur, self.idx, b["dwts"], b["ws_gate"], b["dh_router"], b["dw"], b["db"],
-                              stream=s0)
+        if self.router is None:
+            M.moelb_gate_backward(h, w_cur, b_cur, self.idx, b["dwts"], b["ws_gate"], b["dh_router"], b["dw"],
+                                  b["db"], stream=s0)
+        else:
+            M.moelb_route_backward(h, w_cur, self.z, self.idx, b["dwts"], b["ws_gate"], b["dh_router"], b["dw"],
+                                   b["db"], stream=s0, **self.router.weights_kw())
         M.moelb_combine(b["dx"], self.pos, b["ones"], b["dh"], shared=b["dh_router"], stream=s0)
         if self.shared is None:
             return Gradients(b["dh"], b["dw"], b["db"], b["dw13"], b["dw2"], None, None)
@@ -522,7 +630,8 @@ class MoELayer:
 
 
     def step_two_stage(self, h, w_cur, b_cur, w_next, b_next, home, replica_cur, w13, w2, shared_w13=None,
-                       shared_w2=None, stream=None, events: Optional[HipEvents] = None, ev_base: int = 0) -> StepOut:
+                       shared_w2=None, stream=None, events: Optional[HipEvents] = None, ev_base: int = 0,
+                       route_bias=None, route_bias_next=None) -> StepOut:
         """The same layer step in two stages (Libra README "Key Ideas":
         MoE_local starts right after gating, the token sharding runs beside
         it).  After the histogram, the step's stream places the local pairs
@@ -531,6 +640,8 @@ class MoELayer:
         Outputs are identical to ``step``'s.  Event marks (TWO_STAGE_MARKS):
         ev_base+0..8 on the step's stream, +9..11 on the split stream, +12..13
         on the lookahead stream."""
+        self._check_bias(route_bias, route_bias_next)
+        self._check_mx(w13, w2, shared_w13, shared_w2)
         self._kept = False
         ev = events
         s0 = stream if stream is not None else torch.cuda.current_stream()
@@ -544,7 +655,10 @@ class MoELayer:
 
         def ffn(off):
             all_ = M.MOELB_FFN_ALL | self.ffn_opt
-            if self.gather_rows:
+            if self.mx:
+                M.moelb_mx_grouped_ffn(h if self.gather_rows else self.x_perm, self.P, off, self.E, w13.q, w13.scales,
+                                       w2.q, w2.scales, self.ws_ffn, self.y, G=self.G, stream=s0, **self._gather())
+            elif self.gather_rows:
                 M.moelb_grouped_ffn_stages(all_, h, self.P, off, self.E, w13, w2, self.ws_ffn, self.y, G=self.G,
                                            gather=self.perm, gather_k=self.k, stream=s0)
             else:
@@ -552,7 +666,7 @@ class MoELayer:
                                            G=self.G, stream=s0)
 
         mark(0)
-        M.moelb_gate_topk(h, w_cur, b_cur, w_next, b_next, self.idx, self.wts, self.gap, self.idx_next, stream=s0)
+        self._gate(h, w_cur, b_cur, w_next, b_next, route_bias, route_bias_next, s0)
         self.ev_gate.record(s0)
         self.side.wait_event(self.ev_gate)
         mark(12, self.side)

@@ -61,13 +61,12 @@ __device__ __forceinline__ void quantize_pieces(int block, const T* __restrict__
   m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));  // lane ^ 1
   if (!in) return;
   const uint32_t byte = mx::scale_of(m);
-  const float inv = mx::inverse(byte);
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const float* u = v + 8 * h;
-    w[h] = mx::codes4<false>(0u, u[0], u[1], u[2], u[3], inv);
-    w[h] = mx::codes4<true>(w[h], u[4], u[5], u[6], u[7], inv);
+    w[h] = mx::codes4<false>(0u, u[0], u[1], u[2], u[3], byte);
+    w[h] = mx::codes4<true>(w[h], u[4], u[5], u[6], u[7], byte);
     if (byte == 255u) w[h] = 0u;
   }
   *reinterpret_cast<uint2*>(q + row * (K / 2) + c * 8) = make_uint2(w[0], w[1]);
@@ -156,11 +155,10 @@ __device__ __forceinline__ uint2 act_block(const f32x16_t& g, const f32x16_t& u,
   }
   const auto mm = __builtin_amdgcn_permlane32_swap(m, m, false, false);
   byte = mx::scale_of(max(mm[0], mm[1]));
-  const float inv = mx::inverse(byte);
-  uint32_t lo = mx::codes4<false>(0u, a[0], a[1], a[2], a[3], inv);
-  lo = mx::codes4<true>(lo, a[4], a[5], a[6], a[7], inv);
-  uint32_t hi = mx::codes4<false>(0u, a[8], a[9], a[10], a[11], inv);
-  hi = mx::codes4<true>(hi, a[12], a[13], a[14], a[15], inv);
+  uint32_t lo = mx::codes4<false>(0u, a[0], a[1], a[2], a[3], byte);
+  lo = mx::codes4<true>(lo, a[4], a[5], a[6], a[7], byte);
+  uint32_t hi = mx::codes4<false>(0u, a[8], a[9], a[10], a[11], byte);
+  hi = mx::codes4<true>(hi, a[12], a[13], a[14], a[15], byte);
   if (byte == 255u) lo = hi = 0u;
   // the lane halves trade: columns 0..15 to the lower, 16..31 to the upper
   const auto r = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
@@ -501,6 +499,15 @@ int launch_quantize(const void* x, long long rows, int K, uint8_t* q, uint8_t* s
 using Large = Tile<128, 128, 4, 2, 2>;
 using Small = Tile<64, 128, 4, 2, 3>;
 bool large_rows(int rows, int E) { return (size_t)rows >= (size_t)96 * E; }
+// Where even the most row tiles leave half of the compute units without one, tiles of
+// 64 weight rows: one token of 8 experts 17.9 -> 17.4 us, 16 tokens of one expert,
+// 4096 x 4096, 26.0 -> 23.8.
+using Narrow = Tile<64, 64, 2, 2, 4>;
+bool narrow_columns(int rows, int E, int d, int inter) {
+  const size_t mt = (size_t)rows / 64 + (rows < E ? rows : E);
+  const size_t up = (size_t)(inter + 63) / 64, down = (size_t)(d + 127) / 128;
+  return mt * (up > down ? up : down) <= 128;
+}
 
 template <bool DOWN, typename T, class G>
 int launch_tiles(MxArgs p, size_t mtiles, hipStream_t s) {
@@ -552,8 +559,10 @@ int run_ffn(const MxArgs& p, const Groups& g, const void* x, int d, int inter, c
     if (st != MOELB_OK) return st;
   }
   const size_t mtiles = (size_t)(p.rows + bm - 1) / bm + g.E;
-  return large ? launch_ffn<T, Large>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles)
-               : launch_ffn<T, Small>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
+  if (large) return launch_ffn<T, Large>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
+  return narrow_columns(p.rows, g.E, d, inter)
+             ? launch_ffn<T, Narrow>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles)
+             : launch_ffn<T, Small>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
 }
 
 }  // namespace

@@ -18,22 +18,19 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
   const int e = (int)(amax_bits >> 23);
   return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
 }
-// 2^-X, exact: X is in [-127, 125].  255: 0.
-__device__ __forceinline__ float inverse(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0u : (254u - byte) << 23);
-}
 // 2^X, X = -127 a subnormal.
 __device__ __forceinline__ float power(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23);
 }
 
-// Four values times inv to codes in 16 bits (HI: the upper half of `old`).  The
-// conversion rounds to nearest even; 6 is the largest number.
+// Four values over 2^X to codes in 16 bits (HI: the upper half of `old`), for the
+// scale byte X + 127.  The conversion takes the exponent of its scale operand, rounds
+// to nearest even and saturates at 6, the largest number.
 template <bool HI>
-__device__ __forceinline__ uint32_t codes4(uint32_t old, float a, float b, float c, float d, float inv) {
-  auto s = [&](float x) { return __builtin_amdgcn_fmed3f(x * inv, -6.f, 6.f); };
-  old = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, s(a), s(b), 1.0f, HI ? 2 : 0);
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, s(c), s(d), 1.0f, HI ? 3 : 1);
+__device__ __forceinline__ uint32_t codes4(uint32_t old, float a, float b, float c, float d, uint32_t byte) {
+  const float s = __uint_as_float(byte << 23);
+  old = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, s, HI ? 2 : 0);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, c, d, s, HI ? 3 : 1);
 }
 
 // The eight numbers in w, times f.

@@ -76,6 +76,13 @@ __device__ __forceinline__ void copy16(uint32_t voff, i32x4_t srd, uint32_t soff
                "s"(m0), "s"(soff)
                : "memory", "m0");
 }
+// The same copy marked non-temporal: lines read once, which the caches should give
+// up first.
+__device__ __forceinline__ void copy16_nt(uint32_t voff, i32x4_t srd, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen nt lds" ::"v"(voff), "s"(srd),
+               "s"(m0), "s"(soff)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // Row operand: k contiguous.  DMA instruction j (0 .. 2F-1) of wave w fills

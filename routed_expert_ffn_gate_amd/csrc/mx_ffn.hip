@@ -6,11 +6,19 @@
 // "FreeBalance: Pre-Routing Online MoE Load Balancing via Residual Workload
 // Prediction", section 2.1) with both factors of every product in it.
 //
-// One wave per 32 x 32 block of an expert's rows and columns, its fragments
-// straight from memory, v_mfma_scale_f32_32x32x64_f8f6f4.  The weights'
-// fragment is the instruction's first operand, so a lane ends with 16 columns
-// of one row: the block's magnitude, codes and scale are formed between two
-// lanes, without LDS.
+// Three launches: the schedule with the tokens' quantisation, gate/up with SwiGLU and
+// the activations' quantisation as its epilogue, and down.  The products run on
+// v_mfma_scale_f32_32x32x64_f8f6f4 over tiles streamed into LDS.  The weights'
+// fragment is the instruction's first operand, so a lane ends with 16 columns of one
+// row: a block's magnitude, codes and scale are formed between two lanes, without LDS.
+//
+// Bound by the weights' stream where an expert has few rows (512 tokens of 8, 128
+// experts, d = 2048, inter = 768: 322 MB of weights in 80 us, 4.2 TB/s), and where it
+// has hundreds by the L2's feed of the tiles and the power of the matrix instructions
+// (16384 tokens of 8, 64 experts, inter = 1024: 670 us, 2.5 PFLOP/s; registers alone
+// reach 6.4).
+#include <cmath>
+
 #include "ffn_sched.h"
 #include "mfma_tile.h"
 #include "mx_format.h"
@@ -195,7 +203,6 @@ struct Tile {
   static constexpr int JS = (BM + BN + 64 * NW - 1) / (64 * NW); // of scales, a wave and two steps
   static constexpr int STAGE = (BM + BN) * 128, CHUNK = JS * NW * 1024;
   static constexpr size_t LDS = (size_t)STAGES * STAGE + 2 * CHUNK;
-  static_assert(STAGES >= 2 && STAGES <= 4, "wait_stages");
 };
 
 __device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ (((row >> 1) ^ (row << 2)) & 7); }
@@ -309,20 +316,21 @@ __device__ __forceinline__ void put_tile(const MxArgs& p, const Place& o, int ro
 
 // Waits until only the newest n stages' loads (J a stage) may be in flight, and for
 // this wave's LDS reads.
-template <int J>
+template <int J, int MOST>
 __device__ __forceinline__ void wait_stages(int n) {
-  static_assert(3 * J < 64, "the counter has six bits");
-  if (n >= 3)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * J) : "memory");
-  else if (n == 2)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * J) : "memory");
-  else if (n == 1)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(J) : "memory");
-  else
+  static_assert(MOST * J < 64, "the counter has six bits");
+  if constexpr (MOST > 0) {
+    if (n < MOST)
+      wait_stages<J, MOST - 1>(n);
+    else
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(MOST * J) : "memory");
+  } else {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  }
 }
 
-template <bool DOWN, typename T, class G>
+// NT: the weights' loads are marked non-temporal.
+template <bool DOWN, bool NT, typename T, class G>
 __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) {
   constexpr int BM = G::BM, BN = G::BN, MI = G::MI, NI = G::NI, JA = G::JA, JB = G::JB, J = G::J, JS = G::JS;
   constexpr int STAGE = G::STAGE, S = G::STAGES;
@@ -370,6 +378,9 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
     if (j < JA)
       mt::copy16(in ? aoff[j < JA ? j : 0] : mt::OUTSIDE, da, (uint32_t)t * 128u,
                  st + (uint32_t)((wave * JA + j) * 1024));
+    else if (NT)
+      mt::copy16_nt(in ? boff[j < JA ? 0 : j - JA] : mt::OUTSIDE, db, (uint32_t)t * 128u,
+                    st + (uint32_t)(BM * 128 + (wave * JB + j - JA) * 1024));
     else
       mt::copy16(in ? boff[j < JA ? 0 : j - JA] : mt::OUTSIDE, db, (uint32_t)t * 128u,
                  st + (uint32_t)(BM * 128 + (wave * JB + j - JA) * 1024));
@@ -401,7 +412,7 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
   for (int t = 0; t < S && t < KT; ++t)
 #pragma unroll
     for (int j = 0; j < J; ++j) issue(t, j);
-  wait_stages<J>(min(S, KT) - 1);
+  wait_stages<J, S - 1>(min(S, KT) - 1);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   for (int t = 0; t < KT; ++t) {
@@ -428,7 +439,7 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
       for (int i = 0; i < MI; ++i) fa[i] = *reinterpret_cast<const uint4*>(st + arow[i] * 128 + at[ks]);
       if (ks == 3 && t + 1 < KT) {
         // lgkmcnt(0): this wave's reads of step t are done before its stage is refilled
-        wait_stages<J>(min(S - 2, KT - 2 - t));
+        wait_stages<J, S - 2>(min(S - 2, KT - 2 - t));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if ((t & 1) && t + 3 < KT) issue_scales((t + 3) / 2);
@@ -509,28 +520,41 @@ bool narrow_columns(int rows, int E, int d, int inter) {
   return mt * (up > down ? up : down) <= 128;
 }
 
-template <bool DOWN, typename T, class G>
+template <bool DOWN, bool NT, typename T, class G>
 int launch_tiles(MxArgs p, size_t mtiles, hipStream_t s) {
-  if (!moelb_allow_lds(mx_stream_kernel<DOWN, T, G>, G::LDS)) return MOELB_ELAUNCH;
+  if (!moelb_allow_lds(mx_stream_kernel<DOWN, NT, T, G>, G::LDS)) return MOELB_ELAUNCH;
   p.ntn = (p.N + G::BN - 1) / G::BN;
   if (!DOWN) p.ntn = (p.inter + G::BN / 2 - 1) / (G::BN / 2);
-  hipLaunchKernelGGL((mx_stream_kernel<DOWN, T, G>), dim3((unsigned)(mtiles * p.ntn + 8)), dim3(G::THREADS), G::LDS, s,
-                     p);
+  hipLaunchKernelGGL((mx_stream_kernel<DOWN, NT, T, G>), dim3((unsigned)(mtiles * p.ntn + 8)), dim3(G::THREADS), G::LDS,
+                     s, p);
   MOELB_CHECK_LAUNCH();
   return MOELB_OK;
 }
 
-template <typename T, class G>
+// NT: gate and up weights marked non-temporal.
+template <bool NT, typename T, class G>
 int launch_ffn(const MxArgs& base, int d, int inter, const uint8_t* w13, const uint8_t* w13s, const uint8_t* w2,
                const uint8_t* w2s, const uint8_t* xq, const uint8_t* xs, hipStream_t s, size_t mtiles) {
   MxArgs p = base;
   p.a = xq, p.as = xs, p.w = w13, p.ws = w13s;
   p.K = d, p.N = 2 * inter, p.lda = mx::scale_bytes(d);
-  const int st = launch_tiles<false, T, G>(p, mtiles, s);
+  const int st = launch_tiles<false, NT, T, G>(p, mtiles, s);
   if (st != MOELB_OK) return st;
   p.a = p.q, p.as = p.qs, p.w = w2, p.ws = w2s;
   p.K = inter, p.N = d, p.lda = p.ldq;
-  return launch_tiles<true, T, G>(p, mtiles, s);
+  return launch_tiles<true, false, T, G>(p, mtiles, s);
+}
+
+// 64-row tiles that stream more weights than the 256 MB memory-side cache holds read
+// the gate's and the up's non-temporally: no later call finds them there, and the
+// activations and W2 stay.  512 tokens over 128 experts (322 MB) 86 -> 80 us, 64 tokens
+// 76 -> 72.  Weights that fit are left alone (64 experts, 213 MB, called again at once:
+// 56 us, non-temporal 65; 16 tokens over about 81 of 128 experts: 46 and 50), and so is
+// W2, which the tiles of an expert share (all weights non-temporal: 85 us).  Counted are
+// the experts that so many rows reach when each falls on any of them alike.
+bool streams_weights(int rows, int E, int d, int inter) {
+  const double experts = -E * std::expm1(-(double)rows / E);
+  return experts * 3 * inter * d / 32 * 17 > 256.0 * (1 << 20);
 }
 
 struct Groups {
@@ -559,10 +583,12 @@ int run_ffn(const MxArgs& p, const Groups& g, const void* x, int d, int inter, c
     if (st != MOELB_OK) return st;
   }
   const size_t mtiles = (size_t)(p.rows + bm - 1) / bm + g.E;
-  if (large) return launch_ffn<T, Large>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
-  return narrow_columns(p.rows, g.E, d, inter)
-             ? launch_ffn<T, Narrow>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles)
-             : launch_ffn<T, Small>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
+  if (large) return launch_ffn<false, T, Large>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
+  if (narrow_columns(p.rows, g.E, d, inter))
+    return launch_ffn<false, T, Narrow>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
+  return streams_weights(p.rows, g.E, d, inter)
+             ? launch_ffn<true, T, Small>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles)
+             : launch_ffn<false, T, Small>(p, d, inter, w13, w13s, w2, w2s, xq, xs, s, mtiles);
 }
 
 }  // namespace

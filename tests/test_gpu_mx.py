@@ -178,6 +178,18 @@ def test_ffn(moelb, counts, d, inter, dtype):
     assert torch.equal(y, run_ffn(x, rows, offsets(counts), E, w))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_ffn_of_few_rows_and_more_weights_than_the_caches_hold(moelb, dtype):
+    """20 experts of 17 MB: their loads are marked non-temporal; K and the columns end inside a tile."""
+    counts, d, inter = [2, 0, 3, 1, 9, 1, 0, 2, 4, 1, 5, 2, 1, 0, 6, 3, 1, 66, 2, 1], 2080, 5152
+    x = torch.randn((sum(counts), d), generator=torch.Generator(device="cuda").manual_seed(6), device="cuda").to(dtype)
+    w = weights(len(counts), d, inter, 7)
+    log(f"[mx ffn] 20 experts d={d} inter={inter} {dtype}")
+    y = run_ffn(x, sum(counts), offsets(counts), len(counts), w)
+    check_ffn(x, counts, w, y)
+    assert torch.equal(y, run_ffn(x, sum(counts), offsets(counts), len(counts), w))
+
+
 def test_ffn_gathers_replicas_and_ranks(moelb):
     """Groups of several ranks share experts, rows come through a gather, one rank's share alone."""
     E, G, d, inter, k, T = 6, 4, 192, 160, 3, 90

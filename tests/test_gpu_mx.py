@@ -206,6 +206,28 @@ def test_ffn_gathers_replicas_and_ranks(moelb):
         check_ffn(x, counts, w, part, gather, k, skip=[g for g in range(2 * G * E) if (g // E) % G != rank])
 
 
+def test_ffn_of_more_groups_than_one_launch_schedules(moelb):
+    """6400 groups: the schedule has its own launches."""
+    E, G, d, inter, k, T = 100, 32, 96, 64, 2, 700
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    counts = torch.randint(0, 3, (2 * G * E,), generator=torch.Generator().manual_seed(9))
+    counts[torch.rand((2 * G * E,), generator=torch.Generator().manual_seed(10)) < 0.7] = 0
+    rows = int(counts.sum())
+    x = torch.randn((T, d), generator=gen, device="cuda").to(BF)
+    gather = torch.randint(0, T * k, (rows,), generator=gen, device="cuda").to(torch.int32)
+    w = weights(E, d, inter, 11)
+    y = run_ffn(x, rows, offsets(counts.tolist()), E, w, gather, k, G)
+    check_ffn(x, counts.tolist(), w, y, gather, k)
+
+
+@pytest.mark.parametrize("d,inter", [(1 << 17, 32), (32, 1 << 17)])
+def test_ffn_of_wide_rows(moelb, d, inter):
+    x = torch.randn((70, d), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").to(BF)
+    w = weights(1, d, inter, 12)
+    log(f"[mx ffn] wide d={d} inter={inter}")
+    check_ffn(x, [70], w, run_ffn(x, 70, offsets([70]), 1, w))
+
+
 def test_ffn_rows_outside_groups_and_offsets_out_of_range(moelb):
     E, d, inter, rows = 3, 64, 64, 100
     x = torch.randn((rows, d), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").to(BF)

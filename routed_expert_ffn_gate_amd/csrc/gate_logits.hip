@@ -6,7 +6,8 @@
 //
 // Many tokens: the tile of mfma_tile.h, 128 tokens x 128 experts in bf16, 64 x 64 in
 // fp32; the tiles of the same tokens run side by side on one XCD, so its L2 serves
-// h to all but the first.  Few tokens: a tile of 16 x 16 by one workgroup, its waves
+// h to all but the first.  Where the routers' experts fill 256 columns, a tile of 128 x
+// 256 reads h once.  Few tokens: a tile of 16 x 16 by one workgroup, its waves
 // taking the products' k in turn, so that a router's rows are read by E / 16 compute
 // units at once.
 #include "mfma_tile.h"
@@ -75,6 +76,114 @@ __global__ __launch_bounds__(mt::THREADS) void logits_kernel(LogitArgs<uint16_t>
   mt::drain<LF, false>(lds, acc, [&](int r, int c, const float* v) {
     if (m0 + r < p.Ttok) put_logits(p, z, b, m0 + r, n0 + c, v);
   });
+}
+
+// Many tokens and 256 columns or 512, the experts of all routers side by side: eight
+// waves take 128 tokens x 256 columns, so that h is read once for both routers of 128
+// experts.  K steps of 64 go through a ring of three stages.  T = 32768, d = 4096, two
+// routers of 128 experts 91 -> 83 us (3.7 TB/s), one of 256 86 -> 82; two of 256
+// 160, either tile.  h further ahead than w (four to six stages, loaded by half of the
+// waves) 84-97; h non-temporal 84-98.
+constexpr int WM = 128, WN = 256, WAVES = 8, STAGES = 3;
+constexpr int STAGE = (WM + WN) * 128;
+
+__global__ __launch_bounds__(WAVES * MOELB_WAVE, 2) void logits_wide_kernel(LogitArgs<uint16_t> p) {
+  constexpr int JA = WM / 8 / WAVES, JB = WN / 8 / WAVES, J = JA + JB;
+  extern __shared__ __align__(16) char smem[];
+  const int j8 = blockIdx.x >> 3, m0 = ((j8 / p.nt) * 8 + (blockIdx.x & 7)) * WM, n0 = j8 % p.nt * WN;
+  if (m0 >= p.Ttok) return;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3, fr = lane & 31, fh = lane >> 5;
+  const int KT = (p.d + mt::BK - 1) / mt::BK, whole = p.d / mt::BK, turn = (m0 / WM) % KT;
+  const uint32_t row = (uint32_t)p.d * 2u;
+  // the wave loads weight rows of columns n0 + 32 wave .., all of one router
+  const int c0 = n0 + wave * JB * 8;
+  const mt::i32x4_t da = mt::descriptor(p.h, (uint32_t)p.Ttok * row);
+  const mt::i32x4_t db = mt::descriptor(c0 < p.E ? p.w[0] : p.w[1], (uint32_t)p.E * row);
+  uint32_t off[J], tail = 0;  // tail: in step `whole`, which instructions' chunks lie in K
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int r = j < JA ? (wave * JA + j) * 8 + (lane >> 3) : (wave * JB + j - JA) * 8 + (lane >> 3);
+    const int c = mt::slot_of(r, lane & 7);
+    const int from = j < JA ? min(m0 + r, p.Ttok - 1) : n0 + r - (c0 < p.E ? 0 : p.E);
+    off[j] = (uint32_t)from * row + c * 16;
+    tail |= (uint32_t)(c * 8 < p.d - whole * mt::BK) << j;
+  }
+  auto issue = [&](int t, int j) {
+    const uint32_t st = lds0 + (uint32_t)(t % STAGES * STAGE);
+    const int k = t + turn < KT ? t + turn : t + turn - KT;
+    mt::copy16(k < whole || (tail >> j & 1) ? off[j] : mt::OUTSIDE, j < JA ? da : db, (uint32_t)k * 128u,
+               st + (uint32_t)(j < JA ? (wave * JA + j) * 1024 : WM * 128 + (wave * JB + j - JA) * 1024));
+  };
+  int at[4];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) at[ks] = fr * 128 + mt::slot_of(fr, ks * 2 + fh) * 16;
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i >> 1][i & 1][r] = 0.f;
+  for (int t = 0; t < STAGES && t < KT; ++t)
+#pragma unroll
+    for (int j = 0; j < J; ++j) issue(t, j);
+  mt::wait_stages<J, STAGES - 1>(min(STAGES, KT) - 1);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  for (int t = 0; t < KT; ++t) {
+    const char* sa = smem + t % STAGES * STAGE + wm * 64 * 128;
+    const char* sb = smem + t % STAGES * STAGE + (WM + wn * 64) * 128;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      bf16x8_t a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) b[i] = *reinterpret_cast<const bf16x8_t*>(sb + i * 32 * 128 + at[ks]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const bf16x8_t*>(sa + i * 32 * 128 + at[ks]);
+      if (ks == 3 && t + 1 < KT) {
+        // lgkmcnt(0): this wave's reads of step t are done before its stage is refilled
+        mt::wait_stages<J, STAGES - 2>(min(STAGES - 2, KT - 2 - t));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi) {
+#pragma unroll
+        for (int ni = 0; ni < 2; ++ni)
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[ni], a[mi], acc[mi][ni], 0, 0, 0);
+        if (ks == 3 && t + STAGES < KT) {
+#pragma unroll
+          for (int j = mi; j < J; j += 2) issue(t + STAGES, j);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // The wave's 64 x 64 logits through LDS of its own, row r's 16-byte chunk c at c ^ (r
+  // % 16), so that they leave in whole lines.
+  char* o = smem + wave * 64 * 256;
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16_t& x = acc[mi][ni];
+        *reinterpret_cast<float4*>(o + (mi * 32 + fr) * 256 + ((ni * 8 + q * 2 + fh) ^ (fr & 15)) * 16) =
+            make_float4(x[q * 4], x[q * 4 + 1], x[q * 4 + 2], x[q * 4 + 3]);
+      }
+  const int v = n0 + wn * 64, r1 = v < p.E ? 0 : 1, c = v - r1 * p.E + (lane & 15) * 4;  // this lane's four columns
+  const float* b = r1 ? p.b[1] : p.b[0];
+  float* z = (r1 ? p.z[1] : p.z[0]) + c;
+  float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (b) add = make_float4(b[c], b[c + 1], b[c + 2], b[c + 3]);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = i * 4 + (lane >> 4), t = m0 + wm * 64 + r;
+    float4 x = *reinterpret_cast<const float4*>(o + r * 256 + ((lane & 15) ^ (r & 15)) * 16);
+    x.x += add.x, x.y += add.y, x.z += add.z, x.w += add.w;
+    if (t < p.Ttok) *reinterpret_cast<float4*>(z + (size_t)t * p.E) = x;
+  }
 }
 
 __global__ __launch_bounds__(mt::S_THREADS) void logits_f32_kernel(LogitArgs<float> p) {
@@ -168,7 +277,24 @@ int launch_few(const LogitArgs<T>& p, int routers, hipStream_t s) {
   return MOELB_OK;
 }
 
+// Whether a call takes the wide tile: no column of it is empty (two routers of 160
+// experts 86 | 91, of 72, d = 1000, 37 | 40 us) and every compute unit gets one (T =
+// 24576, d = 4096, two of 128, 62 | 63).
+bool wide_columns(const LogitArgs<uint16_t>& p, int routers) {
+  const int n = p.E * routers;
+  return p.vec && n % WN == 0 && p.E % 128 == 0 && (size_t)(p.Ttok / WM) * (n / WN) >= 256;
+}
+
 int launch(LogitArgs<uint16_t> p, int routers, hipStream_t s) {
+  if (wide_columns(p, routers)) {
+    if (!moelb_allow_lds(logits_wide_kernel, STAGES * STAGE)) return MOELB_ELAUNCH;
+    const int m = (p.Ttok + WM - 1) / WM;
+    p.nt = p.E * routers / WN;
+    hipLaunchKernelGGL(logits_wide_kernel, dim3((m + 7) / 8 * 8 * p.nt), dim3(WAVES * MOELB_WAVE), STAGES * STAGE, s,
+                       p);
+    MOELB_CHECK_LAUNCH();
+    return MOELB_OK;
+  }
   if (!moelb_allow_lds(logits_kernel, mt::lds_bytes<LF>())) return MOELB_ELAUNCH;
   const int m = (p.Ttok + LB - 1) / LB;
   p.nt = (p.E + LB - 1) / LB * routers;

@@ -85,6 +85,24 @@ __device__ __forceinline__ void copy16_nt(uint32_t voff, i32x4_t srd, uint32_t s
 }
 #pragma clang diagnostic pop
 
+// Where a row of 128 bytes holds its 16-byte chunk in LDS (and which chunk a place holds).
+__device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ (((row >> 1) ^ (row << 2)) & 7); }
+
+// Waits until only the newest n stages' loads (J a stage) may be in flight, and for
+// this wave's LDS reads.
+template <int J, int MOST>
+__device__ __forceinline__ void wait_stages(int n) {
+  static_assert(MOST * J < 64, "the counter has six bits");
+  if constexpr (MOST > 0) {
+    if (n < MOST)
+      wait_stages<J, MOST - 1>(n);
+    else
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(MOST * J) : "memory");
+  } else {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  }
+}
+
 // Row operand: k contiguous.  DMA instruction j (0 .. 2F-1) of wave w fills
 // the 8 LDS rows (2F w + j) * 8 ..; lane l row l / 8 of them, slot l % 8, which
 // holds chunk slot ^ swizzle(row).

@@ -205,8 +205,6 @@ struct Tile {
   static constexpr size_t LDS = (size_t)STAGES * STAGE + 2 * CHUNK;
 };
 
-__device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ (((row >> 1) ^ (row << 2)) & 7); }
-
 // Virtual rows, expert and columns of a tile.
 struct Place {
   int e, v0, end, nt;
@@ -314,21 +312,6 @@ __device__ __forceinline__ void put_tile(const MxArgs& p, const Place& o, int ro
   }
 }
 
-// Waits until only the newest n stages' loads (J a stage) may be in flight, and for
-// this wave's LDS reads.
-template <int J, int MOST>
-__device__ __forceinline__ void wait_stages(int n) {
-  static_assert(MOST * J < 64, "the counter has six bits");
-  if constexpr (MOST > 0) {
-    if (n < MOST)
-      wait_stages<J, MOST - 1>(n);
-    else
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(MOST * J) : "memory");
-  } else {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  }
-}
-
 // NT: the weights' loads are marked non-temporal.
 template <bool DOWN, bool NT, typename T, class G>
 __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) {
@@ -354,13 +337,13 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
   uint32_t tail = 0;             // in step `whole`: which instructions' pieces lie in K
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
-    const int r = (wave * JA + j) * 8 + (lane >> 3), c = slot_of(r, lane & 7) * 16;
+    const int r = (wave * JA + j) * 8 + (lane >> 3), c = mt::slot_of(r, lane & 7) * 16;
     aoff[j] = row_of<DOWN>(p, o, r) * (uint32_t)half + c;
     tail |= (uint32_t)(whole * 128 + c < half) << j;
   }
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
-    const int r = (wave * JB + j) * 8 + (lane >> 3), c = slot_of(r, lane & 7) * 16;
+    const int r = (wave * JB + j) * 8 + (lane >> 3), c = mt::slot_of(r, lane & 7) * 16;
     boff[j] = weight_of<DOWN, BN>(p, o, r) * (uint32_t)half + c;
     tail |= (uint32_t)(whole * 128 + c < half) << (JA + j);
   }
@@ -399,7 +382,7 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
   for (int i = 0; i < NI; ++i) brow[i] = block_row<DOWN, BN, NI>(wn, i) + fr;
   int at[4];  // byte of a row in sub-step ks: rows are a multiple of 32 and fr
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) at[ks] = slot_of(fr, ks * 2 + fh) * 16;
+  for (int ks = 0; ks < 4; ++ks) at[ks] = mt::slot_of(fr, ks * 2 + fh) * 16;
   f32x16_t acc[MI][NI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
@@ -412,7 +395,7 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
   for (int t = 0; t < S && t < KT; ++t)
 #pragma unroll
     for (int j = 0; j < J; ++j) issue(t, j);
-  wait_stages<J, S - 1>(min(S, KT) - 1);
+  mt::wait_stages<J, S - 1>(min(S, KT) - 1);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   for (int t = 0; t < KT; ++t) {
@@ -439,7 +422,7 @@ __global__ __launch_bounds__(G::THREADS, G::EU) void mx_stream_kernel(MxArgs p) 
       for (int i = 0; i < MI; ++i) fa[i] = *reinterpret_cast<const uint4*>(st + arow[i] * 128 + at[ks]);
       if (ks == 3 && t + 1 < KT) {
         // lgkmcnt(0): this wave's reads of step t are done before its stage is refilled
-        wait_stages<J, S - 2>(min(S - 2, KT - 2 - t));
+        mt::wait_stages<J, S - 2>(min(S - 2, KT - 2 - t));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if ((t & 1) && t + 3 < KT) issue_scales((t + 3) / 2);

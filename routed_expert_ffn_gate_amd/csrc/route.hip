@@ -14,7 +14,9 @@
 //  * What the list does not hold (ties beyond it, groups near the border of the kept
 //    ones, values below the keys' window): route_token, a whole wave a token, four
 //    experts a lane, in 64 bits.
-// So the picks are those of exact arithmetic.
+// So the picks are those of 64-bit arithmetic.  Bound by vector instructions (60-70 %
+// active): T = 32768, 256 experts, sigmoid, bias, 4 of 8 groups, top 8 in 23 us (7 for
+// the logits' bytes); 128 experts, softmax 12; 512 tokens 4.9.
 #include <float.h>
 #include <math.h>
 

@@ -43,7 +43,8 @@ def close(got, want, allow, what):
 @pytest.mark.parametrize("T,d,E,both", [(1, 8, 1, False), (1, 4096, 128, True), (3, 72, 60, True), (17, 1000, 8, False),
                                         (64, 2048, 128, True), (65, 520, 256, False), (130, 192, 256, True),
                                         (512, 256, 160, True), (700, 136, 96, True), (1031, 64, 65, False),
-                                        (9000, 128, 64, True), (33000, 64, 128, True)])
+                                        (9000, 128, 64, True), (33000, 64, 128, True), (33001, 200, 128, True),
+                                        (32768, 8, 256, False), (16511, 328, 256, True), (40000, 136, 128, True)])
 def test_logits(moelb, dtype, T, d, E, both):
     from routed_expert_ffn_gate_amd import moelb as M
     gen = torch.Generator(device="cuda").manual_seed(T + d + E)

@@ -4,18 +4,19 @@
 // Definition (include/moelb.h, moelb_route): s = scores of z, c = s + bias;
 // the groups with the largest scores stay; idx = the k largest c, w = scale s.
 //
-// Three forms of the same rule:
+// Forms of the same rule:
 //  * route_fast: eight lanes a token, in fp32.  Values become 24-bit fixed-point
 //    keys with the id below (larger value, then lower id), and the k + 2 largest
 //    are kept by an insertion list, one v_med3_u32 an entry; the lanes' lists are
 //    merged by DPP.  It also finds where fp32 cannot tell.
 //  * Two of the first k + 1 keys nearer than their error bounds: the listed experts
 //    are ranked in 64 bits by the token's eight lanes.
-//  * What the list does not hold (ties beyond it, groups near the border of the kept
-//    ones, values below the keys' window): route_token, a whole wave a token, four
+//  * Sigmoid groups near the border of the kept ones: their best two in 64 bits.
+//  * What that does not decide (ties beyond the list or the two, a softmax's groups,
+//    values below the keys' window): route_token, a whole wave a token, four
 //    experts a lane, in 64 bits.
 // So the picks are those of 64-bit arithmetic.  Bound by vector instructions (60-70 %
-// active): T = 32768, 256 experts, sigmoid, bias, 4 of 8 groups, top 8 in 23 us (7 for
+// active): T = 32768, 256 experts, sigmoid, bias, 4 of 8 groups, top 8 in 21 us (7 for
 // the logits' bytes); 128 experts, softmax 12; 512 tokens 4.9.
 #include <float.h>
 #include <math.h>
@@ -349,38 +350,39 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
     wave_fence();
     const int size = p.E / p.groups;
     const bool quads = size % 4 == 0;
-    for (int g = sub; g < p.groups; g += LPT) {
-      float a = -INFINITY, b = -INFINITY;
-      auto take = [&](float x) {
-        b = med3(a, b, x);
-        a = fmaxf(a, x);
-      };
-      auto use = [&](auto x) {
-        if constexpr (sizeof(x) == 16)
-          take(x.x), take(x.y), take(x.z), take(x.w);
-        else
-          take(x);
-      };
-      // four reads ahead of their use; each lane starts elsewhere: groups of a power
-      // of two would meet on one bank
-      auto scan = [&](int cnt, auto read) {
+    // take(x, i) for the values of group g.  Four reads ahead of their use; each lane
+    // starts elsewhere: groups of a power of two would meet on one bank
+    auto scan = [&](int g, auto take) {
+      auto run = [&](int cnt, auto read, auto use) {
         int i = sub % cnt;
         for (int n = 0; n < cnt; n += 4) {
           decltype(read(0)) x[4];
+          int at[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             x[q] = read(i);
+            at[q] = i;
             i = i + 1 < cnt ? i + 1 : 0;
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (n + q < cnt) use(x[q]);
+            if (n + q < cnt) use(x[q], at[q]);
         }
       };
+      const float* r = row + g * size;
       if (quads)
-        scan(size / 4, [&](int i) { return *reinterpret_cast<const float4*>(row + g * size + 4 * i); });
+        run(
+            size / 4, [&](int i) { return *reinterpret_cast<const float4*>(r + 4 * i); },
+            [&](float4 x, int i) { take(x.x, 4 * i), take(x.y, 4 * i + 1), take(x.z, 4 * i + 2), take(x.w, 4 * i + 3); });
       else
-        scan(size, [&](int i) { return row[g * size + i]; });
+        run(size, [&](int i) { return r[i]; }, take);
+    };
+    for (int g = sub; g < p.groups; g += LPT) {
+      float a = -INFINITY, b = -INFINITY;
+      scan(g, [&](float x, int) {
+        b = med3(a, b, x);
+        a = fmaxf(a, x);
+      });
       if (!p.bias) {
         a = a > -INFINITY ? score(a) : -INFINITY;
         b = b > -INFINITY ? score(b) : -INFINITY;
@@ -391,6 +393,7 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
     // a group's place among the others; beyond doubt if it is the same with the
     // error bound taken off and added: that of two sums of two c
     const float tol = (p.sigmoid ? 0x1p-19f : 0x1p-18f) * M;
+    bool doubt = false;
     for (int g = sub; g < p.groups; g += LPT) {
       const float x = gs[g];
       int before = 0, least = 0, most = 0;
@@ -406,10 +409,48 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
           most += in && y[q] >= x - tol;  // itself among them
         }
       }
-      if (least < p.topk_groups && most > p.topk_groups && x > -INFINITY) redo = true;
+      if (least < p.topk_groups && most > p.topk_groups && x > -INFINITY) doubt = true;
       if (before < p.topk_groups) kept[before] = g;
     }
     wave_fence();
+    // Doubtful groups of a sigmoid, one a lane: the sum of their best two in 64 bits,
+    // unless a third value is near them.  Left to route_token instead: 22.8 us
+    // against 21.0 at T = 32768, 4 of 8 groups of 32 (16.8 without any such token).
+    const uint64_t doubts = __ballot(doubt && active);
+    if (p.sigmoid && p.groups <= LPT && doubts != 0ull) {
+      doubt = false;
+      if ((doubts >> (tok * LPT)) & 0xff) {
+        double c = -INFINITY;
+        if (sub < p.groups && gs[sub] > -INFINITY) {
+          float a = -INFINITY, b = -INFINITY;
+          int ia = -1, ib = -1, count = 0;
+          scan(sub, [&](float x, int i) {
+            if (x > a)
+              b = a, ib = ia, a = x, ia = i;
+            else if (x > b)
+              b = x, ib = i;
+          });
+          const float least = (p.group_top == 1 ? a : b) - 0x1p-20f * M;  // twice the errors of two c
+          scan(sub, [&](float x, int) { count += x >= least; });
+          doubt = p.bias && count > 2;
+          auto exact = [&](int i) {
+            if (i < 0) return (double)-INFINITY;
+            const int e = sub * size + i;
+            return 1.0 / (1.0 + exp(-(double)taken(zr[e]))) + (p.bias ? (double)p.bias[e] : 0.0);
+          };
+          const double ca = exact(ia), cb = exact(ib);
+          c = p.group_top == 1 ? (ca > cb ? ca : cb) : ca + cb;
+        }
+        int before = 0;
+        for (int f = 0; f < p.groups; ++f) {
+          const double o = __shfl(c, tok * LPT + f, MOELB_WAVE);
+          before += o > c || (o == c && f < sub);
+        }
+        if (sub < p.groups && before < p.topk_groups) kept[before] = sub;
+      }
+      wave_fence();
+    }
+    redo = redo || doubt;
     // the kept groups' values, four groups' reads ahead of their use
     for (int n = 0; n < p.topk_groups; n += 4) {
       int e0[4];

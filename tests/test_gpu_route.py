@@ -160,6 +160,27 @@ def test_neighbours_one_step_apart(moelb, score, biased):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("groups,size,group_top", [(8, 32, 1), (8, 32, 2), (4, 5, 1), (4, 5, 2), (7, 6, 1), (7, 6, 2),
+                                                   (3, 1, 1), (16, 8, 1), (16, 8, 2)])
+def test_groups_that_fp32_cannot_tell(moelb, score, biased, groups, size, group_top):
+    """The groups' scores differ by about 1e-7, the two experts behind each by much more."""
+    T, gen = 203, torch.Generator(device="cuda").manual_seed(groups * size)
+    u = lambda *s: torch.rand(s, generator=gen, device="cuda", dtype=torch.float64)  # noqa: E731
+    c = 0.05 + 0.1 * u(T, groups, size)
+    bias = (0.01 * u(groups * size)).float() if biased else None
+    first = torch.full((T, groups), 0.6, dtype=torch.float64, device="cuda") if group_top == 1 else 0.6 + 0.2 * u(T, groups)
+    place = u(T, groups, size).argsort(-1)
+    c.scatter_(2, place[..., :1], first[..., None])
+    if group_top == 2:
+        c.scatter_(2, place[..., 1:2], (1.1 - first)[..., None])
+    s = c.view(T, -1) - (bias.double() if biased else 0.0)
+    z = (torch.log(s / (1 - s)) if score == "sigmoid" else torch.log(s)).float()
+    z[T - 3:] = z[T - 3:].fill_(1.0)  # and some rows of equal logits
+    check_route(z, min(size, 4), score, bias=bias, groups=groups, topk_groups=max(1, groups // 2), group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("std", [30.0, 1e-6, 1e4])
 def test_far_and_near_logits(moelb, score, std):
     """Scores that underflow or saturate; without a bias the order is the logits'."""

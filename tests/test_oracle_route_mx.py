@@ -92,3 +92,14 @@ def test_flip_step_is_zero_away_from_borders():
     a[0, 0] = 5.5
     step = mx.flip_step(a, torch.full_like(a, 1e-7))
     assert step[0, 1] == 0.5 and step[0, 2] == 0
+
+
+def test_mx_ffn_by_hand():
+    """One activation of 100 in its block: 2^4 times 6.25, which rounds to 6, so 96; times 2."""
+    x, w13, w2 = torch.zeros(1, 32).double(), torch.zeros(64, 32).double(), torch.zeros(32, 32).double()
+    x[0, 0], w13[0, 0], w13[32, 0], w2[0, 0] = 2.0, 50.0, 0.5, 2.0
+    y, bound = mx.ffn_rows(x, w13, w2)
+    want = torch.zeros(1, 32).double()
+    want[0, 0] = 192.0
+    assert torch.equal(y, want)
+    assert (bound[0, 1:] == 0).all() and 0 < bound[0, 0] < 1e-2

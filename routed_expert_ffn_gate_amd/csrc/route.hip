@@ -242,7 +242,7 @@ struct Keys {
 __device__ __forceinline__ float masked(float v) { return fmaf(v, 0.f, v); }
 
 // Eight tokens by one wave.  `lds`: TPW rows of p.stride floats, then TPW x groups
-// scores and TPW x groups kept groups (groups > 1).  Returns the mask of lanes
+// scores with their errors and TPW x groups kept groups (groups > 1).  Returns the mask of lanes
 // whose token has to be routed in 64 bits (outputs not written).
 template <int NV, int KL>
 __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float* lds) {
@@ -328,6 +328,8 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
   // keys are in order if they are further apart than twice that, 5 or 15 units, and
   // 4 units of their own rounding.  Logits are exact: unequal keys are in order.
   const uint32_t near = p.bias ? (p.sigmoid ? 9u : 19u) : 0u;
+  // one c with a bias, and room for one more rounding of it and of a sum with it
+  auto c_error = [&](float c) { return (p.sigmoid ? 0x1p-22f : 14 * 0x1p-24f) + fabsf(c) * 0x1p-22f; };
   // a window too far from 0 for its sums (the bound is 2^-24 |top| of error, far
   // under a tenth of the window)
   bool redo = fabsf(top) >= (p.bias ? 1e30f : 1e7f);
@@ -339,8 +341,9 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
     for (int i = 0; i < NV; ++i) list_insert<KL>(l, keys.of(v[i], id_of(i)));
   } else {
     float* row = lds + tok * p.stride;
-    float* gs = lds + TPW * p.stride + tok * p.groups;
-    int* kept = reinterpret_cast<int*>(lds + TPW * (p.stride + p.groups)) + tok * p.groups;
+    // a group's score, and how far it can be from its value in 64 bits
+    float2* gs = reinterpret_cast<float2*>(lds + TPW * p.stride) + tok * p.groups;
+    int* kept = reinterpret_cast<int*>(lds + TPW * (p.stride + 2 * p.groups)) + tok * p.groups;
 #pragma unroll
     for (int j = 0; j < NV / 4; ++j) {
       const int e = id_of(4 * j);
@@ -387,26 +390,31 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
         a = a > -INFINITY ? score(a) : -INFINITY;
         b = b > -INFINITY ? score(b) : -INFINITY;
       }
-      gs[g] = p.group_top == 1 ? a : a + b;
+      // c: the bounds below, the bias's rounding by the c itself (a group's best two
+      // may lie far below the token's); the sum, and the two ends of the comparison,
+      // round by as much again
+      const float err = p.bias ? c_error(a) + (p.group_top == 1 ? 0.f : c_error(b))
+                               : (p.sigmoid ? 0x1p-20f : 0x1p-19f) * M;
+      gs[g] = make_float2(p.group_top == 1 ? a : a + b, err);
     }
     wave_fence();
     // a group's place among the others; beyond doubt if it is the same with the
-    // error bound taken off and added: that of two sums of two c
-    const float tol = (p.sigmoid ? 0x1p-19f : 0x1p-18f) * M;
+    // errors of both taken off and added
     bool doubt = false;
     for (int g = sub; g < p.groups; g += LPT) {
-      const float x = gs[g];
+      const float2 me = gs[g];
+      const float x = me.x, lo = x - me.y, hi = x + me.y;
       int before = 0, least = 0, most = 0;
       for (int f = 0; f < p.groups; f += 8) {
-        float y[8];
+        float2 y[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) y[q] = gs[min(f + q, p.groups - 1)];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const bool in = f + q < p.groups;
-          before += in && (y[q] > x || (y[q] == x && f + q < g));
-          least += in && y[q] > x + tol;
-          most += in && y[q] >= x - tol;  // itself among them
+          before += in && (y[q].x > x || (y[q].x == x && f + q < g));
+          least += in && y[q].x - y[q].y > hi;
+          most += in && y[q].x + y[q].y >= lo;  // itself among them
         }
       }
       if (least < p.topk_groups && most > p.topk_groups && x > -INFINITY) doubt = true;
@@ -421,7 +429,7 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
       doubt = false;
       if ((doubts >> (tok * LPT)) & 0xff) {
         double c = -INFINITY;
-        if (sub < p.groups && gs[sub] > -INFINITY) {
+        if (sub < p.groups && gs[sub].x > -INFINITY) {
           float a = -INFINITY, b = -INFINITY;
           int ia = -1, ib = -1, count = 0;
           scan(sub, [&](float x, int i) {
@@ -430,7 +438,7 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
             else if (x > b)
               b = x, ib = i;
           });
-          const float least = (p.group_top == 1 ? a : b) - 0x1p-20f * M;  // twice the errors of two c
+          const float last = p.group_top == 1 ? a : b, least = last - 2.f * c_error(last);
           scan(sub, [&](float x, int) { count += x >= least; });
           doubt = p.bias && count > 2;
           auto exact = [&](int i) {
@@ -596,11 +604,11 @@ __global__ __launch_bounds__(WAVES * MOELB_WAVE) void route_kernel(RouteArgs p, 
 
 template <int NV, int KL>
 int launch_route(RouteArgs p, hipStream_t s) {
-  // LDS of a wave: rows, group scores and kept groups; the 64-bit form takes E +
+  // LDS of a wave: rows, group scores with their errors, and kept groups; the 64-bit form takes E +
   // groups doubles of it
   int floats = 0;
   if (p.groups > 1) {
-    const int fast = TPW * (p.stride + 2 * p.groups), slow = 2 * (p.E + p.groups);
+    const int fast = TPW * (p.stride + 3 * p.groups), slow = 2 * (p.E + p.groups);
     floats = ((fast > slow ? fast : slow) + 3) / 4 * 4;
   }
   // few tokens: a wave a workgroup, so that they spread over the compute units

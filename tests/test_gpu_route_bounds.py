@@ -1,0 +1,84 @@
+"""GPU: the routing rule where its fp32 form has to know how far its own values can be off.
+
+Picks are equal to those of 64-bit arithmetic, on many tokens at once: the reference
+here is the one of oracle/scored_router.py, vectorised.
+"""
+import math
+
+import pytest
+import torch
+
+from oracle import scored_router as R
+from tests.gpu_layer import log
+
+pytestmark = pytest.mark.gpu
+
+
+def code(score):
+    from routed_expert_ffn_gate_amd import moelb as M
+    return {"softmax": M.MOELB_SCORE_SOFTMAX, "sigmoid": M.MOELB_SCORE_SIGMOID}[score]
+
+
+def picks(z, k, score, bias=None, groups=1, topk_groups=1, group_top=1):
+    """idx [T, k] of moelb_route in float64."""
+    T, E = z.shape
+    low = torch.full((T, E), -math.inf, dtype=torch.float64, device=z.device)
+    s, on = R.scores(z, score)
+    c = s if bias is None else s + bias.double()
+    c = torch.where(on & (c > -math.inf), c.clamp(max=R.F32_MAX), low)
+    key = c if bias is not None else torch.where(on, z.double().clamp(max=R.F32_MAX), low)
+    if groups > 1:
+        best = c.view(T, groups, -1).topk(group_top, dim=2).values.sum(2)
+        kept = torch.sort(best, dim=1, descending=True, stable=True).indices[:, :topk_groups]
+        may = torch.zeros((T, groups), dtype=torch.bool, device=z.device).scatter_(1, kept, True)
+        key = torch.where(may.repeat_interleave(E // groups, dim=1), key, low)
+    top = torch.sort(key, dim=1, descending=True, stable=True)
+    return torch.where(top.values > -math.inf, top.indices, -1)[:, :k].to(torch.int32)
+
+
+def check_picks(z, k, score, **kw):
+    from routed_expert_ffn_gate_amd import moelb as M
+    idx = torch.full((z.shape[0], k), -7, dtype=torch.int32, device="cuda")
+    wts = torch.empty((z.shape[0], k), device="cuda")
+    M.moelb_route(z, idx, wts, score=code(score), **kw)
+    torch.cuda.synchronize()
+    wrong = (idx != picks(z, k, score, **kw)).any(1)
+    log(f"    {int(wrong.sum())} of {z.shape[0]} tokens have other picks")
+    assert not wrong.any()
+
+
+def normal(*shape, seed=1):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def test_the_reference_is_the_oracles():
+    """On the CPU's terms of a few tokens with ties, masks and groups."""
+    z = torch.round(normal(60, 24, seed=3) * 2) / 2
+    z[3], z[4, 5:], z[5, 2] = -math.inf, math.nan, math.inf
+    bias = 0.25 * torch.round(normal(24, seed=4) * 2)
+    bias[7] = -math.inf
+    for score in ("softmax", "sigmoid"):
+        for b in (None, bias):
+            for g, tg, gt in ((1, 1, 1), (6, 2, 1), (6, 4, 2)):
+                kw = dict(bias=b, groups=g, topk_groups=tg, group_top=gt)
+                assert torch.equal(picks(z, 6, score, **kw).cpu(), R.route(z, 6, score, **kw)[0])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("live", [1, 2])
+@pytest.mark.parametrize("off", [1e3, 1e4, 1e5, 1e6])
+@pytest.mark.parametrize("groups,size,topk_groups,k", [(8, 2, 4, 2), (8, 4, 4, 3), (8, 32, 4, 8), (5, 5, 2, 2),
+                                                       (16, 16, 3, 4)])
+def test_groups_of_experts_that_a_finite_bias_switches_off(moelb, score, live, off, groups, size, topk_groups, k):
+    """All but one or two experts of a group lie at -off: the sum of a group's best two is rounded by the lower one's
+    size, which the token's largest value says nothing of."""
+    T = 1 << 16
+    z = normal(T, groups * size, seed=groups + size)
+    bias = 0.05 * normal(groups * size, seed=2)
+    bias.view(groups, size)[:, min(live, size):] = -off
+    log(f"[groups, bias of {-off:g} on all but {live}] {score} {groups} x {size}")
+    for group_top in (1, 2):
+        check_picks(z, k, score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)
+    # experts of one group differ by what the bias leaves of their scores
+    bias = torch.where(bias == -off, bias * (1 + 1e-6 * normal(groups * size, seed=5)), bias)
+    check_picks(z, k, score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=2)

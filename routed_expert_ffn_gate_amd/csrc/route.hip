@@ -390,12 +390,12 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
         a = a > -INFINITY ? score(a) : -INFINITY;
         b = b > -INFINITY ? score(b) : -INFINITY;
       }
-      // c: the bounds below, the bias's rounding by the c itself (a group's best two
+      // c: the bounds above, the bias's rounding by the c itself (a group's best two
       // may lie far below the token's); the sum, and the two ends of the comparison,
-      // round by as much again
-      const float err = p.bias ? c_error(a) + (p.group_top == 1 ? 0.f : c_error(b))
-                               : (p.sigmoid ? 0x1p-20f : 0x1p-19f) * M;
-      gs[g] = make_float2(p.group_top == 1 ? a : a + b, err);
+      // round by as much again.  Halves: two c of the lowest float stay above -inf
+      const float err = p.bias ? 0.5f * c_error(a) + (p.group_top == 1 ? 0.f : 0.5f * c_error(b))
+                               : (p.sigmoid ? 0x1p-21f : 0x1p-20f) * M;
+      gs[g] = make_float2(0.5f * a + (p.group_top == 1 ? 0.f : 0.5f * b), err);
     }
     wave_fence();
     // a group's place among the others; beyond doubt if it is the same with the

@@ -82,3 +82,22 @@ def test_groups_of_experts_that_a_finite_bias_switches_off(moelb, score, live, o
     # experts of one group differ by what the bias leaves of their scores
     bias = torch.where(bias == -off, bias * (1 + 1e-6 * normal(groups * size, seed=5)), bias)
     check_picks(z, k, score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("lowest", [torch.finfo(torch.float32).min, -2e38, -1.8e38, -1e30])
+def test_groups_at_the_lowest_bias(moelb, score, lowest):
+    """The sum of two c of the type's lowest value is below it, and above that of a group without two experts."""
+    groups, size, T = 8, 4, 3000
+    z = normal(T, groups * size, seed=9)
+    zg = z.view(T, groups, size)
+    zg[:, 0] = -math.inf                          # no expert at all: never kept before one that has two
+    zg[1::3, 2, :3] = -math.inf                   # one expert
+    bias = 0.1 * normal(groups * size, seed=10)
+    b = bias.view(groups, size)
+    b[1], b[4, 1:], b[6, 1:] = lowest, lowest, lowest  # all of a group, all but one of two groups
+    b[3] = lowest * torch.tensor([1.0, 0.99, 0.98, 0.97], device="cuda")
+    log(f"[groups at {lowest:g}] {score}")
+    for topk_groups in range(2, groups + 1):
+        for group_top in (1, 2):
+            check_picks(z, 8, score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)

@@ -330,6 +330,15 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
   const uint32_t near = p.bias ? (p.sigmoid ? 9u : 19u) : 0u;
   // one c with a bias, and room for one more rounding of it and of a sum with it
   auto c_error = [&](float c) { return (p.sigmoid ? 0x1p-22f : 14 * 0x1p-24f) + fabsf(c) * 0x1p-22f; };
+  // one s without a bias, of logit x: relative to it, since scores may be of any size.
+  // In 2^-24: 2.5 |y| of the exponential's argument y (its rounding, the product with
+  // log2 e and that constant's), of a softmax's sum 2.5 times the scores' entropy, at
+  // most 5.6, and 8 additions, and a few units of the exponential and the quotient.
+  // A sigmoid of x > 0 has no more than one of 0.  2^-120: results under the normals
+  auto s_error = [&](float x, float s) {
+    const float y = fminf(p.sigmoid ? fmaxf(-x, 0.f) : m - x, 128.f);
+    return s > -INFINITY ? fmaf(s * 0x1p-23f, fmaf(1.5f, y, 20.f), 0x1p-120f) : 0.f;
+  };
   // a window too far from 0 for its sums (the bound is 2^-24 |top| of error, far
   // under a tenth of the window)
   bool redo = fabsf(top) >= (p.bias ? 1e30f : 1e7f);
@@ -386,16 +395,19 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
         b = med3(a, b, x);
         a = fmaxf(a, x);
       });
-      if (!p.bias) {
-        a = a > -INFINITY ? score(a) : -INFINITY;
-        b = b > -INFINITY ? score(b) : -INFINITY;
-      }
       // c: the bounds above, the bias's rounding by the c itself (a group's best two
       // may lie far below the token's); the sum, and the two ends of the comparison,
       // round by as much again.  Halves: two c of the lowest float stay above -inf
-      const float err = p.bias ? 0.5f * c_error(a) + (p.group_top == 1 ? 0.f : 0.5f * c_error(b))
-                               : (p.sigmoid ? 0x1p-21f : 0x1p-20f) * M;
-      gs[g] = make_float2(0.5f * a + (p.group_top == 1 ? 0.f : 0.5f * b), err);
+      float ea = 0.f, eb = 0.f;
+      if (p.bias) {
+        ea = c_error(a), eb = c_error(b);
+      } else {
+        const float za = a, zb = b;
+        a = a > -INFINITY ? score(a) : -INFINITY;
+        b = b > -INFINITY ? score(b) : -INFINITY;
+        ea = s_error(za, a), eb = s_error(zb, b);
+      }
+      gs[g] = p.group_top == 1 ? make_float2(0.5f * a, 0.5f * ea) : make_float2(0.5f * a + 0.5f * b, 0.5f * ea + 0.5f * eb);
     }
     wave_fence();
     // a group's place among the others; beyond doubt if it is the same with the

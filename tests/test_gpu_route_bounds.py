@@ -101,3 +101,61 @@ def test_groups_at_the_lowest_bias(moelb, score, lowest):
     for topk_groups in range(2, groups + 1):
         for group_top in (1, 2):
             check_picks(z, 8, score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1.0, 1e-5, 1e-12, 1e-26, 1e-37, 1e-40, 1e-60])
+@pytest.mark.parametrize("groups,size,group_top", [(8, 20, 1), (8, 20, 2), (5, 3, 2), (16, 16, 2)])
+def test_small_scores_of_groups_next_to_each_other(moelb, score, scale, groups, size, group_top):
+    """No bias: the scores of all groups but the first differ by about 1e-6 of themselves, whatever their size."""
+    T, gen = 4001, torch.Generator(device="cuda").manual_seed(groups * size)
+    u = lambda *s: torch.rand(s, generator=gen, device="cuda", dtype=torch.float64)  # noqa: E731
+    c = 0.05 + 0.1 * u(T, groups, size)
+    first = torch.full((T, groups), 0.6, dtype=torch.float64, device="cuda") if group_top == 1 else 0.56 + 0.2 * u(T, groups)
+    place = u(T, groups, size).argsort(-1)
+    c.scatter_(2, place[..., :1], first[..., None])
+    if group_top == 2:
+        c.scatter_(2, place[..., 1:2], (1.1 - first)[..., None])
+    c = c * scale * (1 + 1e-6 * (u(T, groups, 1) - 0.5))
+    c[:, 0] = 0.5  # and one group far above
+    z = (torch.log(c / (1 - c)) if score == "sigmoid" else torch.log(c)).view(T, -1).float()
+    log(f"[groups of scores about {scale:g}] {score} {groups} x {size} top {group_top}")
+    for topk_groups in (2, groups // 2 + 1):
+        check_picks(z, min(4, size), score, groups=groups, topk_groups=topk_groups, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("std,add", [(1.0, 0.0), (8.0, 0.0), (1.0, 1000.0), (30.0, -50.0), (1e4, 0.0)])
+@pytest.mark.parametrize("E,groups,topk_groups,group_top", [(160, 8, 3, 1), (160, 8, 3, 2), (256, 16, 4, 2), (60, 6, 2, 2)])
+def test_peaked_and_shifted_logits_of_groups(moelb, score, std, add, E, groups, topk_groups, group_top):
+    z = std * normal(20011, E, seed=E + groups) + add
+    check_picks(z, 6, score, groups=groups, topk_groups=topk_groups, group_top=group_top)
+
+
+def test_groups_cost_the_same_for_peaked_and_shifted_logits(moelb):
+    """What tells groups apart is the size of their scores: neither peaked logits nor a constant added to all of them
+    (which changes no score) sends tokens to the 64-bit form.  (Errors by the largest logit cost 3 and 4 times as
+    much.)"""
+    from routed_expert_ffn_gate_amd import moelb as M
+    base = normal(32768, 160, seed=7)
+    idx = torch.empty((32768, 6), dtype=torch.int32, device="cuda")
+    wts = torch.empty((32768, 6), device="cuda")
+    took = []
+    for z in (base, 8 * base, base + 1000):
+        call = lambda: M.moelb_route(z, idx, wts, groups=8, topk_groups=3, group_top=1)  # noqa: E731, B023
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                call()
+        us = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            us.append(a.elapsed_time(b) * 50)
+        took.append(min(us))
+    log(f"    us a call: {took}")
+    assert max(took) <= 2 * took[0]

@@ -574,14 +574,15 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
 #pragma unroll
   for (int h = 0; h < H; ++h) total += at[h] < p.k ? s[h] : 0.f;
   total = token_all(total, add);
-  const float f = p.renorm ? p.scale / (total + 1e-20f) : p.scale;
+  // the scale last: over a sum of 0 it may be past the largest float
+  const float share = p.renorm ? 1.0f / (total + 1e-20f) : 1.0f;
   float ck = 0.f, cn = 0.f;  // c of entries k - 1 and k
   bool more = false;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     if (at[h] < p.k && active && !skip) {
       p.idx[t * p.k + at[h]] = id[h];
-      if (p.wts) p.wts[t * p.k + at[h]] = s[h] * f;
+      if (p.wts) p.wts[t * p.k + at[h]] = s[h] * share * p.scale;
     }
     ck += at[h] == p.k - 1 && id[h] >= 0 ? cc[h] : 0.f;
     cn += at[h] == p.k && id[h] >= 0 ? cc[h] : 0.f;

@@ -159,3 +159,24 @@ def test_groups_cost_the_same_for_peaked_and_shifted_logits(moelb):
         took.append(min(us))
     log(f"    us a call: {took}")
     assert max(took) <= 2 * took[0]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1.0, 2.5, 1e19, -1e30, 3e38])
+def test_renormalised_weights_at_any_scale(moelb, score, scale):
+    """A weight is scale times a share in [0, 1] of the picks' scores: rows without a score have weight 0 at any finite
+    scale.  Off by (2 max|x| + E + 32) f of itself, as in test_gpu_route.py, and where scores lie under fp32's normals
+    by their spacing's share of the sum, at most 2^-120 / 1e-20."""
+    from routed_expert_ffn_gate_amd import moelb as M
+    T, E, k = 90, 24, 4
+    z = normal(T, E, seed=12)
+    z[3], z[4], z[5, 2:] = -math.inf, math.nan, -math.inf
+    z[6], z[7], z[8], z[9, :20] = -200.0, -60.0, -46.0, -1e30
+    idx, wts = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    M.moelb_route(z, idx, wts, score=code(score), renorm=True, scale=scale)
+    torch.cuda.synchronize()
+    want_idx, want, _ = R.route(z, k, score, renorm=True, scale=scale)
+    assert torch.equal(idx.cpu(), want_idx) and torch.isfinite(wts).all()
+    assert (wts[3:5] == 0).all() and (wts[5, 2:] == 0).all()
+    allow = (2 * 104 + E + 32) * 2.0 ** -24 * want.abs() + abs(scale) * 2.0 ** -120 / 1e-20 + 2.0 ** -120
+    assert ((wts.cpu().double() - want).abs() <= allow).all()

@@ -323,6 +323,8 @@ __global__ __launch_bounds__(MOELB_WAVE * ROW_WAVES) void gate_softmax_backward_
 //   sigmoid: dz = ds s (1 - s) at the picks; softmax: dz_e = s_e (ds_e - C), C =
 //   sum_j s_j ds_j.  renorm: C = scale A 1e-20 / S^2, without the cancellation
 //   of two sums that are equal but for the 1e-20.
+// Computed from shares s / S, which a pick has in [0, 1], with the scale as the last
+// factor: q / S alone may be past the largest float where the picks' scores vanish.
 // 16 lanes take a token, lane s the experts s NC .. and pick s; sums go over the 16
 // lanes by row rotations.  T = 32768, E = 128: 14 us (25 MB), where a wave a token
 // with its chain of dependent loads took 22.
@@ -392,15 +394,11 @@ __global__ __launch_bounds__(DZ_THREADS) void route_dz_kernel(GateArgs<T> p, Rou
       sj = live ? expf(zj - m) * inv : 0.f;
       cj = 0.f;
     }
-    const float A = row_reduce(q * sj, add);
-    float ds = u.scale * q, C = u.scale * A;
-    if (u.renorm) {
-      const float S = row_reduce(sj, add) + 1e-20f;
-      ds = u.scale * (q - A / S) / S;
-      C = u.scale * (A / S) * (1e-20f / S);
-    }
-    if (id < 0) ds = 0.f;
-    const float mine = u.sigmoid ? ds * sj * cj : ds;
+    // dz = scale s r (hit - D), r = 1 / S (renorm) or 1
+    const float r = u.renorm ? 1.0f / (row_reduce(sj, add) + 1e-20f) : 1.0f;
+    const float share = sj * r, A = row_reduce(q * share, add);
+    const float hit = id < 0 ? 0.f : u.renorm ? q - A : q, D = u.renorm ? A * 1e-20f : A;
+    const float mine = u.sigmoid ? hit * share * cj : hit;
     float dz[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) dz[i] = 0.f;
@@ -412,7 +410,8 @@ __global__ __launch_bounds__(DZ_THREADS) void route_dz_kernel(GateArgs<T> p, Rou
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (!u.sigmoid) dz[i] = z[i] * (dz[i] - C);
+      if (!u.sigmoid) dz[i] = z[i] * r * (dz[i] - D);
+      dz[i] *= u.scale;
       db[i] += dz[i];
     }
     // rounded to the storage type: the matrix products below read it as an operand,

@@ -10,6 +10,7 @@ import torch
 
 from oracle import scored_router as R
 from tests.gpu_layer import log
+from tests.test_gpu_route import check_gradient
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +181,22 @@ def test_renormalised_weights_at_any_scale(moelb, score, scale):
     assert (wts[3:5] == 0).all() and (wts[5, 2:] == 0).all()
     allow = (2 * 104 + E + 32) * 2.0 ** -24 * want.abs() + abs(scale) * 2.0 ** -120 / 1e-20 + 2.0 ** -120
     assert ((wts.cpu().double() - want).abs() <= allow).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["scores", "renorm"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.5, 1e19, -1e30])
+def test_gradient_at_any_scale(moelb, dtype, score, renorm, scale):
+    """Masked picks have gradient 0, and picks of scores far below 1e-20 what the formula gives, at any scale that the
+    results can hold."""
+    T, E, k = 60, 24, 4
+    z = normal(T, E, seed=13)
+    idx = z.topk(k, dim=1).indices.to(torch.int32)
+    idx[11, 2:] = -1
+    z[3], z[4], z[5, 12:] = -math.inf, math.nan, -math.inf
+    z[6], z[7], z[8], z[9, :20] = -200.0, -60.0, -46.0, -1e30
+    z[10] = normal(E, seed=14) - 50.0
+    z[10, 0] = 0.0  # picks of about e^-50 beside an expert that is not picked
+    idx[10] = torch.tensor([5, 9, 2, 17], dtype=torch.int32)
+    check_gradient(T, 64, E, k, dtype, score, renorm, idx=idx, z=z, scale=scale)

@@ -589,7 +589,8 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
     more = more || (at[h] == p.k && id[h] >= 0);
   }
   if (p.gap) {
-    const float g = token_all(ck, add) - token_all(cn, add);
+    // entries ranked in 64 bits may stand the other way round in fp32
+    const float g = fmaxf(token_all(ck, add) - token_all(cn, add), 0.f);
     const float some = token_all(more ? 1.f : 0.f, add);
     if (sub == 0 && active && !skip) p.gap[t] = some > 0.f ? g : INFINITY;
   }

@@ -200,3 +200,20 @@ def test_gradient_at_any_scale(moelb, dtype, score, renorm, scale):
     z[10, 0] = 0.0  # picks of about e^-50 beside an expert that is not picked
     idx[10] = torch.tensor([5, 9, 2, 17], dtype=torch.int32)
     check_gradient(T, 64, E, k, dtype, score, renorm, idx=idx, z=z, scale=scale)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gap_is_not_negative(moelb, score):
+    """Scores of different sizes whose biases make them nearly equal: the larger c in 64 bits may be the smaller in
+    fp32."""
+    from routed_expert_ffn_gate_amd import moelb as M
+    T, E, k = 20000, 6, 5
+    p = torch.tensor([0.05, 0.1, 0.15, 0.2, 0.22, 0.28], dtype=torch.float64, device="cuda")
+    z = (torch.log(p / (1 - p)) if score == "sigmoid" else torch.log(p)) * (1 + 2.0 ** -23 * normal(T, E, seed=16).double())
+    bias = (0.9 - p).float()
+    idx, gap = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T,), device="cuda")
+    M.moelb_route(z.float(), idx, None, gap, score=code(score), bias=bias)
+    torch.cuda.synchronize()
+    assert torch.equal(idx, picks(z.float(), k, score, bias=bias))
+    log(f"    {score}: {int((gap < 0).sum())} negative, smallest {float(gap.min()):.3g}")
+    assert (gap >= 0).all()

@@ -649,7 +649,9 @@ enum moelb_score {
  * only those.  A group's score counts a masked expert as -inf.  Logits of +inf are
  * taken as the largest float, and so is a c above it.
  * The picks do not depend on fp32's rounding of the scores: those that are near each
- * other in fp32 are compared in 64 bits.  wts and gap are fp32.
+ * other in fp32, and groups whose scores are, are compared in 64 bits.  wts and gap are
+ * fp32: a weight is off by about |z| 2^-23 of itself (softmax: |z - the token's largest|)
+ * beside a few roundings, from the exponent of its exponential; gap is not negative.
  *  z    [T,E] fp32, bias [E] fp32 or NULL
  *  idx  [T,k] int32 out; wts [T,k] fp32 out or NULL; gap [T] fp32 out or NULL
  * Requires T >= 0, 1 <= k <= min(E, 16), E <= 256, groups >= 1 dividing E,

@@ -11,13 +11,15 @@
 //    merged by DPP.  It also finds where fp32 cannot tell.
 //  * Two of the first k + 1 keys nearer than their error bounds: the listed experts
 //    are ranked in 64 bits by the token's eight lanes.
-//  * Sigmoid groups near the border of the kept ones: their best two in 64 bits.
+//  * Groups nearer to the border of the kept ones than the errors of their own best
+//    two: a sigmoid's by those two in 64 bits.
 //  * What that does not decide (ties beyond the list or the two, a softmax's groups,
 //    values below the keys' window): route_token, a whole wave a token, four
 //    experts a lane, in 64 bits.
 // So the picks are those of 64-bit arithmetic.  Bound by vector instructions (60-70 %
 // active): T = 32768, 256 experts, sigmoid, bias, 4 of 8 groups, top 8 in 21 us (7 for
-// the logits' bytes); 128 experts, softmax 12; 512 tokens 4.9.
+// the logits' bytes); 160 experts, softmax, 3 of 8 groups, top 6 20, of peaked logits
+// 13; 128 experts, softmax 11; 512 tokens 4.4.
 #include <float.h>
 #include <math.h>
 
@@ -324,9 +326,11 @@ __device__ __forceinline__ uint64_t route_fast(const RouteArgs& p, int t0, float
   const Keys keys(top, W);
   // Errors: s of a sigmoid under 2^-22 (0.19 of it from the exponential, 0.75 from
   // the sum and the reciprocal), of a softmax under 14 x 2^-24 (8 additions, the
-  // exponentials, the quotient); c has the bias's rounding beside it (2^-24 M).  Two
-  // keys are in order if they are further apart than twice that, 5 or 15 units, and
-  // 4 units of their own rounding.  Logits are exact: unequal keys are in order.
+  // exponentials, the quotient); c has the sum's rounding beside it, under 1.5 x 2^-23
+  // M in the window, where |c| <= 3 M.  In units that is 3.5 or 8.5 a key.  Two keys
+  // are in order if they are further apart than both, 7 or 17 units, and 2 of their
+  // own (half a unit each from the product and sum, under one from dropping the
+  // fraction).  Logits are exact: unequal keys are in order.
   const uint32_t near = p.bias ? (p.sigmoid ? 9u : 19u) : 0u;
   // one c with a bias, and room for one more rounding of it and of a sum with it
   auto c_error = [&](float c) { return (p.sigmoid ? 0x1p-22f : 14 * 0x1p-24f) + fabsf(c) * 0x1p-22f; };
